@@ -245,6 +245,145 @@ moe_status moe_route_permute(const void* logits, int logits_dtype, const void* x
                              void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * moe_route_balance -- the router of a training step: moe_route_topk's
+ * routing with per-expert counts, the load-balance loss and the router z-loss.
+ *
+ * logits      [T, E] in logits_dtype (MOE_F32 or MOE_BF16), device.
+ * token_mask  optional device bytes [T]: 0 marks a token that does not count
+ *             (padding).  Such a token is routed like any other, but enters
+ *             neither counts nor losses.  NULL: every token counts.
+ * topk_idx    [T, k] int32 out, topk_prob [T, k] fp32 out, as moe_route_topk
+ *             (largest logits first, equal logits -> lower expert id;
+ *             softmax of the k selected).
+ * counts      [E] int32 out: slots of the counting tokens that went to e.
+ * losses      [2] fp32 out, with p = softmax over all E experts and n the
+ *             number of counting tokens:
+ *               losses[0] = E / (k n^2) sum_e counts[e] sum_t p[t, e]
+ *               losses[1] = 1/n sum_t (log sum_e exp logits[t, e])^2
+ *             0 when nothing counts.
+ * A token without a logit above -inf gets expert ids 0 .. k-1 with
+ * probability 0 and does not count.  A NaN logit is selected first; NaN and
+ * +inf make the token's probabilities and both losses NaN.  Ids are always in
+ * range.
+ * 1 <= k <= min(E, 16), E <= 256.  workspace: at least
+ * moe_route_balance_workspace(T, E) bytes (device, caller-owned; nothing in
+ * it is read before it is written, nothing is kept from call to call).
+ * ------------------------------------------------------------------------ */
+size_t moe_route_balance_workspace(int64_t T, int E);
+moe_status moe_route_balance(const void* logits, int logits_dtype, const uint8_t* token_mask, int64_t T, int E,
+                             int k, int32_t* topk_idx, float* topk_prob, int32_t* counts, float* losses,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_route_balance_bwd -- the gradient of moe_route_balance with respect to
+ * the logits.
+ *
+ * logits, token_mask, topk_idx, topk_prob, counts: the forward's (every token
+ *             that counts put k slots into counts).
+ * dprob       [T, k] fp32 gradient of topk_prob (moe_grouped_mlp_bwd's dprob),
+ *             or NULL: none.  It reaches a masked token's logits too.
+ * dlosses     [2] fp32 gradient of losses, device, or NULL: none.
+ * dlogits     [T, E] out in logits_dtype:
+ *               g0 p (f - sum_i p_i f_i) + g1 2/n lse p     (counting tokens)
+ *               + w_j (dprob_j - sum_m w_m dprob_m) at expert topk_idx[., j]
+ *             with f_e = E counts[e] / (k n^2), w = topk_prob.  The counts are
+ *             constants of the balance loss.  Zero (but for dprob's part) for
+ *             a token that does not count.  Computed in fp32, rounded once.
+ * An id outside [0, E) in topk_idx receives nothing.
+ * ------------------------------------------------------------------------ */
+moe_status moe_route_balance_bwd(const void* logits, int logits_dtype, const uint8_t* token_mask, int64_t T, int E,
+                                 int k, const int32_t* topk_idx, const float* topk_prob, const int32_t* counts,
+                                 const float* dprob, const float* dlosses, void* dlogits, void* stream);
+
+/* ------------------------------------------------------------------------
+ * fp8_block_quantize -- E4M3 with one fp32 scale per 128 values.
+ *
+ * x        [rows, cols] in x_dtype (MOE_F32 or MOE_BF16), device.
+ * Per block: amax = max |v|; d = amax / 448 and f = 448 / amax as fp32
+ *          divisions rounded to nearest, d not below and 1 / f not above the
+ *          smallest normal number's range (d >= 2^-126, f <= 2^126); amax = 0
+ *          gives d = f = 1.  code = E4M3FN(fp32(v f)), nearest even; a code
+ *          stands for decode(code) * d.  A block with an infinite or NaN value
+ *          decodes to infinities and NaN only.
+ * axis 0:  blocks of 128 consecutive values along cols (cols % 128 == 0).
+ *          q [rows, cols] bytes; scales fp32 [cols/128, rows] -- block-major,
+ *          so that the scales of one block of K are consecutive.
+ *          group_offsets and num_groups are not used.
+ * axis 1:  blocks of 128 consecutive rows of one segment (cols % 16 == 0),
+ *          the segments given by the device array group_offsets
+ *          [num_groups+1] (as mxfp8_quantize; NULL with num_groups == 1: all
+ *          rows).  Transposed: segment g occupies columns [P_g, P_g +
+ *          ceil(M_g/128)*128) of q [cols, rows_pad] and rows P_g/128 .. of
+ *          scales fp32 [rows_pad/128, cols], P_g the prefix sum of the padded
+ *          segment sizes and rows_pad = ceil(rows/128)*128 + 128*num_groups.
+ *          Padding, also behind the last segment, is code 0x00 and (where a
+ *          whole block is padding) scale 1.  Offsets outside [0, rows] or
+ *          decreasing are clamped on the device.
+ * x and q 16-byte aligned, rows < 2^31, 1 <= num_groups <= 256.
+ * ------------------------------------------------------------------------ */
+moe_status fp8_block_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int axis,
+                              const int32_t* group_offsets, int num_groups, uint8_t* q, float* scales,
+                              void* stream);
+
+/* ------------------------------------------------------------------------
+ * fp8_block_quantize_weights -- E4M3 of a table of E bf16 weight matrices with
+ * one fp32 scale per 128 x 128 block (rule as fp8_block_quantize), one launch.
+ *
+ * w           HOST array of E device pointers, each a bf16 matrix [rows, cols].
+ * transposed  0: q [E, rows, cols], scales fp32 [E, ceil(rows/128), cols/128]
+ *             (cols % 128 == 0, rows % 16 == 0) -- the forward's B operand;
+ *             1: q [E, cols, rows], scales [E, ceil(cols/128), rows/128]
+ *             (rows % 128 == 0, cols % 16 == 0) -- dgrad's.  Both orientations
+ *             hold the same codes.
+ * skip        optional device int32 [E]: matrices with skip[e] == 0 are left
+ *             untouched.
+ * w[e] and q 16-byte aligned; 1 <= E <= 256.
+ * ------------------------------------------------------------------------ */
+moe_status fp8_block_quantize_weights(const void* const* w, int E, int64_t rows, int64_t cols, int transposed,
+                                      const int32_t* skip, uint8_t* q, float* scales, void* stream);
+
+/* ------------------------------------------------------------------------
+ * fp8_block_grouped_gemm -- the experts' products on operands with one scale
+ * per block of 128, all experts in one submission.
+ *
+ *   out[r, n] = sum_b a_scales[b, r] w_scales[e, n/128, b]
+ *               sum_{k in block b} a[r, k] w[e, n, k],  offsets[e] <= r < offsets[e+1]
+ *
+ * a        [R, K] E4M3 codes, a_scales [K/128, R] (fp8_block_quantize, axis 0).
+ * w        [E, N, K] codes, w_scales [E, ceil(N/128), K/128]
+ *          (fp8_block_quantize_weights; transposed for dgrad).
+ * offsets  [E+1] int32, device: each expert's rows, an exclusive prefix sum
+ *          (moe_permute's).  Clamped into [0, R] and made non-decreasing on
+ *          the device.  Rows outside [offsets[0], offsets[E]) of out are left
+ *          as they were.
+ * out      [R, N] in out_dtype (MOE_BF16 or MOE_F32), fp32 sums rounded once.
+ * K % 128 == 0, N % 16 == 0 (else MOE_ERR_UNSUPPORTED); pointers of codes and
+ * out 16-byte aligned; 256 K, 256 N * 4 and R K / 32 below 2^32.
+ * ------------------------------------------------------------------------ */
+moe_status fp8_block_grouped_gemm(const uint8_t* a, const float* a_scales, const uint8_t* w, const float* w_scales,
+                                  const int32_t* offsets, int64_t R, int64_t N, int64_t K, int E, int out_dtype,
+                                  void* out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * fp8_block_grouped_wgrad -- the experts' weight gradients on token-axis
+ * operands: dw[e] = sum over the 128-token blocks b of expert e of
+ *   dyt_scales[b, n] xt_scales[b, k] sum_{t in b} dyt[n, t] xt[k, t].
+ *
+ * dyt      [N, rows_pad] codes, dyt_scales [rows_pad/128, N]; xt [K, rows_pad],
+ *          xt_scales [rows_pad/128, K]: fp8_block_quantize, axis 1, of both
+ *          with the same group_offsets.
+ * offsets  [E+1] int32, device: the group_offsets of the quantization.
+ * dw       [E, N, K] in out_dtype (MOE_BF16 or MOE_F32), overwritten; experts
+ *          without tokens get zeros.
+ * N % 16 == 0, K % 16 == 0, rows_pad % 128 == 0 (else MOE_ERR_UNSUPPORTED);
+ * pointers 16-byte aligned; 256 rows_pad and 256 K * 4 and rows_pad N / 32 and
+ * rows_pad K / 32 below 2^32.
+ * ------------------------------------------------------------------------ */
+moe_status fp8_block_grouped_wgrad(const uint8_t* dyt, const float* dyt_scales, const uint8_t* xt,
+                                   const float* xt_scales, const int32_t* offsets, int64_t rows_pad, int64_t N,
+                                   int64_t K, int E, int out_dtype, void* dw, void* stream);
+
+/* ------------------------------------------------------------------------
  * moe_grouped_mlp_fwd -- the whole expert MLP forward.
  *
  * Source: page "BioNeMo Uses Grouped Kernels and MXFP8", Grouping fragmented

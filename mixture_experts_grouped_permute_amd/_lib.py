@@ -30,6 +30,8 @@ EXPORTS = (
     "moe_route_topk", "moe_route_permute", "moe_grouped_mlp_fwd_loop", "fp8_tensor_quantize_workspace",
     "fp8_tensor_quantize", "mxfp8_quantize_weights", "moe_permute_noalloc", "moe_tile_stats_bytes",
     "moe_set_tile_stats", "moe_probe_workgroups", "moe_mfma_probe", "moe_load_probe_bytes", "moe_load_probe",
+    "moe_route_balance_workspace", "moe_route_balance", "moe_route_balance_bwd", "fp8_block_quantize",
+    "fp8_block_quantize_weights", "fp8_block_grouped_gemm", "fp8_block_grouped_wgrad",
 )
 NOALLOC_SCRATCH_BYTES = 4 << 20    # MOE_NOALLOC_SCRATCH_BYTES
 
@@ -149,6 +151,25 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.moe_route_permute.argtypes = [_vp, ctypes.c_int, _vp, ctypes.c_int, _i64, _i64, ctypes.c_int, ctypes.c_int,
                                       ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                       ctypes.c_size_t, _vp]
+    lib.moe_route_balance_workspace.restype = ctypes.c_size_t
+    lib.moe_route_balance_workspace.argtypes = [_i64, ctypes.c_int]
+    lib.moe_route_balance.restype = ctypes.c_int
+    lib.moe_route_balance.argtypes = [_vp, ctypes.c_int, _vp, _i64, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp,
+                                      _vp, ctypes.c_size_t, _vp]
+    lib.moe_route_balance_bwd.restype = ctypes.c_int
+    lib.moe_route_balance_bwd.argtypes = [_vp, ctypes.c_int, _vp, _i64, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp,
+                                          _vp, _vp, _vp, _vp]
+    lib.fp8_block_quantize.restype = ctypes.c_int
+    lib.fp8_block_quantize.argtypes = [_vp, ctypes.c_int, _i64, _i64, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp, _vp]
+    lib.fp8_block_quantize_weights.restype = ctypes.c_int
+    lib.fp8_block_quantize_weights.argtypes = [ctypes.POINTER(_vp), ctypes.c_int, _i64, _i64, ctypes.c_int, _vp, _vp,
+                                               _vp, _vp]
+    lib.fp8_block_grouped_gemm.restype = ctypes.c_int
+    lib.fp8_block_grouped_gemm.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int,
+                                           _vp, _vp]
+    lib.fp8_block_grouped_wgrad.restype = ctypes.c_int
+    lib.fp8_block_grouped_wgrad.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int,
+                                            _vp, _vp]
     if path is None:
         _lib = lib
     return lib
@@ -412,6 +433,193 @@ def moe_route_permute(logits: torch.Tensor, x: Optional[torch.Tensor], k: int, p
                                ws.data_ptr(), ws.numel(), _stream(dev))
     _check(st, "moe_route_permute")
     out["workspace"] = ws
+    return out
+
+
+def _on(t: torch.Tensor, what: str) -> torch.device:
+    """The GPU that holds t (TypeError otherwise)."""
+    if not t.is_cuda:
+        raise TypeError(f"{what} must be on a GPU, got {t.device}")
+    return t.device
+
+
+def _shape(t: Optional[torch.Tensor], shape, dtype: torch.dtype, device: torch.device, what: str) -> None:
+    """Raise unless t (if given) is a contiguous `dtype` tensor of `shape` on `device`."""
+    if t is None:
+        return
+    _need(t, dtype, device, what)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+
+
+def _mask(token_mask: Optional[torch.Tensor], T: int, device: torch.device) -> None:
+    if token_mask is None:
+        return
+    if token_mask.dtype not in (torch.bool, torch.uint8):
+        raise TypeError(f"token_mask must be bool or uint8, got {token_mask.dtype}")
+    _shape(token_mask, (T,), token_mask.dtype, device, "token_mask")
+
+
+def moe_route_balance(logits: torch.Tensor, k: int, token_mask: Optional[torch.Tensor] = None):
+    """The router of a training step: moe_route_topk's routing of logits [T, E] (bf16 or f32) with
+    per-expert counts, the load-balance loss and the router z-loss.
+    token_mask: optional bool or uint8 [T]; tokens where it is 0 (padding) are routed, but enter
+    neither counts nor losses.
+    Returns (topk_idx int32 [T, k], topk_prob float32 [T, k], counts int32 [E], losses float32 [2]),
+    losses[0] = E / (k n^2) sum_e counts[e] sum_t p[t, e] and losses[1] = mean of lse^2, over the n
+    tokens that count."""
+    lib = load()
+    dev = _on(logits, "logits")
+    T, E = logits.shape
+    _mask(token_mask, T, dev)
+    with torch.cuda.device(dev):
+        idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+        prob = torch.empty((T, k), dtype=torch.float32, device=dev)
+        counts = torch.empty(E, dtype=torch.int32, device=dev)
+        losses = torch.empty(2, dtype=torch.float32, device=dev)
+        # a workspace of the call's own: a captured call keeps it in its graph's memory
+        ws = torch.empty(max(lib.moe_route_balance_workspace(T, E), 256), dtype=torch.uint8, device=dev)
+        _check(lib.moe_route_balance(_ptr(logits), _io(logits), _ptr(token_mask), T, E, k, _ptr(idx), _ptr(prob),
+                                     _ptr(counts), _ptr(losses), ws.data_ptr(), ws.numel(), _stream(dev)),
+               "moe_route_balance")
+    return idx, prob, counts, losses
+
+
+def moe_route_balance_bwd(logits: torch.Tensor, topk_idx: torch.Tensor, topk_prob: torch.Tensor,
+                          counts: torch.Tensor, dprob: Optional[torch.Tensor] = None,
+                          dlosses: Optional[torch.Tensor] = None, token_mask: Optional[torch.Tensor] = None):
+    """Gradient of moe_route_balance with respect to the logits, in their dtype.  topk_idx, topk_prob,
+    counts and token_mask: the forward's; dprob: gradient of topk_prob (float32 [T, k], e.g.
+    moe_grouped_mlp_bwd's dprob); dlosses: gradient of losses (float32 [2])."""
+    lib = load()
+    dev = _on(logits, "logits")
+    T, E = logits.shape
+    if topk_idx.dim() != 2:
+        raise ValueError("topk_idx must be [T, k]")
+    k = topk_idx.shape[1]
+    _shape(topk_idx, (T, k), torch.int32, dev, "topk_idx")
+    _shape(topk_prob, (T, k), torch.float32, dev, "topk_prob")
+    _shape(counts, (E,), torch.int32, dev, "counts")
+    _shape(dprob, (T, k), torch.float32, dev, "dprob")
+    _shape(dlosses, (2,), torch.float32, dev, "dlosses")
+    _mask(token_mask, T, dev)
+    with torch.cuda.device(dev):
+        dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
+        _check(lib.moe_route_balance_bwd(_ptr(logits), _io(logits), _ptr(token_mask), T, E, k, _ptr(topk_idx),
+                                         _ptr(topk_prob), _ptr(counts), _ptr(dprob), _ptr(dlosses), _ptr(dlogits),
+                                         _stream(dev)), "moe_route_balance_bwd")
+    return dlogits
+
+
+def fp8_block_quantize(x: torch.Tensor, axis: int = 0, group_offsets: Optional[torch.Tensor] = None):
+    """E4M3 of x [rows, cols] (bf16 or f32) with one fp32 scale per 128 values; a code stands for
+    decode(code) * scale.
+
+    axis 0: blocks along cols; returns (codes uint8 [rows, cols], scales float32 [cols/128, rows]).
+    axis 1: blocks along the rows of each segment of group_offsets (int32 device [G+1]; None: one
+            segment), transposed; returns (codes [cols, rows_pad], scales [rows_pad/128, cols]),
+            rows_pad = ceil(rows/128)*128 + 128 G, segments padded as documented in moe.h."""
+    lib = load()
+    dev = _on(x, "x")
+    rows, cols = x.shape
+    if axis == 0 and group_offsets is not None:
+        raise ValueError("group_offsets go with axis 1")
+    G = 1
+    if group_offsets is not None:
+        G = group_offsets.numel() - 1
+        _shape(group_offsets, (G + 1,), torch.int32, dev, "group_offsets")
+    with torch.cuda.device(dev):
+        if axis == 0:
+            q = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
+            s = torch.empty((cols // 128, rows), dtype=torch.float32, device=dev)
+        else:
+            rp = (rows + 127) // 128 * 128 + 128 * G
+            q = torch.empty((cols, rp), dtype=torch.uint8, device=dev)      # every byte is written
+            s = torch.empty((rp // 128, cols), dtype=torch.float32, device=dev)
+        _check(lib.fp8_block_quantize(_ptr(x), _io(x), rows, cols, axis, _ptr(group_offsets), G, _ptr(q), _ptr(s),
+                                      _stream(dev)), "fp8_block_quantize")
+    return q, s
+
+
+def fp8_block_quantize_weights(w, transposed: bool = False, skip: Optional[torch.Tensor] = None):
+    """E4M3 of E bf16 matrices [rows, cols] (a stacked tensor or a list) with one fp32 scale per
+    128 x 128 block, in one launch: (codes [E, rows, cols], scales [E, ceil(rows/128), cols/128]), or
+    transposed (codes [E, cols, rows], scales [E, ceil(cols/128), rows/128]).
+    skip: optional int32 device [E]; matrices with skip[e] == 0 are left as zeros."""
+    lib = load()
+    tab, items = _table(w, torch.bfloat16, None, "w")
+    E = len(items)
+    if E == 0:
+        raise ValueError("no matrices")
+    rows, cols = items[0].shape
+    dev = _on(items[0], "w")
+    for t in items:
+        if t.shape != (rows, cols) or t.device != dev:
+            raise ValueError("every matrix must have the same shape and device")
+    _shape(skip, (E,), torch.int32, dev, "skip")
+    n, kd = (cols, rows) if transposed else (rows, cols)
+    make = torch.zeros if skip is not None else torch.empty
+    with torch.cuda.device(dev):
+        q = make((E, n, kd), dtype=torch.uint8, device=dev)
+        s = make((E, (n + 127) // 128, kd // 128), dtype=torch.float32, device=dev)
+        _check(lib.fp8_block_quantize_weights(tab, E, rows, cols, int(transposed), _ptr(skip), _ptr(q), _ptr(s),
+                                              _stream(dev)), "fp8_block_quantize_weights")
+    return q, s
+
+
+def fp8_block_grouped_gemm(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                           offsets: torch.Tensor, out_dtype=torch.bfloat16, out: Optional[torch.Tensor] = None):
+    """The experts' products out[r] = a[r] . w[e]^T of codes with one scale per block of 128, for the rows
+    offsets[e] <= r < offsets[e+1] (int32 device [E+1], e.g. moe_permute's).  a [R, K] and a_scales
+    [K/128, R] from fp8_block_quantize; w [E, N, K] and w_scales [E, ceil(N/128), K/128] from
+    fp8_block_quantize_weights (transposed for dgrad).  out: optional [R, N] tensor to write (its dtype
+    counts); rows outside the offsets are left as they are.  Returns out [R, N]."""
+    lib = load()
+    dev = _on(a, "a")
+    R, K = a.shape
+    E, N, K2 = w.shape
+    if K2 != K:
+        raise ValueError(f"a has {K} columns, w has {K2}")
+    _shape(a, (R, K), torch.uint8, dev, "a")
+    _shape(a_scales, (K // 128, R), torch.float32, dev, "a_scales")
+    _shape(w, (E, N, K), torch.uint8, dev, "w")
+    _shape(w_scales, (E, (N + 127) // 128, K // 128), torch.float32, dev, "w_scales")
+    _shape(offsets, (E + 1,), torch.int32, dev, "offsets")
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty((R, N), dtype=out_dtype, device=dev)
+        else:
+            _shape(out, (R, N), out.dtype, dev, "out")
+        _check(lib.fp8_block_grouped_gemm(_ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), _ptr(offsets), R, N, K, E,
+                                          _io(out), _ptr(out), _stream(dev)), "fp8_block_grouped_gemm")
+    return out
+
+
+def fp8_block_grouped_wgrad(dyt: torch.Tensor, dyt_scales: torch.Tensor, xt: torch.Tensor, xt_scales: torch.Tensor,
+                            offsets: torch.Tensor, out_dtype=torch.float32, out: Optional[torch.Tensor] = None):
+    """The experts' weight gradients dw[e] = dy_e^T . x_e of token-axis operands: dyt [N, rows_pad] with
+    dyt_scales [rows_pad/128, N] and xt [K, rows_pad] with xt_scales [rows_pad/128, K], both from
+    fp8_block_quantize(axis=1) with group_offsets = offsets (int32 device [E+1]).  Experts without
+    tokens get zeros.  Returns dw [E, N, K]."""
+    lib = load()
+    dev = _on(dyt, "dyt")
+    N, rp = dyt.shape
+    K = xt.shape[0]
+    _shape(dyt, (N, rp), torch.uint8, dev, "dyt")
+    _shape(dyt_scales, (rp // 128, N), torch.float32, dev, "dyt_scales")
+    _shape(xt, (K, rp), torch.uint8, dev, "xt")
+    _shape(xt_scales, (rp // 128, K), torch.float32, dev, "xt_scales")
+    E = offsets.numel() - 1
+    _shape(offsets, (E + 1,), torch.int32, dev, "offsets")
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty((max(E, 0), N, K), dtype=out_dtype, device=dev)
+        else:
+            _shape(out, (E, N, K), out.dtype, dev, "out")
+        _check(lib.fp8_block_grouped_wgrad(_ptr(dyt), _ptr(dyt_scales), _ptr(xt), _ptr(xt_scales), _ptr(offsets), rp, N,
+                                           K, E, _io(out), _ptr(out), _stream(dev)), "fp8_block_grouped_wgrad")
     return out
 
 

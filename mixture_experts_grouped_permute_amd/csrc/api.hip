@@ -580,6 +580,125 @@ moe_status moe_route_permute(const void* logits, int logits_dtype, const void* x
   return MOE_OK;
 }
 
+namespace {
+struct BalanceWs {
+  float* psum;
+  int32_t* cnt;
+};
+BalanceWs carve_balance(Carver& c, int64_t T, int E) {
+  const size_t n = (size_t)balance_blocks(T, E) * (size_t)(E + 1);
+  BalanceWs w;
+  w.psum = reinterpret_cast<float*>(c.take(n * sizeof(float)));
+  w.cnt = reinterpret_cast<int32_t*>(c.take(n * sizeof(int32_t)));
+  return w;
+}
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool under_4g(int64_t bytes) { return bytes < (int64_t)UINT32_MAX; }
+}  // namespace
+
+size_t moe_route_balance_workspace(int64_t T, int E) {
+  if (T <= 0 || E <= 0 || E > MOE_MAX_EXPERTS) return 0;
+  Carver c(nullptr);
+  carve_balance(c, T, E);
+  return c.used;
+}
+
+moe_status moe_route_balance(const void* logits, int logits_dtype, const uint8_t* token_mask, int64_t T, int E, int k,
+                             int32_t* topk_idx, float* topk_prob, int32_t* counts, float* losses, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  moe_status s = check_common(T, 1, E, k);
+  if (s != MOE_OK) return s;
+  MOE_CHECK(logits && io_ok(logits_dtype) && topk_idx && topk_prob && counts && losses, MOE_ERR_INVALID_ARG);
+  MOE_CHECK(workspace && workspace_bytes >= moe_route_balance_workspace(T, E), MOE_ERR_WORKSPACE);
+  Carver c(workspace);
+  const BalanceWs w = carve_balance(c, T, E);
+  HIP_TRY(launch_route_balance(logits, logits_dtype == MOE_F32, token_mask, T, E, k, topk_idx, topk_prob, counts,
+                               losses, w.psum, w.cnt, reinterpret_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_route_balance_bwd(const void* logits, int logits_dtype, const uint8_t* token_mask, int64_t T, int E,
+                                 int k, const int32_t* topk_idx, const float* topk_prob, const int32_t* counts,
+                                 const float* dprob, const float* dlosses, void* dlogits, void* stream) {
+  moe_status s = check_common(T, 1, E, k);
+  if (s != MOE_OK) return s;
+  MOE_CHECK(logits && io_ok(logits_dtype) && counts && dlogits, MOE_ERR_INVALID_ARG);
+  MOE_CHECK(!dprob || (topk_idx && topk_prob), MOE_ERR_INVALID_ARG);
+  HIP_TRY(launch_route_balance_bwd(logits, logits_dtype == MOE_F32, token_mask, T, E, k, topk_idx, topk_prob, counts,
+                                   dprob, dlosses, dlogits, reinterpret_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status fp8_block_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int axis,
+                              const int32_t* group_offsets, int num_groups, uint8_t* q, float* scales, void* stream) {
+  MOE_CHECK(x && q && scales, MOE_ERR_INVALID_ARG);
+  MOE_CHECK(rows > 0 && cols > 0 && io_ok(x_dtype) && (axis == 0 || axis == 1), MOE_ERR_INVALID_ARG);
+  MOE_CHECK(rows < (int64_t)INT32_MAX && cols < (int64_t)INT32_MAX, MOE_ERR_UNSUPPORTED);
+  MOE_CHECK(aligned16(x) && aligned16(q), MOE_ERR_UNSUPPORTED);
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  const bool f32 = x_dtype == MOE_F32;
+  if (axis == 0) {
+    MOE_CHECK(cols % 128 == 0, MOE_ERR_UNSUPPORTED);
+    HIP_TRY(launch_block_rows(x, f32, rows, cols, nullptr, 1, q, scales, st));
+    return MOE_OK;
+  }
+  MOE_CHECK(num_groups >= 1 && num_groups <= MOE_MAX_EXPERTS, MOE_ERR_INVALID_ARG);
+  MOE_CHECK(group_offsets || num_groups == 1, MOE_ERR_INVALID_ARG);
+  MOE_CHECK(cols % 16 == 0, MOE_ERR_UNSUPPORTED);
+  const int64_t rows_pad = block_rows_pad(rows, num_groups);
+  MOE_CHECK(rows_pad < (int64_t)INT32_MAX, MOE_ERR_UNSUPPORTED);
+  HIP_TRY(launch_block_tokens(x, f32, rows, cols, group_offsets, num_groups, rows_pad, nullptr, 1, q, scales, st));
+  return MOE_OK;
+}
+
+moe_status fp8_block_quantize_weights(const void* const* w, int E, int64_t rows, int64_t cols, int transposed,
+                                      const int32_t* skip, uint8_t* q, float* scales, void* stream) {
+  MOE_CHECK(w && q && scales, MOE_ERR_INVALID_ARG);
+  MOE_CHECK(E >= 1 && E <= MOE_MAX_EXPERTS && rows > 0 && cols > 0, MOE_ERR_INVALID_ARG);
+  MOE_CHECK(transposed == 0 || transposed == 1, MOE_ERR_INVALID_ARG);
+  for (int e = 0; e < E; ++e) MOE_CHECK(w[e] != nullptr, MOE_ERR_INVALID_ARG);
+  const int64_t kdim = transposed ? rows : cols, ndim = transposed ? cols : rows;
+  MOE_CHECK(kdim % 128 == 0 && ndim % 16 == 0, MOE_ERR_UNSUPPORTED);
+  MOE_CHECK(rows < (int64_t)INT32_MAX && cols < (int64_t)INT32_MAX && aligned16(q), MOE_ERR_UNSUPPORTED);
+  for (int e = 0; e < E; ++e) MOE_CHECK(aligned16(w[e]), MOE_ERR_UNSUPPORTED);
+  HIP_TRY(launch_block_weights(w, E, rows, cols, transposed != 0, skip, q, scales,
+                               reinterpret_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status fp8_block_grouped_gemm(const uint8_t* a, const float* a_scales, const uint8_t* w, const float* w_scales,
+                                  const int32_t* offsets, int64_t R, int64_t N, int64_t K, int E, int out_dtype,
+                                  void* out, void* stream) {
+  MOE_CHECK(a && a_scales && w && w_scales && offsets && out, MOE_ERR_INVALID_ARG);
+  MOE_CHECK(R > 0 && N > 0 && K > 0 && E >= 1 && E <= MOE_MAX_EXPERTS && io_ok(out_dtype), MOE_ERR_INVALID_ARG);
+  MOE_CHECK(K % 128 == 0 && N % 16 == 0, MOE_ERR_UNSUPPORTED);
+  MOE_CHECK(aligned16(a) && aligned16(w) && aligned16(out), MOE_ERR_UNSUPPORTED);
+  // descriptors span one 256-row tile of a, w or out, the scales of all rows, or one expert's weight scales
+  MOE_CHECK(R < (int64_t)INT32_MAX && N < (int64_t)INT32_MAX && K < (int64_t)INT32_MAX, MOE_ERR_UNSUPPORTED);
+  MOE_CHECK(under_4g(256 * K) && under_4g(256 * N * 4) && under_4g(K / 128 * R * 4), MOE_ERR_UNSUPPORTED);
+  MOE_CHECK(under_4g((N + 127) / 128 * (K / 128) * 4), MOE_ERR_UNSUPPORTED);
+  MOE_CHECK((R / 256 + E) * ((N + 127) / 128) < (int64_t)INT32_MAX, MOE_ERR_UNSUPPORTED);
+  BlockGemm g{a, a_scales, w, w_scales, offsets, out, R, N, K, E, false, out_dtype == MOE_F32};
+  HIP_TRY(launch_block_gemm(g, reinterpret_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status fp8_block_grouped_wgrad(const uint8_t* dyt, const float* dyt_scales, const uint8_t* xt,
+                                   const float* xt_scales, const int32_t* offsets, int64_t rows_pad, int64_t N,
+                                   int64_t K, int E, int out_dtype, void* dw, void* stream) {
+  MOE_CHECK(dyt && dyt_scales && xt && xt_scales && offsets && dw, MOE_ERR_INVALID_ARG);
+  MOE_CHECK(rows_pad > 0 && N > 0 && K > 0 && E >= 1 && E <= MOE_MAX_EXPERTS && io_ok(out_dtype), MOE_ERR_INVALID_ARG);
+  MOE_CHECK(rows_pad % 128 == 0 && N % 16 == 0 && K % 16 == 0, MOE_ERR_UNSUPPORTED);
+  MOE_CHECK(aligned16(dyt) && aligned16(xt) && aligned16(dw), MOE_ERR_UNSUPPORTED);
+  MOE_CHECK(N < (int64_t)INT32_MAX && K < (int64_t)INT32_MAX, MOE_ERR_UNSUPPORTED);
+  MOE_CHECK(under_4g(256 * rows_pad) && under_4g(256 * K * 4) && under_4g(rows_pad / 128 * N * 4) &&
+                under_4g(rows_pad / 128 * K * 4), MOE_ERR_UNSUPPORTED);
+  MOE_CHECK(((N + 255) / 256) * ((K + 127) / 128) * E < (int64_t)INT32_MAX, MOE_ERR_UNSUPPORTED);
+  BlockGemm g{dyt, dyt_scales, xt, xt_scales, offsets, dw, rows_pad, N, K, E, true, out_dtype == MOE_F32};
+  HIP_TRY(launch_block_gemm(g, reinterpret_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
 size_t moe_grouped_mlp_fwd_workspace(const moe_mlp_fwd_args* a) {
   if (validate_fwd(a) != MOE_OK) return 0;
   return plan_fwd(a, nullptr).bytes;

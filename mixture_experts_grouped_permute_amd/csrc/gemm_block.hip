@@ -1,0 +1,431 @@
+// Grouped products of E4M3 operands that carry one fp32 scale per block of 128 along K (gfx950).
+//
+//   product          out[r, n]  = sum_b a_s[b, r] w_s[e, n / 128, b] sum_{k in b} a[r, k] w[e, n, k]
+//                    for the rows r of expert e (forward: N outputs; dgrad: the transposed weights)
+//   weight gradient  dw[e, n, k] = sum_b dy_s[b, n] x_s[b, k] sum_{t in b} dy[n, t] x[k, t]
+//                    over the blocks b of 128 tokens of expert e (token-axis operands)
+//
+// The matrix cores have no fp32 block scale (their scaled form takes powers of two per 32 values), so
+// a block's 128 products are summed by one v_mfma_f32_16x16x128_f8f6f4 from a zero accumulator and the
+// four results a lane holds are added, scaled, to the running sum by four VALU fused multiply-adds.
+// 16 x 16 x 128 is the shape whose K is exactly one block: a 32 x 32 x 64 pair would need 16 temporary
+// registers per tile instead of 4.  The running sums have to be in registers the VALU reads, so a wave
+// owns 128 x 64 outputs (128 registers) and 8 waves, two per SIMD, share a 256 x 256 tile: while one
+// wave's VALU adds a block, the other's MFMAs run.  Per stage and SIMD the MFMAs take 2048 cycles, the
+// adds 1024 (weight gradient, whose scale differs in every column as well: 2048).
+//
+// fp32 outputs take another path (kWide).  The E4M3 matrix instructions align the products of a group to
+// its largest one and drop what falls below about 2^-16 of it: 1.3e-5 (normwise) off on Gaussian
+// codes, under a bf16 output's own 1.7e-3, but not what an fp32 output promises.  The same codes,
+// converted to bf16 (exact) and multiplied by v_mfma_f32_16x16x32_bf16, gave 1e-8.  That costs twice the
+// matrix cycles and 16 registers per converted fragment, so its waves own 64 x 64 of a 256 x 128 tile.
+//
+// A stage is one block of K: 128 bytes of 256 A rows and 256 B rows, loaded straight to LDS into one
+// of two buffers while the other is multiplied, with the stage's 512 scales beside them.  Tiles are
+// dealt to a persistent grid of one workgroup per CU from the expert offsets on the device.
+#include "gemm_core.h"
+
+namespace moe {
+namespace {
+using namespace gemm;
+
+typedef float f32x4v __attribute__((ext_vector_type(4)));
+
+struct BlkKArgs {
+  const uint8_t* a;
+  const float* a_s;
+  const uint8_t* b;
+  const float* b_s;
+  const int32_t* offsets;
+  uint8_t* out;
+  int64_t rows;      // product: R; weight gradient: rows_pad (the token axis' length)
+  int64_t N, K;      // outputs per row, and product: the contracted length / weight gradient: columns
+  int E, nN;
+};
+
+// Row offsets, K units (weight gradient) and tile prefix of the experts.
+struct BlkSched {
+  int off[kMaxExperts + 1];    // first row of the expert; weight gradient: its first block of 128 tokens
+  int units[kMaxExperts];      // product: rows of the expert; weight gradient: its blocks
+  int tile[kMaxExperts + 1];
+};
+
+// One wave scans the offsets, 64 experts at a time.  They are device data: clamped into [0, rows] and
+// made non-decreasing, so that no access leaves the buffers whatever they hold.
+template <bool kWgrad>
+__device__ __forceinline__ void build_blk_sched(BlkSched& s, const BlkKArgs& p, int nM) {
+  const int lane = threadIdx.x & 63;
+  if (threadIdx.x < 64) {
+    const int R = (int)p.rows;
+    int carry = 0, tcarry = 0, top = min(max(p.offsets[0], 0), R);
+    for (int e0 = 0; e0 < p.E; e0 += 64) {
+      const int e = e0 + lane;
+      int hi = e < p.E ? min(max(p.offsets[e + 1], 0), R) : 0;
+      hi = max(hi, top);
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(hi, d, 64);
+        if (lane >= d) hi = max(hi, o);
+      }
+      int lo = __shfl_up(hi, 1, 64);
+      if (lane == 0) lo = top;
+      const int cnt = e < p.E ? hi - lo : 0;
+      const int nblk = (cnt + 127) / 128;
+      int t = kWgrad ? (e < p.E ? nM * p.nN : 0) : (cnt + kBM - 1) / kBM * p.nN;
+      int inc = kWgrad ? nblk : 0;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(inc, d, 64), ot = __shfl_up(t, d, 64);
+        if (lane >= d) { inc += o; t += ot; }
+      }
+      int before = __shfl_up(t, 1, 64);
+      if (lane == 0) before = 0;
+      if (e < p.E) {
+        if (kWgrad) {
+          // the padded segments fit the token axis unless the offsets lie: cut there
+          const int all = R / 128, first = min(carry + inc - nblk, all);
+          s.off[e] = first;
+          s.units[e] = min(nblk, all - first);
+        } else {
+          s.off[e] = lo;
+          s.units[e] = cnt;
+        }
+        s.tile[e] = tcarry + before;
+      }
+      const int last = min(63, p.E - e0 - 1);
+      top = __shfl(hi, last, 64);
+      carry += __shfl(inc, 63, 64);
+      tcarry += __shfl(t, 63, 64);
+    }
+    if (lane == 0) s.tile[p.E] = tcarry;
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ int blk_find(const BlkSched& s, int E, int t) {
+  int lo = 0, hi = E - 1;   // largest e with tile[e] <= t; experts without tiles share a prefix value,
+  while (lo < hi) {         // and the last of them, which has the tiles, is found
+    const int mid = (lo + hi + 1) >> 1;
+    if (s.tile[mid] <= t) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+struct BlkItem {
+  int t, e, mt, nt, n;       // n: stages
+  int row0, mrows;           // A rows: first (product: of all rows; weight gradient: of dw's N) and valid
+};
+
+constexpr int kBlkThreads = 512;
+constexpr int kScaleBytes = 2048;                       // A scales of a stage, then B scales
+constexpr int kBlkScOff = 2 * kStageBytes;
+constexpr int kBlkEpOff = kBlkScOff + 2 * kScaleBytes;  // 2 KB per wave for the epilogue's full-line stores
+constexpr int kBlkLds = kBlkEpOff + 8 * 2048;
+
+typedef __bf16 bf16x2w __attribute__((ext_vector_type(2)));
+
+// A fragment's 32 codes as the matrix instructions take them: as they are, or as bf16.  Group c of 8
+// codes (c < 4) is the lane's share of one 16 x 16 x 32 product.
+template <bool kWide>
+struct Frag;
+template <>
+struct Frag<false> {
+  i32x8 v;
+  __device__ __forceinline__ void set(const i32x8& c) { v = c; }
+};
+template <>
+struct Frag<true> {
+  bf16x8 v[4];
+  __device__ __forceinline__ void set(const i32x8& c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const bf16x2w lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * i + w], 1.0f, false);
+        const bf16x2w hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * i + w], 1.0f, true);
+        v[i][4 * w] = lo[0];
+        v[i][4 * w + 1] = lo[1];
+        v[i][4 * w + 2] = hi[0];
+        v[i][4 * w + 3] = hi[1];
+      }
+  }
+};
+// t[j] = the block's products of B fragment j and A fragment a, j < 4
+__device__ __forceinline__ void blk_mma(const Frag<false> (&b)[4], const Frag<false>& a, f32x4v (&t)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    t[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j].v, a.v, f32x4v{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ void blk_mma(const Frag<true> (&b)[4], const Frag<true>& a, f32x4v (&t)[4]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      t[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j].v[c], a.v[c], c == 0 ? f32x4v{0.f, 0.f, 0.f, 0.f} : t[j], 0, 0, 0);
+}
+
+// kWide (fp32 output): bf16 products
+template <bool kWgrad, bool kWide>
+__global__ __launch_bounds__(kBlkThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void blk_gemm_kernel(const BlkKArgs p) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kBlkLds];
+  __shared__ BlkSched sched;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  constexpr bool kOutF32 = kWide;
+  constexpr int kTN = kWide ? 128 : 256;                // tile columns
+  constexpr int kI = kWide ? 4 : 8;                     // 16-row fragments of a wave; its columns are 64
+  constexpr int kQB = kTN / 64;                         // B loads per wave and stage
+  const int wm = wave / (kTN / 64), wn = wave % (kTN / 64);
+  const int E = p.E;
+  const int64_t N = p.N, K = p.K;
+  const int nM_w = (int)((N + kBM - 1) / kBM);          // weight gradient: tiles along dw's rows
+  build_blk_sched<kWgrad>(sched, p, nM_w);
+  const int total = __builtin_amdgcn_readfirstlane(sched.tile[E]);
+  const int G = gridDim.x, per = G >> 3, xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+  const uint32_t lda = kWgrad ? (uint32_t)p.rows : (uint32_t)K;   // bytes per operand row
+  const int kU = (int)(K / 128);                        // product: blocks of K
+
+  auto decode = [&](int round, BlkItem& it) {
+    it.t = round * G + xcd * per + slot;
+    if (it.t >= total) return;
+    it.e = __builtin_amdgcn_readfirstlane(blk_find(sched, E, it.t));
+    const int local = it.t - __builtin_amdgcn_readfirstlane(sched.tile[it.e]);
+    const int units = __builtin_amdgcn_readfirstlane(sched.units[it.e]);
+    const int nM = kWgrad ? nM_w : (units + kBM - 1) / kBM;
+    tile_coords(local, nM, p.nN, it.mt, it.nt);
+    if (kWgrad) {
+      it.row0 = it.mt * kBM;
+      it.mrows = min(kBM, (int)N - it.row0);
+      it.n = max(units, 1);                             // an expert without tokens: one stage of zeros
+    } else {
+      it.row0 = __builtin_amdgcn_readfirstlane(sched.off[it.e]) + it.mt * kBM;
+      it.mrows = min(kBM, units - it.mt * kBM);
+      it.n = kU;
+    }
+  };
+  // Descriptors: the valid rows of the tile, so that everything past them reads zeros.  Scale rows are
+  // block-major; a stage's are 256 consecutive words, of which those past the valid rows belong to
+  // other rows and only ever multiply zeros.
+  struct Desc { i32x4 va, vb, vs; uint32_t k0; };  // vs: the scales this wave loads; k0: first stage's byte within the rows
+  auto descs = [&](const BlkItem& it, Desc& d) {
+    d.k0 = 0;
+    if (it.t >= total) {
+      d.va = make_vsharp(p.a, 0); d.vb = d.va; d.vs = d.va;
+      return;
+    }
+    const int n0 = it.nt * kTN;
+    if (kWgrad) {
+      const int first = __builtin_amdgcn_readfirstlane(sched.off[it.e]);
+      const bool none = __builtin_amdgcn_readfirstlane(sched.units[it.e]) == 0;
+      const int nrows = min(kTN, (int)K - n0);
+      const int64_t blocks = p.rows / 128;
+      d.va = make_vsharp(p.a + (int64_t)it.row0 * lda, none ? 0u : (uint32_t)it.mrows * lda);
+      d.vb = make_vsharp(p.b + (int64_t)n0 * lda, none ? 0u : (uint32_t)nrows * lda);
+      const float* base = wave < 4 ? p.a_s : p.b_s;
+      const int64_t ldsc = wave < 4 ? N : K, r0 = wave < 4 ? it.row0 : n0;
+      d.vs = make_vsharp(base + (int64_t)first * ldsc + r0, none ? 0u : (uint32_t)(((blocks - first) * ldsc - r0) * 4));
+      d.k0 = (uint32_t)first * 128u;
+    } else {
+      const int nrows = min(kTN, (int)N - n0);
+      const int64_t nb = (N + 127) / 128;
+      d.va = make_vsharp(p.a + (int64_t)it.row0 * K, (uint32_t)it.mrows * lda);
+      d.vb = make_vsharp(p.b + ((int64_t)it.e * N + n0) * K, (uint32_t)nrows * lda);
+      const int b0 = n0 / 128;
+      const float* base = wave < 4 ? p.a_s + it.row0 : p.b_s + ((int64_t)it.e * nb + b0) * kU;
+      d.vs = make_vsharp(base, (uint32_t)((wave < 4 ? (int64_t)kU * p.rows - it.row0 : (nb - b0) * kU) * 4));
+    }
+  };
+
+  // Loads straight to LDS: 1 KB per load, the swz layout; load q of wave w fills row pairs
+  // 4 (n w + q) + lane / 16 of an operand of which a wave loads n KB.  One 4-byte load per stage brings
+  // the scales of A row 64 w + lane (waves 0-3) or B row 64 (w - 4) + lane (waves 4-7).
+  auto row_off = [&](int j) {
+    const uint32_t hs = (uint32_t)((j & 7) | ((j & 4) << 1));
+    const uint32_t sl = (uint32_t)(lane & 15) ^ hs;
+    return (2u * (uint32_t)j + (sl >> 3)) * lda + (sl & 7u) * 16u;
+  };
+  uint32_t vo[4], vob[kQB];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) vo[q] = row_off((wave * 4 + q) * 4 + (lane >> 4));
+#pragma unroll
+  for (int q = 0; q < kQB; ++q) vob[q] = kQB == 4 ? vo[q] : row_off((wave * kQB + q) * 4 + (lane >> 4));
+  const uint32_t sr = (uint32_t)((wave & 3) * 64 + lane);
+  const uint32_t svo = (wave < 4 || kWgrad) ? sr * 4u : (sr >> 7) * (uint32_t)kU * 4u;
+  const uint32_t lds0 = lds_addr(smem) + (uint32_t)wave * 4096u;
+  const uint32_t ldsb = lds_addr(smem) + (uint32_t)kTileBytes + (uint32_t)(wave * kQB) * 1024u;
+  const uint32_t lds_sc = lds_addr(smem + kBlkScOff) + (uint32_t)wave * 256u;
+  // bytes from one stage's scales to the next
+  const uint32_t s_step = (uint32_t)(wave < 4 ? (kWgrad ? N : p.rows) : (kWgrad ? K : 1)) * 4u;
+  auto dma_a = [&](const Desc& d, int b, int kt, int q) {
+    dma16(d.va, lds0 + (uint32_t)b * (uint32_t)kStageBytes + q * 1024u, vo[q], d.k0 + (uint32_t)kt * 128u);
+  };
+  auto dma_b = [&](const Desc& d, int b, int kt, int q) {
+    dma16(d.vb, ldsb + (uint32_t)b * (uint32_t)kStageBytes + q * 1024u, vob[q], d.k0 + (uint32_t)kt * 128u);
+  };
+  auto dma_s = [&](const Desc& d, int b, int kt) {
+    dma4(d.vs, lds_sc + (uint32_t)b * (uint32_t)kScaleBytes, svo, (uint32_t)kt * s_step);
+  };
+
+  // The lane's place in the fragments: row lane % 16 of a 16-row block, 16-byte chunks g and g + 4 of
+  // its 128 bytes (g = lane / 16).  Which of a block's 128 values a lane holds does not matter as long
+  // as A and B agree.  Rows of block i sit 2048 i bytes on, the second chunk at the address ^ 64.
+  const int r16 = lane & 15, g = lane >> 4;
+  const uint32_t fa = swz((uint32_t)(wm * 16 * kI + r16), (uint32_t)g);
+  const uint32_t fb = (uint32_t)kTileBytes + swz((uint32_t)(wn * 64 + r16), (uint32_t)g);
+  auto frag = [&](const uint8_t* st, uint32_t at, int i) {
+    const u32x4 lo = *reinterpret_cast<const u32x4*>(st + at + i * 2048);
+    const u32x4 hi = *reinterpret_cast<const u32x4*>(st + (at ^ 64u) + i * 2048);
+    return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+  };
+
+  BlkItem cur, nxt;
+  Desc dc, dn;
+  decode(0, cur);
+  descs(cur, dc);
+  int par = 0;
+  if (cur.t < total) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) dma_a(dc, 0, 0, q);
+#pragma unroll
+    for (int q = 0; q < kQB; ++q) dma_b(dc, 0, 0, q);
+    dma_s(dc, 0, 0);
+  }
+  for (int round = 0; cur.t < total; ++round) {
+    decode(round + 1, nxt);
+    descs(nxt, dn);
+    f32x4v acc[kI][4];
+#pragma unroll
+    for (int i = 0; i < kI; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int s = 0; s < cur.n; ++s) {
+      const int b = (par + s) & 1;
+      wait_vmcnt<0>();
+      __syncthreads();
+      const bool last = s + 1 == cur.n;
+      Desc dd;
+      dd.va = last ? dn.va : dc.va;
+      dd.vb = last ? dn.vb : dc.vb;
+      dd.vs = last ? dn.vs : dc.vs;
+      dd.k0 = last ? dn.k0 : dc.k0;
+      const int kn = last ? 0 : s + 1;
+      const uint8_t* st = smem + b * kStageBytes;
+      const float* sc = reinterpret_cast<const float*>(smem + kBlkScOff + b * kScaleBytes);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) dma_a(dd, b ^ 1, kn, q);
+#pragma unroll
+      for (int q = 0; q < kQB; ++q) dma_b(dd, b ^ 1, kn, q);
+      dma_s(dd, b ^ 1, kn);
+      Frag<kWide> fbv[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) fbv[j].set(frag(st, fb, j));
+      f32x4v sbv[kWgrad ? 4 : 1];
+      if constexpr (kWgrad) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sbv[j] = *reinterpret_cast<const f32x4v*>(sc + 256 + wn * 64 + j * 16 + g * 4);
+      } else {
+        const float v = sc[256 + wn * 64];
+        sbv[0] = f32x4v{v, v, v, v};
+      }
+      f32x4v t[2][4];
+      float sa[2];
+      i32x8 raw = frag(st, fa, 0);
+#pragma unroll
+      for (int i = 0; i <= kI; ++i) {
+        if (i < kI) {
+          sa[i & 1] = sc[wm * 16 * kI + i * 16 + r16];
+          Frag<kWide> fav;
+          fav.set(raw);
+          blk_mma(fbv, fav, t[i & 1]);
+          if (i + 1 < kI) raw = frag(st, fa, i + 1);
+        }
+        if (i > 0) {
+          const int u = i - 1;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (kWgrad) {
+#pragma unroll
+              for (int r = 0; r < 4; ++r) acc[u][j][r] += (sa[u & 1] * sbv[j][r]) * t[u & 1][j][r];
+            } else {
+              const float sv = sa[u & 1] * sbv[0][0];
+#pragma unroll
+              for (int r = 0; r < 4; ++r) acc[u][j][r] += sv * t[u & 1][j][r];
+            }
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    par = (par + cur.n) & 1;
+
+    // ---- epilogue: lane l holds row 16 i + l % 16 of the wave's block at columns 16 j + 4 (l / 16) + r.
+    // Through the wave's LDS slot 16 rows x 128 bytes at a time, so that stores move whole lines;
+    // the slot's 16-byte chunks are placed at chunk ^ (row & 7).
+    const int64_t ncols = kWgrad ? K : N;
+    const uint32_t osz = kOutF32 ? 4u : 2u;
+    const uint32_t ld = (uint32_t)(ncols * osz);
+    const int64_t o0 = kWgrad ? ((int64_t)cur.e * N + cur.row0) * ld : (int64_t)cur.row0 * ld;
+    const rsrc_t ro = make_rsrc(p.out + o0, (uint32_t)cur.mrows * ld);
+    uint8_t* sl = smem + kBlkEpOff + wave * 2048;
+    const uint32_t row_r = (uint32_t)lane >> 3, ch_r = (uint32_t)lane & 7u;
+#pragma unroll
+    for (int i = 0; i < kI; ++i) {
+#pragma unroll
+      for (int h = 0; h < (kOutF32 ? 2 : 1); ++h) {
+        if constexpr (kOutF32) {
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj)
+            *reinterpret_cast<f32x4v*>(sl + r16 * 128 + (((uint32_t)(jj * 4 + g) ^ (uint32_t)(r16 & 7)) << 4)) = acc[i][2 * h + jj];
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<u32x2*>(sl + r16 * 128 + (((uint32_t)(j * 2 + (g >> 1)) ^ (uint32_t)(r16 & 7)) << 4) + (g & 1) * 8) =
+                u32x2{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
+        }
+        asm volatile("" ::: "memory");   // the LDS unit runs one wave's operations in order
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t row = 8u * q + row_r;
+          const u32x4 v = *reinterpret_cast<const u32x4*>(sl + row * 128u + ((ch_r ^ (row & 7u)) << 4));
+          const uint32_t col = (uint32_t)(cur.nt * kTN + wn * 64) * osz + (uint32_t)h * 128u + ch_r * 16u;   // byte
+          // a chunk past the last column, or a row past the tile's last, is outside the descriptor
+          const uint32_t at = col < ld ? (uint32_t)(wm * 16 * kI + i * 16 + row) * ld + col : 0xFFFFFFF0u;
+          __builtin_amdgcn_raw_buffer_store_b128(v, ro, at, 0, 0);
+        }
+        asm volatile("" ::: "memory");
+      }
+    }
+    cur = nxt;
+    dc = dn;
+  }
+  wait_vmcnt<0>();
+}
+
+}  // namespace
+
+hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t st) {
+  BlkKArgs k{};
+  k.a = g.a;
+  k.a_s = g.a_scales;
+  k.b = g.b;
+  k.b_s = g.b_scales;
+  k.offsets = g.offsets;
+  k.out = reinterpret_cast<uint8_t*>(g.out);
+  k.rows = g.rows;
+  k.N = g.N;
+  k.K = g.K;
+  k.E = g.E;
+  const int tn = g.out_f32 ? 128 : 256;
+  k.nN = (int)(((g.wgrad ? g.K : g.N) + tn - 1) / tn);
+  if (g.wgrad) {
+    if (g.out_f32) blk_gemm_kernel<true, true><<<kGemmGrid, kBlkThreads, 0, st>>>(k);
+    else blk_gemm_kernel<true, false><<<kGemmGrid, kBlkThreads, 0, st>>>(k);
+  } else {
+    if (g.out_f32) blk_gemm_kernel<false, true><<<kGemmGrid, kBlkThreads, 0, st>>>(k);
+    else blk_gemm_kernel<false, false><<<kGemmGrid, kBlkThreads, 0, st>>>(k);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace moe

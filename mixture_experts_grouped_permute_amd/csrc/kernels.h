@@ -174,4 +174,46 @@ hipError_t launch_scale_tail_zero(uint8_t* scales, int64_t rows, int64_t ld, con
                                   hipStream_t st);
 int bwd_dprob_parts(int64_t I);
 
+// ---- router with its losses (balance.hip).  psum: balance_blocks(T, E) x (E + 1) floats, cnt: as many
+// int32.  mask (optional): bytes, 0 = the token does not count.
+constexpr int kBalanceThreads = 1024;
+constexpr int kBalanceMaxBlocks = 256;
+int balance_blocks(int64_t T, int E);
+hipError_t launch_route_balance(const void* logits, bool f32, const uint8_t* mask, int64_t T, int E, int k,
+                                int32_t* idx, float* prob, int32_t* counts, float* losses, float* psum, int32_t* cnt,
+                                hipStream_t st);
+hipError_t launch_route_balance_bwd(const void* logits, bool f32, const uint8_t* mask, int64_t T, int E, int k,
+                                    const int32_t* idx, const float* prob, const int32_t* counts, const float* dprob,
+                                    const float* dlosses, void* dlogits, hipStream_t st);
+
+// ---- FP8 with one fp32 scale per block of 128 (blockq.hip).  src_index (optional): row r is row
+// src_index[r] / src_k of x.
+// rows: codes [rows, cols], scales [cols / 128, rows]; cols % 128 == 0.
+hipError_t launch_block_rows(const void* x, bool x_f32, int64_t rows, int64_t cols, const int32_t* src_index, int src_k,
+                             uint8_t* q, float* scales, hipStream_t st);
+// tokens: segments padded to 128 rows, codes [cols, rows_pad], scales [rows_pad / 128, cols]; cols % 8 == 0.
+inline int64_t block_rows_pad(int64_t rows, int groups) { return (rows + 127) / 128 * 128 + 128 * (int64_t)groups; }
+hipError_t launch_block_tokens(const void* x, bool x_f32, int64_t rows, int64_t cols, const int32_t* offsets, int groups,
+                               int64_t rows_pad, const int32_t* src_index, int src_k, uint8_t* q, float* scales,
+                               hipStream_t st);
+// weights (host table of E bf16 matrices [rows, cols]): codes [E, rows, cols], scales [E, ceil(rows / 128),
+// cols / 128], cols % 128 == 0; transposed: codes [E, cols, rows], scales [E, ceil(cols / 128), rows / 128],
+// rows % 128 == 0.  The other dimension % 8 == 0.
+hipError_t launch_block_weights(const void* const* w, int E, int64_t rows, int64_t cols, bool transposed,
+                                const int32_t* skip, uint8_t* q, float* scales, hipStream_t st);
+
+// ---- grouped products of such operands (gemm_block.hip)
+struct BlockGemm {
+  const uint8_t* a;          // product: [rows, K] codes; weight gradient: dy^T [N, rows]
+  const float* a_scales;     // [K / 128, rows]; [rows / 128, N]
+  const uint8_t* b;          // [E, N, K]; x^T [K, rows]
+  const float* b_scales;     // [E, ceil(N / 128), K / 128]; [rows / 128, K]
+  const int32_t* offsets;    // [E + 1]
+  void* out;                 // [rows, N]; [E, N, K]
+  int64_t rows, N, K;        // weight gradient: rows is the padded token axis
+  int E;
+  bool wgrad, out_f32;
+};
+hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t st);
+
 }  // namespace moe

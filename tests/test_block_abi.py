@@ -1,0 +1,113 @@
+"""Host-side argument checks of the training router and the block-scaled FP8 entry points: every call
+here returns before anything is enqueued (no GPU needed)."""
+import ctypes
+
+import pytest
+import torch
+
+P = 0x1000
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import mixture_experts_grouped_permute_amd as m
+    return m.load()
+
+
+def _codes():
+    from mixture_experts_grouped_permute_amd import _lib as L
+    return L.MOE_ERR_INVALID_ARG, L.MOE_ERR_UNSUPPORTED, L.MOE_ERR_WORKSPACE
+
+
+def test_route_balance_validation(lib):
+    inv, _, wsp = _codes()
+    need = lib.moe_route_balance_workspace(1000, 8)
+    assert need > 0 and lib.moe_route_balance_workspace(0, 8) == 0 and lib.moe_route_balance_workspace(5, 257) == 0
+    good = [P, 0, None, 1000, 8, 2, P, P, P, P, P, need - 1, None]      # refused last, for its workspace
+    assert lib.moe_route_balance(*good) == wsp
+    for at, bad in ((0, None), (1, 2), (3, 0), (4, 257), (5, 0), (5, 9), (5, 17), (6, None), (7, None), (8, None),
+                    (9, None)):
+        a = list(good)
+        a[at] = bad
+        assert lib.moe_route_balance(*a) == inv, at
+    a = list(good)
+    a[10] = None
+    assert lib.moe_route_balance(*a) == wsp
+
+
+def test_route_balance_bwd_validation(lib):
+    inv, uns, _ = _codes()
+    f = lib.moe_route_balance_bwd
+    assert f(None, 0, None, 10, 8, 2, P, P, P, P, P, P, None) == inv
+    assert f(P, 0, None, 10, 8, 2, None, P, P, P, P, P, None) == inv      # dprob without ids
+    assert f(P, 0, None, 10, 8, 2, P, None, P, P, P, P, None) == inv
+    assert f(P, 0, None, 10, 8, 2, P, P, None, P, P, P, None) == inv
+    assert f(P, 0, None, 10, 8, 2, P, P, P, P, P, None, None) == inv
+    assert f(P, 0, None, 10, 8, 9, P, P, P, P, P, P, None) == inv
+    assert f(P, 0, None, 1 << 31, 8, 2, P, P, P, P, P, P, None) == uns
+
+
+def test_fp8_block_quantize_validation(lib):
+    inv, uns, _ = _codes()
+    f = lib.fp8_block_quantize
+    assert f(None, 1, 8, 128, 0, None, 0, P, P, None) == inv
+    assert f(P, 1, 0, 128, 0, None, 0, P, P, None) == inv
+    assert f(P, 2, 8, 128, 0, None, 0, P, P, None) == inv
+    assert f(P, 1, 8, 128, 2, None, 0, P, P, None) == inv
+    assert f(P, 1, 8, 192, 0, None, 0, P, P, None) == uns
+    assert f(P + 8, 1, 8, 128, 0, None, 0, P, P, None) == uns             # alignment
+    assert f(P, 1, 8, 128, 1, None, 2, P, P, None) == inv                 # two groups need offsets
+    assert f(P, 1, 8, 128, 1, P, 257, P, P, None) == inv
+    assert f(P, 1, 8, 24, 1, P, 2, P, P, None) == uns
+    assert f(P, 1, 1 << 31, 128, 0, None, 0, P, P, None) == uns
+
+
+def test_fp8_block_weights_validation(lib):
+    inv, uns, _ = _codes()
+    f = lib.fp8_block_quantize_weights
+    tab = (ctypes.c_void_p * 2)(P, P)
+    bad = (ctypes.c_void_p * 2)(P, None)
+    assert f(tab, 0, 128, 128, 0, None, P, P, None) == inv
+    assert f(bad, 2, 128, 128, 0, None, P, P, None) == inv
+    assert f(tab, 2, 128, 128, 2, None, P, P, None) == inv
+    assert f(tab, 2, 128, 144, 0, None, P, P, None) == uns
+    assert f(tab, 2, 136, 128, 0, None, P, P, None) == uns
+    assert f(tab, 2, 144, 128, 1, None, P, P, None) == uns
+    assert f(tab, 2, 128, 136, 1, None, P, P, None) == uns
+    assert f(tab, 2, 128, 128, 0, None, P + 4, P, None) == uns
+
+
+def test_fp8_block_products_validation(lib):
+    inv, uns, _ = _codes()
+    f = lib.fp8_block_grouped_gemm
+    good = [P, P, P, P, P, 8, 128, 128, 2, 1, P, None]
+    for at, val, code in ((0, None, inv), (4, None, inv), (5, 0, inv), (8, 0, inv), (8, 257, inv), (9, 2, inv),
+                          (10, None, inv), (7, 192, uns), (6, 136, uns), (0, P + 8, uns), (10, P + 8, uns),
+                          (5, 1 << 31, uns), (6, 1 << 23, uns), (7, 1 << 24, uns)):
+        a = list(good)
+        a[at] = val
+        assert f(*a) == code, (at, val)
+    f = lib.fp8_block_grouped_wgrad
+    for at, val, code in ((0, None, inv), (3, None, inv), (5, 0, inv), (9, 3, inv), (5, 136, uns), (6, 136, uns),
+                          (7, 24, uns), (10, P + 4, uns), (5, 1 << 24, uns)):
+        a = list(good)
+        a[at] = val
+        assert f(*a) == code, (at, val)
+
+
+def test_binding_refuses_tensors_off_the_gpu():
+    import mixture_experts_grouped_permute_amd as m
+    x = torch.zeros(4, 128, dtype=torch.bfloat16)
+    u8, f4, i4 = torch.zeros(4, 128, dtype=torch.uint8), torch.zeros(1, 4), torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(TypeError):
+        m.moe_route_balance(x, 2)
+    with pytest.raises(TypeError):
+        m.moe_route_balance_bwd(x, i4, f4, i4)
+    with pytest.raises(TypeError):
+        m.fp8_block_quantize(x)
+    with pytest.raises(TypeError):
+        m.fp8_block_quantize_weights(x[None])
+    with pytest.raises(TypeError):
+        m.fp8_block_grouped_gemm(u8, f4, u8[None], f4, i4)
+    with pytest.raises(TypeError):
+        m.fp8_block_grouped_wgrad(u8, f4, u8, f4, i4)
