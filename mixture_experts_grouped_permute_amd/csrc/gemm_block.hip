@@ -112,7 +112,7 @@ __device__ __forceinline__ int blk_find(const BlkSched& s, int E, int t) {
 }
 
 struct BlkItem {
-  int t, e, mt, nt, n;       // n: stages
+  int t, e, mt, nt, n;       // n: blocks of the contracted axis
   int row0, mrows;           // A rows: first (product: of all rows; weight gradient: of dw's N) and valid
 };
 
@@ -174,6 +174,7 @@ void blk_gemm_kernel(const BlkKArgs p) {
   constexpr bool kOutF32 = kWide;
   constexpr int kTN = kWide ? 128 : 256;                // tile columns
   constexpr int kI = kWide ? 4 : 8;                     // 16-row fragments of a wave; its columns are 64
+  constexpr int kAt = kWide ? 1 : 2;                    // the fragment whose products free the B rows' buffer
   constexpr int kQB = kTN / 64;                         // B loads per wave and stage
   const int wm = wave / (kTN / 64), wn = wave % (kTN / 64);
   const int E = p.E;
@@ -187,6 +188,7 @@ void blk_gemm_kernel(const BlkKArgs p) {
 
   auto decode = [&](int round, BlkItem& it) {
     it.t = round * G + xcd * per + slot;
+    it.n = 0;
     if (it.t >= total) return;
     it.e = __builtin_amdgcn_readfirstlane(blk_find(sched, E, it.t));
     const int local = it.t - __builtin_amdgcn_readfirstlane(sched.tile[it.e]);
@@ -196,7 +198,7 @@ void blk_gemm_kernel(const BlkKArgs p) {
     if (kWgrad) {
       it.row0 = it.mt * kBM;
       it.mrows = min(kBM, (int)N - it.row0);
-      it.n = max(units, 1);                             // an expert without tokens: one stage of zeros
+      it.n = units;
     } else {
       it.row0 = __builtin_amdgcn_readfirstlane(sched.off[it.e]) + it.mt * kBM;
       it.mrows = min(kBM, units - it.mt * kBM);
@@ -216,14 +218,13 @@ void blk_gemm_kernel(const BlkKArgs p) {
     const int n0 = it.nt * kTN;
     if (kWgrad) {
       const int first = __builtin_amdgcn_readfirstlane(sched.off[it.e]);
-      const bool none = __builtin_amdgcn_readfirstlane(sched.units[it.e]) == 0;
       const int nrows = min(kTN, (int)K - n0);
       const int64_t blocks = p.rows / 128;
-      d.va = make_vsharp(p.a + (int64_t)it.row0 * lda, none ? 0u : (uint32_t)it.mrows * lda);
-      d.vb = make_vsharp(p.b + (int64_t)n0 * lda, none ? 0u : (uint32_t)nrows * lda);
+      d.va = make_vsharp(p.a + (int64_t)it.row0 * lda, (uint32_t)it.mrows * lda);
+      d.vb = make_vsharp(p.b + (int64_t)n0 * lda, (uint32_t)nrows * lda);
       const float* base = wave < 4 ? p.a_s : p.b_s;
       const int64_t ldsc = wave < 4 ? N : K, r0 = wave < 4 ? it.row0 : n0;
-      d.vs = make_vsharp(base + (int64_t)first * ldsc + r0, none ? 0u : (uint32_t)(((blocks - first) * ldsc - r0) * 4));
+      d.vs = make_vsharp(base + (int64_t)first * ldsc + r0, (uint32_t)(((blocks - first) * ldsc - r0) * 4));
       d.k0 = (uint32_t)first * 128u;
     } else {
       const int nrows = min(kTN, (int)N - n0);
@@ -278,86 +279,137 @@ void blk_gemm_kernel(const BlkKArgs p) {
     return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
   };
 
+  // Loads run two stages ahead of the products, so every item has at least two: those past its blocks
+  // (an expert without tokens, a single block) load zeros.
+  const i32x4 none = make_vsharp(p.a, 0);
+  // part 0: the A rows and the scales; 1: the B rows.
+  auto issue = [&](const Desc& d, int n, int kt, int b, int part) {
+    const bool live = kt < n;
+    Desc l;
+    l.va = live ? d.va : none;
+    l.vb = live ? d.vb : none;
+    l.vs = live ? d.vs : none;
+    l.k0 = d.k0;
+    if (part == 0) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) dma_a(l, b, kt, q);
+      dma_s(l, b, kt);
+    } else {
+#pragma unroll
+      for (int q = 0; q < kQB; ++q) dma_b(l, b, kt, q);
+    }
+  };
+  // this wave's LDS reads returned, then every wave's
+  auto barrier = [&]() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+
   BlkItem cur, nxt;
   Desc dc, dn;
   decode(0, cur);
+  if (cur.t >= total) return;
   descs(cur, dc);
-  int par = 0;
-  if (cur.t < total) {
+  issue(dc, cur.n, 0, 0, 0);
+  issue(dc, cur.n, 0, 0, 1);
+  wait_vmcnt<0>();
+  barrier();
+  issue(dc, cur.n, 1, 1, 1);
+  issue(dc, cur.n, 1, 1, 0);
+
+  // The stage being multiplied is in buffer `b`, its B fragments and first A fragment in registers.
+  // Stage schedule: the products of A fragment i are issued while the sums of fragment i - 1 are added
+  // and fragment i + 1 is read; once the last A fragment is in registers the buffer is free, and the
+  // barrier there -- after which the next stage has landed -- lets the loads of the stage after next
+  // into it and the next stage's first fragments out of the other one, both under the last products.
+  int b = 0;
+  Frag<kWide> fbv[4];
+  i32x8 raw;
+  auto first_frags = [&](int buf) {
+    const uint8_t* st = smem + buf * kStageBytes;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) dma_a(dc, 0, 0, q);
-#pragma unroll
-    for (int q = 0; q < kQB; ++q) dma_b(dc, 0, 0, q);
-    dma_s(dc, 0, 0);
-  }
+    for (int j = 0; j < 4; ++j) fbv[j].set(frag(st, fb, j));
+    raw = frag(st, fa, 0);
+  };
+  first_frags(0);
   for (int round = 0; cur.t < total; ++round) {
     decode(round + 1, nxt);
     descs(nxt, dn);
+    const int ns = max(cur.n, 2);
     f32x4v acc[kI][4];
 #pragma unroll
     for (int i = 0; i < kI; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = f32x4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-    for (int s = 0; s < cur.n; ++s) {
-      const int b = (par + s) & 1;
-      wait_vmcnt<0>();
-      __syncthreads();
-      const bool last = s + 1 == cur.n;
-      Desc dd;
-      dd.va = last ? dn.va : dc.va;
-      dd.vb = last ? dn.vb : dc.vb;
-      dd.vs = last ? dn.vs : dc.vs;
-      dd.k0 = last ? dn.k0 : dc.k0;
-      const int kn = last ? 0 : s + 1;
+    for (int s = 0; s < ns; ++s) {
       const uint8_t* st = smem + b * kStageBytes;
       const float* sc = reinterpret_cast<const float*>(smem + kBlkScOff + b * kScaleBytes);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) dma_a(dd, b ^ 1, kn, q);
-#pragma unroll
-      for (int q = 0; q < kQB; ++q) dma_b(dd, b ^ 1, kn, q);
-      dma_s(dd, b ^ 1, kn);
-      Frag<kWide> fbv[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) fbv[j].set(frag(st, fb, j));
-      f32x4v sbv[kWgrad ? 4 : 1];
-      if constexpr (kWgrad) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sbv[j] = *reinterpret_cast<const f32x4v*>(sc + 256 + wn * 64 + j * 16 + g * 4);
-      } else {
-        const float v = sc[256 + wn * 64];
-        sbv[0] = f32x4v{v, v, v, v};
-      }
+      // the stage after next, of this item or the next one, into this stage's buffer
+      auto issue_ahead = [&](int s, int ns, int part) {
+        const bool in = s + 2 < ns;
+        Desc l;
+        l.va = in ? dc.va : dn.va;
+        l.vb = in ? dc.vb : dn.vb;
+        l.vs = in ? dc.vs : dn.vs;
+        l.k0 = in ? dc.k0 : dn.k0;
+        issue(l, in ? cur.n : nxt.n, in ? s + 2 : s + 2 - ns, b, part);
+      };
       f32x4v t[2][4];
-      float sa[2];
-      i32x8 raw = frag(st, fa, 0);
+      float sa[2], sal = 0.f;
+      f32x4v sbv[kWgrad ? 4 : 1];
+      auto add = [&](int u) {
 #pragma unroll
-      for (int i = 0; i <= kI; ++i) {
-        if (i < kI) {
-          sa[i & 1] = sc[wm * 16 * kI + i * 16 + r16];
-          Frag<kWide> fav;
-          fav.set(raw);
-          blk_mma(fbv, fav, t[i & 1]);
-          if (i + 1 < kI) raw = frag(st, fa, i + 1);
-        }
-        if (i > 0) {
-          const int u = i - 1;
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (kWgrad) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if constexpr (kWgrad) {
+            for (int r = 0; r < 4; ++r) acc[u][j][r] += ((u == kI - 1 ? sal : sa[u & 1]) * sbv[j][r]) * t[u & 1][j][r];
+          } else {
+            const float sv = (u == kI - 1 ? sal : sa[u & 1]) * sbv[0][0];
 #pragma unroll
-              for (int r = 0; r < 4; ++r) acc[u][j][r] += (sa[u & 1] * sbv[j][r]) * t[u & 1][j][r];
-            } else {
-              const float sv = sa[u & 1] * sbv[0][0];
-#pragma unroll
-              for (int r = 0; r < 4; ++r) acc[u][j][r] += sv * t[u & 1][j][r];
-            }
+            for (int r = 0; r < 4; ++r) acc[u][j][r] += sv * t[u & 1][j][r];
           }
         }
+      };
+#pragma unroll
+      for (int i = 0; i < kI; ++i) {
+        if (i == kAt) {                                 // every wave holds the stage's B fragments
+          barrier();
+          issue_ahead(s, ns, 1);
+        }
+        if (i == kI - 1) {
+          wait_vmcnt<kQB>();                            // the next stage landed: all but the kQB loads above
+          barrier();
+        }
+        Frag<kWide> fav;
+        fav.set(raw);
+        blk_mma(fbv, fav, t[i & 1]);
+        __builtin_amdgcn_sched_barrier(0);
+        // scales: all of the stage's are read ahead of the barrier
+        if (i + 1 < kI) sa[i & 1] = sc[wm * 16 * kI + i * 16 + r16];
+        if (i + 2 == kI) sal = sc[wm * 16 * kI + (kI - 1) * 16 + r16];
+        if (i == 0) {
+          if constexpr (kWgrad) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sbv[j] = *reinterpret_cast<const f32x4v*>(sc + 256 + wn * 64 + j * 16 + g * 4);
+          } else {
+            sbv[0][0] = sc[256 + wn * 64];
+          }
+        }
+        if (i + 1 < kI) {
+          raw = frag(st, fa, i + 1);
+        } else {
+          issue_ahead(s, ns, 0);
+        }
+        if (i > 0) add(i - 1);
         __builtin_amdgcn_sched_barrier(0);
       }
+      first_frags(b ^ 1);
+      __builtin_amdgcn_sched_barrier(0);
+      add(kI - 1);
+      b ^= 1;
     }
-    par = (par + cur.n) & 1;
 
     // ---- epilogue: lane l holds row 16 i + l % 16 of the wave's block at columns 16 j + 4 (l / 16) + r.
     // Through the wave's LDS slot 16 rows x 128 bytes at a time, so that stores move whole lines;
