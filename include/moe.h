@@ -356,13 +356,21 @@ moe_status fp8_block_quantize_weights(const void* const* w, int E, int64_t rows,
  *          (moe_permute's).  Clamped into [0, R] and made non-decreasing on
  *          the device.  Rows outside [offsets[0], offsets[E]) of out are left
  *          as they were.
- * out      [R, N] in out_dtype (MOE_BF16 or MOE_F32), fp32 sums rounded once.
+ * out      [R, N] in out_dtype, sums in fp32 rounded once.  MOE_F32: exact E4M3
+ *          products and fp32 sums throughout.  MOE_BF16: the E4M3 matrix
+ *          instructions, which are twice as fast and align the products of a
+ *          group to its largest one (about 1e-5 normwise, under the rounding
+ *          of the output).
  * K % 128 == 0, N % 16 == 0 (else MOE_ERR_UNSUPPORTED); pointers of codes and
  * out 16-byte aligned; 256 K, 256 N * 4 and R K / 32 below 2^32.
+ * workspace: fp8_block_grouped_gemm_workspace bytes (device, 16-byte aligned;
+ * 0 for some sizes, then NULL will do): fp32 sums of tiles that are split
+ * along K.  Nothing is read before it is written or kept from call to call.
  * ------------------------------------------------------------------------ */
+size_t fp8_block_grouped_gemm_workspace(int64_t R, int64_t N, int64_t K, int out_dtype);
 moe_status fp8_block_grouped_gemm(const uint8_t* a, const float* a_scales, const uint8_t* w, const float* w_scales,
                                   const int32_t* offsets, int64_t R, int64_t N, int64_t K, int E, int out_dtype,
-                                  void* out, void* stream);
+                                  void* out, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * fp8_block_grouped_wgrad -- the experts' weight gradients on token-axis
@@ -377,11 +385,14 @@ moe_status fp8_block_grouped_gemm(const uint8_t* a, const float* a_scales, const
  *          without tokens get zeros.
  * N % 16 == 0, K % 16 == 0, rows_pad % 128 == 0 (else MOE_ERR_UNSUPPORTED);
  * pointers 16-byte aligned; 256 rows_pad and 256 K * 4 and rows_pad N / 32 and
- * rows_pad K / 32 below 2^32.
+ * rows_pad K / 32 below 2^32.  workspace: fp8_block_grouped_wgrad_workspace
+ * bytes, as above (tiles split along the tokens).
  * ------------------------------------------------------------------------ */
+size_t fp8_block_grouped_wgrad_workspace(int64_t rows_pad, int64_t N, int64_t K, int out_dtype);
 moe_status fp8_block_grouped_wgrad(const uint8_t* dyt, const float* dyt_scales, const uint8_t* xt,
                                    const float* xt_scales, const int32_t* offsets, int64_t rows_pad, int64_t N,
-                                   int64_t K, int E, int out_dtype, void* dw, void* stream);
+                                   int64_t K, int E, int out_dtype, void* dw, void* workspace,
+                                   size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * moe_grouped_mlp_fwd -- the whole expert MLP forward.

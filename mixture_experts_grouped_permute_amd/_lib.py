@@ -31,7 +31,8 @@ EXPORTS = (
     "fp8_tensor_quantize", "mxfp8_quantize_weights", "moe_permute_noalloc", "moe_tile_stats_bytes",
     "moe_set_tile_stats", "moe_probe_workgroups", "moe_mfma_probe", "moe_load_probe_bytes", "moe_load_probe",
     "moe_route_balance_workspace", "moe_route_balance", "moe_route_balance_bwd", "fp8_block_quantize",
-    "fp8_block_quantize_weights", "fp8_block_grouped_gemm", "fp8_block_grouped_wgrad",
+    "fp8_block_quantize_weights", "fp8_block_grouped_gemm_workspace", "fp8_block_grouped_gemm",
+    "fp8_block_grouped_wgrad_workspace", "fp8_block_grouped_wgrad",
 )
 NOALLOC_SCRATCH_BYTES = 4 << 20    # MOE_NOALLOC_SCRATCH_BYTES
 
@@ -164,12 +165,14 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.fp8_block_quantize_weights.restype = ctypes.c_int
     lib.fp8_block_quantize_weights.argtypes = [ctypes.POINTER(_vp), ctypes.c_int, _i64, _i64, ctypes.c_int, _vp, _vp,
                                                _vp, _vp]
-    lib.fp8_block_grouped_gemm.restype = ctypes.c_int
-    lib.fp8_block_grouped_gemm.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int,
-                                           _vp, _vp]
-    lib.fp8_block_grouped_wgrad.restype = ctypes.c_int
-    lib.fp8_block_grouped_wgrad.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int,
-                                            _vp, _vp]
+    for name in ("fp8_block_grouped_gemm", "fp8_block_grouped_wgrad"):
+        f = getattr(lib, name + "_workspace")
+        f.restype = ctypes.c_size_t
+        f.argtypes = [_i64, _i64, _i64, ctypes.c_int]
+        f = getattr(lib, name)
+        f.restype = ctypes.c_int
+        f.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, _vp, _vp,
+                      ctypes.c_size_t, _vp]
     if path is None:
         _lib = lib
     return lib
@@ -454,6 +457,15 @@ def _shape(t: Optional[torch.Tensor], shape, dtype: torch.dtype, device: torch.d
         raise ValueError(f"{what} must be contiguous")
 
 
+def _scratch(nbytes: int, device: torch.device) -> Optional[torch.Tensor]:
+    """A workspace of the call's own (None for 0 bytes): a captured call keeps it in its graph's memory."""
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def _nbytes(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.numel()
+
+
 def _mask(token_mask: Optional[torch.Tensor], T: int, device: torch.device) -> None:
     if token_mask is None:
         return
@@ -479,10 +491,9 @@ def moe_route_balance(logits: torch.Tensor, k: int, token_mask: Optional[torch.T
         prob = torch.empty((T, k), dtype=torch.float32, device=dev)
         counts = torch.empty(E, dtype=torch.int32, device=dev)
         losses = torch.empty(2, dtype=torch.float32, device=dev)
-        # a workspace of the call's own: a captured call keeps it in its graph's memory
-        ws = torch.empty(max(lib.moe_route_balance_workspace(T, E), 256), dtype=torch.uint8, device=dev)
+        ws = _scratch(lib.moe_route_balance_workspace(T, E), dev)
         _check(lib.moe_route_balance(_ptr(logits), _io(logits), _ptr(token_mask), T, E, k, _ptr(idx), _ptr(prob),
-                                     _ptr(counts), _ptr(losses), ws.data_ptr(), ws.numel(), _stream(dev)),
+                                     _ptr(counts), _ptr(losses), _ptr(ws), _nbytes(ws), _stream(dev)),
                "moe_route_balance")
     return idx, prob, counts, losses
 
@@ -592,8 +603,11 @@ def fp8_block_grouped_gemm(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Ten
             out = torch.empty((R, N), dtype=out_dtype, device=dev)
         else:
             _shape(out, (R, N), out.dtype, dev, "out")
+        od = _io(out)
+        ws = _scratch(lib.fp8_block_grouped_gemm_workspace(R, N, K, od), dev)
         _check(lib.fp8_block_grouped_gemm(_ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), _ptr(offsets), R, N, K, E,
-                                          _io(out), _ptr(out), _stream(dev)), "fp8_block_grouped_gemm")
+                                          od, _ptr(out), _ptr(ws), _nbytes(ws), _stream(dev)),
+               "fp8_block_grouped_gemm")
     return out
 
 
@@ -618,8 +632,11 @@ def fp8_block_grouped_wgrad(dyt: torch.Tensor, dyt_scales: torch.Tensor, xt: tor
             out = torch.empty((max(E, 0), N, K), dtype=out_dtype, device=dev)
         else:
             _shape(out, (E, N, K), out.dtype, dev, "out")
+        od = _io(out)
+        ws = _scratch(lib.fp8_block_grouped_wgrad_workspace(rp, N, K, od), dev)
         _check(lib.fp8_block_grouped_wgrad(_ptr(dyt), _ptr(dyt_scales), _ptr(xt), _ptr(xt_scales), _ptr(offsets), rp, N,
-                                           K, E, _io(out), _ptr(out), _stream(dev)), "fp8_block_grouped_wgrad")
+                                           K, E, od, _ptr(out), _ptr(ws), _nbytes(ws), _stream(dev)),
+               "fp8_block_grouped_wgrad")
     return out
 
 

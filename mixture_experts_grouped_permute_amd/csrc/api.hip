@@ -666,9 +666,19 @@ moe_status fp8_block_quantize_weights(const void* const* w, int E, int64_t rows,
   return MOE_OK;
 }
 
+size_t fp8_block_grouped_gemm_workspace(int64_t R, int64_t N, int64_t K, int out_dtype) {
+  if (R <= 0 || N <= 0 || K <= 0 || !io_ok(out_dtype)) return 0;
+  return align_up(block_gemm_part_bytes(false, out_dtype == MOE_F32, R, N, K));
+}
+
+size_t fp8_block_grouped_wgrad_workspace(int64_t rows_pad, int64_t N, int64_t K, int out_dtype) {
+  if (rows_pad <= 0 || N <= 0 || K <= 0 || !io_ok(out_dtype)) return 0;
+  return align_up(block_gemm_part_bytes(true, out_dtype == MOE_F32, rows_pad, N, K));
+}
+
 moe_status fp8_block_grouped_gemm(const uint8_t* a, const float* a_scales, const uint8_t* w, const float* w_scales,
                                   const int32_t* offsets, int64_t R, int64_t N, int64_t K, int E, int out_dtype,
-                                  void* out, void* stream) {
+                                  void* out, void* workspace, size_t workspace_bytes, void* stream) {
   MOE_CHECK(a && a_scales && w && w_scales && offsets && out, MOE_ERR_INVALID_ARG);
   MOE_CHECK(R > 0 && N > 0 && K > 0 && E >= 1 && E <= MOE_MAX_EXPERTS && io_ok(out_dtype), MOE_ERR_INVALID_ARG);
   MOE_CHECK(K % 128 == 0 && N % 16 == 0, MOE_ERR_UNSUPPORTED);
@@ -678,14 +688,19 @@ moe_status fp8_block_grouped_gemm(const uint8_t* a, const float* a_scales, const
   MOE_CHECK(under_4g(256 * K) && under_4g(256 * N * 4) && under_4g(K / 128 * R * 4), MOE_ERR_UNSUPPORTED);
   MOE_CHECK(under_4g((N + 127) / 128 * (K / 128) * 4), MOE_ERR_UNSUPPORTED);
   MOE_CHECK((R / 256 + E) * ((N + 127) / 128) < (int64_t)INT32_MAX, MOE_ERR_UNSUPPORTED);
-  BlockGemm g{a, a_scales, w, w_scales, offsets, out, R, N, K, E, false, out_dtype == MOE_F32};
+  const size_t need = fp8_block_grouped_gemm_workspace(R, N, K, out_dtype);
+  MOE_CHECK(!need || (workspace && workspace_bytes >= need), MOE_ERR_WORKSPACE);
+  MOE_CHECK(!need || aligned16(workspace), MOE_ERR_UNSUPPORTED);
+  BlockGemm g{a, a_scales, w, w_scales, offsets, out, R, N, K, E, false, out_dtype == MOE_F32,
+              need ? reinterpret_cast<float*>(workspace) : nullptr};
   HIP_TRY(launch_block_gemm(g, reinterpret_cast<hipStream_t>(stream)));
   return MOE_OK;
 }
 
 moe_status fp8_block_grouped_wgrad(const uint8_t* dyt, const float* dyt_scales, const uint8_t* xt,
                                    const float* xt_scales, const int32_t* offsets, int64_t rows_pad, int64_t N,
-                                   int64_t K, int E, int out_dtype, void* dw, void* stream) {
+                                   int64_t K, int E, int out_dtype, void* dw, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
   MOE_CHECK(dyt && dyt_scales && xt && xt_scales && offsets && dw, MOE_ERR_INVALID_ARG);
   MOE_CHECK(rows_pad > 0 && N > 0 && K > 0 && E >= 1 && E <= MOE_MAX_EXPERTS && io_ok(out_dtype), MOE_ERR_INVALID_ARG);
   MOE_CHECK(rows_pad % 128 == 0 && N % 16 == 0 && K % 16 == 0, MOE_ERR_UNSUPPORTED);
@@ -694,7 +709,11 @@ moe_status fp8_block_grouped_wgrad(const uint8_t* dyt, const float* dyt_scales, 
   MOE_CHECK(under_4g(256 * rows_pad) && under_4g(256 * K * 4) && under_4g(rows_pad / 128 * N * 4) &&
                 under_4g(rows_pad / 128 * K * 4), MOE_ERR_UNSUPPORTED);
   MOE_CHECK(((N + 255) / 256) * ((K + 127) / 128) * E < (int64_t)INT32_MAX, MOE_ERR_UNSUPPORTED);
-  BlockGemm g{dyt, dyt_scales, xt, xt_scales, offsets, dw, rows_pad, N, K, E, true, out_dtype == MOE_F32};
+  const size_t need = fp8_block_grouped_wgrad_workspace(rows_pad, N, K, out_dtype);
+  MOE_CHECK(!need || (workspace && workspace_bytes >= need), MOE_ERR_WORKSPACE);
+  MOE_CHECK(!need || aligned16(workspace), MOE_ERR_UNSUPPORTED);
+  BlockGemm g{dyt, dyt_scales, xt, xt_scales, offsets, dw, rows_pad, N, K, E, true, out_dtype == MOE_F32,
+              need ? reinterpret_cast<float*>(workspace) : nullptr};
   HIP_TRY(launch_block_gemm(g, reinterpret_cast<hipStream_t>(stream)));
   return MOE_OK;
 }

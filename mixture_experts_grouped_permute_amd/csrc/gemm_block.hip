@@ -41,13 +41,30 @@ struct BlkKArgs {
   int64_t rows;      // product: R; weight gradient: rows_pad (the token axis' length)
   int64_t N, K;      // outputs per row, and product: the contracted length / weight gradient: columns
   int E, nN;
+  float* part;       // fp32 sums of the split tiles' parts, or null: no tile is split
+  int part_rows;     // rows of a part's slot
+  int min_units;     // blocks per part, at least
 };
+
+// The tiles of the last, partly filled round -- of all of them, where there are fewer than workgroups --
+// are split along the contracted axis into S parts each, so that every workgroup has one: tiles
+// [full, total) as (total - full) S items.  S = 1: none are split.
+struct BlkSplit {
+  int full, S;
+};
+__device__ __forceinline__ BlkSplit blk_split(int total, int G, int units, const BlkKArgs& p) {
+  const int rem = total % G;
+  if (!p.part || rem == 0) return {total, 1};
+  const int S = min(G / rem, units / p.min_units);
+  return S < 2 ? BlkSplit{total, 1} : BlkSplit{total - rem, S};
+}
 
 // Row offsets, K units (weight gradient) and tile prefix of the experts.
 struct BlkSched {
   int off[kMaxExperts + 1];    // first row of the expert; weight gradient: its first block of 128 tokens
   int units[kMaxExperts];      // product: rows of the expert; weight gradient: its blocks
   int tile[kMaxExperts + 1];
+  int most;                    // most K units of an expert
 };
 
 // One wave scans the offsets, 64 experts at a time.  They are device data: clamped into [0, rows] and
@@ -57,7 +74,7 @@ __device__ __forceinline__ void build_blk_sched(BlkSched& s, const BlkKArgs& p, 
   const int lane = threadIdx.x & 63;
   if (threadIdx.x < 64) {
     const int R = (int)p.rows;
-    int carry = 0, tcarry = 0, top = min(max(p.offsets[0], 0), R);
+    int carry = 0, tcarry = 0, most = 0, top = min(max(p.offsets[0], 0), R);
     for (int e0 = 0; e0 < p.E; e0 += 64) {
       const int e = e0 + lane;
       int hi = e < p.E ? min(max(p.offsets[e + 1], 0), R) : 0;
@@ -71,6 +88,7 @@ __device__ __forceinline__ void build_blk_sched(BlkSched& s, const BlkKArgs& p, 
       if (lane == 0) lo = top;
       const int cnt = e < p.E ? hi - lo : 0;
       const int nblk = (cnt + 127) / 128;
+      most = max(most, nblk);
       int t = kWgrad ? (e < p.E ? nM * p.nN : 0) : (cnt + kBM - 1) / kBM * p.nN;
       int inc = kWgrad ? nblk : 0;
 #pragma unroll
@@ -97,7 +115,12 @@ __device__ __forceinline__ void build_blk_sched(BlkSched& s, const BlkKArgs& p, 
       carry += __shfl(inc, 63, 64);
       tcarry += __shfl(t, 63, 64);
     }
-    if (lane == 0) s.tile[p.E] = tcarry;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) most = max(most, __shfl_xor(most, d, 64));
+    if (lane == 0) {
+      s.tile[p.E] = tcarry;
+      s.most = kWgrad ? most : (int)(p.K / 128);
+    }
   }
   __syncthreads();
 }
@@ -112,7 +135,8 @@ __device__ __forceinline__ int blk_find(const BlkSched& s, int E, int t) {
 }
 
 struct BlkItem {
-  int t, e, mt, nt, n;       // n: blocks of the contracted axis
+  int t, e, mt, nt;
+  int part, u0, n;           // part of a split tile (-1: whole), first block of the contracted axis, blocks
   int row0, mrows;           // A rows: first (product: of all rows; weight gradient: of dw's N) and valid
 };
 
@@ -171,7 +195,6 @@ void blk_gemm_kernel(const BlkKArgs p) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[kBlkLds];
   __shared__ BlkSched sched;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  constexpr bool kOutF32 = kWide;
   constexpr int kTN = kWide ? 128 : 256;                // tile columns
   constexpr int kI = kWide ? 4 : 8;                     // 16-row fragments of a wave; its columns are 64
   constexpr int kAt = kWide ? 1 : 2;                    // the fragment whose products free the B rows' buffer
@@ -181,17 +204,25 @@ void blk_gemm_kernel(const BlkKArgs p) {
   const int64_t N = p.N, K = p.K;
   const int nM_w = (int)((N + kBM - 1) / kBM);          // weight gradient: tiles along dw's rows
   build_blk_sched<kWgrad>(sched, p, nM_w);
-  const int total = __builtin_amdgcn_readfirstlane(sched.tile[E]);
+  const int tiles = __builtin_amdgcn_readfirstlane(sched.tile[E]);
   const int G = gridDim.x, per = G >> 3, xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+  const BlkSplit sp = blk_split(tiles, G, __builtin_amdgcn_readfirstlane(sched.most), p);
+  const int total = sp.full + (tiles - sp.full) * sp.S;   // items
   const uint32_t lda = kWgrad ? (uint32_t)p.rows : (uint32_t)K;   // bytes per operand row
   const int kU = (int)(K / 128);                        // product: blocks of K
 
   auto decode = [&](int round, BlkItem& it) {
     it.t = round * G + xcd * per + slot;
-    it.n = 0;
+    it.n = it.u0 = 0;
     if (it.t >= total) return;
-    it.e = __builtin_amdgcn_readfirstlane(blk_find(sched, E, it.t));
-    const int local = it.t - __builtin_amdgcn_readfirstlane(sched.tile[it.e]);
+    int tile = it.t;
+    it.part = -1;
+    if (it.t >= sp.full) {
+      tile = sp.full + (it.t - sp.full) / sp.S;
+      if (sp.S > 1) it.part = (it.t - sp.full) % sp.S;
+    }
+    it.e = __builtin_amdgcn_readfirstlane(blk_find(sched, E, tile));
+    const int local = tile - __builtin_amdgcn_readfirstlane(sched.tile[it.e]);
     const int units = __builtin_amdgcn_readfirstlane(sched.units[it.e]);
     const int nM = kWgrad ? nM_w : (units + kBM - 1) / kBM;
     tile_coords(local, nM, p.nN, it.mt, it.nt);
@@ -204,13 +235,18 @@ void blk_gemm_kernel(const BlkKArgs p) {
       it.mrows = min(kBM, units - it.mt * kBM);
       it.n = kU;
     }
+    it.u0 = 0;
+    if (it.part >= 0) {
+      it.u0 = it.part * it.n / sp.S;
+      it.n = (it.part + 1) * it.n / sp.S - it.u0;
+    }
   };
   // Descriptors: the valid rows of the tile, so that everything past them reads zeros.  Scale rows are
   // block-major; a stage's are 256 consecutive words, of which those past the valid rows belong to
   // other rows and only ever multiply zeros.
-  struct Desc { i32x4 va, vb, vs; uint32_t k0; };  // vs: the scales this wave loads; k0: first stage's byte within the rows
+  struct Desc { i32x4 va, vb, vs; int u0, s0; };  // vs: the scales this wave loads; u0, s0: first block within the rows, the scales
   auto descs = [&](const BlkItem& it, Desc& d) {
-    d.k0 = 0;
+    d.u0 = d.s0 = it.u0;
     if (it.t >= total) {
       d.va = make_vsharp(p.a, 0); d.vb = d.va; d.vs = d.va;
       return;
@@ -225,7 +261,7 @@ void blk_gemm_kernel(const BlkKArgs p) {
       const float* base = wave < 4 ? p.a_s : p.b_s;
       const int64_t ldsc = wave < 4 ? N : K, r0 = wave < 4 ? it.row0 : n0;
       d.vs = make_vsharp(base + (int64_t)first * ldsc + r0, (uint32_t)(((blocks - first) * ldsc - r0) * 4));
-      d.k0 = (uint32_t)first * 128u;
+      d.u0 += first;
     } else {
       const int nrows = min(kTN, (int)N - n0);
       const int64_t nb = (N + 127) / 128;
@@ -258,13 +294,13 @@ void blk_gemm_kernel(const BlkKArgs p) {
   // bytes from one stage's scales to the next
   const uint32_t s_step = (uint32_t)(wave < 4 ? (kWgrad ? N : p.rows) : (kWgrad ? K : 1)) * 4u;
   auto dma_a = [&](const Desc& d, int b, int kt, int q) {
-    dma16(d.va, lds0 + (uint32_t)b * (uint32_t)kStageBytes + q * 1024u, vo[q], d.k0 + (uint32_t)kt * 128u);
+    dma16(d.va, lds0 + (uint32_t)b * (uint32_t)kStageBytes + q * 1024u, vo[q], (uint32_t)(d.u0 + kt) * 128u);
   };
   auto dma_b = [&](const Desc& d, int b, int kt, int q) {
-    dma16(d.vb, ldsb + (uint32_t)b * (uint32_t)kStageBytes + q * 1024u, vob[q], d.k0 + (uint32_t)kt * 128u);
+    dma16(d.vb, ldsb + (uint32_t)b * (uint32_t)kStageBytes + q * 1024u, vob[q], (uint32_t)(d.u0 + kt) * 128u);
   };
   auto dma_s = [&](const Desc& d, int b, int kt) {
-    dma4(d.vs, lds_sc + (uint32_t)b * (uint32_t)kScaleBytes, svo, (uint32_t)kt * s_step);
+    dma4(d.vs, lds_sc + (uint32_t)b * (uint32_t)kScaleBytes, svo, (uint32_t)(d.s0 + kt) * s_step);
   };
 
   // The lane's place in the fragments: row lane % 16 of a 16-row block, 16-byte chunks g and g + 4 of
@@ -289,7 +325,8 @@ void blk_gemm_kernel(const BlkKArgs p) {
     l.va = live ? d.va : none;
     l.vb = live ? d.vb : none;
     l.vs = live ? d.vs : none;
-    l.k0 = d.k0;
+    l.u0 = d.u0;
+    l.s0 = d.s0;
     if (part == 0) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) dma_a(l, b, kt, q);
@@ -353,7 +390,8 @@ void blk_gemm_kernel(const BlkKArgs p) {
         l.va = in ? dc.va : dn.va;
         l.vb = in ? dc.vb : dn.vb;
         l.vs = in ? dc.vs : dn.vs;
-        l.k0 = in ? dc.k0 : dn.k0;
+        l.u0 = in ? dc.u0 : dn.u0;
+        l.s0 = in ? dc.s0 : dn.s0;
         issue(l, in ? cur.n : nxt.n, in ? s + 2 : s + 2 - ns, b, part);
       };
       f32x4v t[2][4];
@@ -415,36 +453,57 @@ void blk_gemm_kernel(const BlkKArgs p) {
     // Through the wave's LDS slot 16 rows x 128 bytes at a time, so that stores move whole lines;
     // the slot's 16-byte chunks are placed at chunk ^ (row & 7).
     const int64_t ncols = kWgrad ? K : N;
-    const uint32_t osz = kOutF32 ? 4u : 2u;
-    const uint32_t ld = (uint32_t)(ncols * osz);
-    const int64_t o0 = kWgrad ? ((int64_t)cur.e * N + cur.row0) * ld : (int64_t)cur.row0 * ld;
-    const rsrc_t ro = make_rsrc(p.out + o0, (uint32_t)cur.mrows * ld);
     uint8_t* sl = smem + kBlkEpOff + wave * 2048;
-    const uint32_t row_r = (uint32_t)lane >> 3, ch_r = (uint32_t)lane & 7u;
+    // (the lane is laundered, so that its addresses are not worked out ahead of the stages and kept)
+    int el = lane;
+    asm volatile("" : "+v"(el));
+    const uint32_t row_r = (uint32_t)el >> 3, ch_r = (uint32_t)el & 7u;
+    const uint32_t er = (uint32_t)el & 15u, eg = (uint32_t)el >> 4;
+    // rows of `ld` bytes from the tile's first one, its columns from byte c0; chunks past the last
+    // column and rows past the tile's last are outside the descriptor
+    auto store = [&](const rsrc_t& ro, uint32_t ld, uint32_t c0, uint32_t i, uint32_t c) {
 #pragma unroll
-    for (int i = 0; i < kI; ++i) {
+      for (int q = 0; q < 2; ++q) {
+        const uint32_t row = 8u * q + row_r;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(sl + row * 128u + ((ch_r ^ (row & 7u)) << 4));
+        const uint32_t col = c0 + c + ch_r * 16u;
+        const uint32_t at = col < ld ? ((uint32_t)(wm * 16 * kI) + i * 16u + row) * ld + col : 0xFFFFFFF0u;
+        __builtin_amdgcn_raw_buffer_store_b128(v, ro, at, 0, 0);
+      }
+    };
+    if (kWide || cur.part >= 0) {
+      const bool whole = cur.part < 0;
+      const uint32_t ld = whole ? (uint32_t)ncols * 4u : kTN * 4u;
+      const int64_t o0 = ((kWgrad ? (int64_t)cur.e * N : 0) + cur.row0) * ncols;
+      const rsrc_t ro = make_rsrc(whole ? reinterpret_cast<float*>(p.out) + o0
+                                        : p.part + (int64_t)(cur.t - sp.full) * p.part_rows * kTN,
+                                  (uint32_t)cur.mrows * ld);
+      const uint32_t c0 = ((whole ? (uint32_t)cur.nt * kTN : 0u) + (uint32_t)wn * 64u) * 4u;
 #pragma unroll
-      for (int h = 0; h < (kOutF32 ? 2 : 1); ++h) {
-        if constexpr (kOutF32) {
+      for (int i = 0; i < kI; ++i) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
           for (int jj = 0; jj < 2; ++jj)
-            *reinterpret_cast<f32x4v*>(sl + r16 * 128 + (((uint32_t)(jj * 4 + g) ^ (uint32_t)(r16 & 7)) << 4)) = acc[i][2 * h + jj];
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<u32x2*>(sl + r16 * 128 + (((uint32_t)(j * 2 + (g >> 1)) ^ (uint32_t)(r16 & 7)) << 4) + (g & 1) * 8) =
-                u32x2{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
+            *reinterpret_cast<f32x4v*>(sl + er * 128u + (((uint32_t)jj * 4u + eg) ^ (er & 7u)) * 16u) = acc[i][2 * h + jj];
+          asm volatile("" ::: "memory");   // the LDS unit runs one wave's operations in order
+          store(ro, ld, c0, (uint32_t)i, (uint32_t)h * 128u);
+          asm volatile("" ::: "memory");
         }
-        asm volatile("" ::: "memory");   // the LDS unit runs one wave's operations in order
+      }
+    } else {
+      const uint32_t ld = (uint32_t)ncols * 2u;
+      const int64_t o0 = ((kWgrad ? (int64_t)cur.e * N : 0) + cur.row0) * ncols;
+      const rsrc_t ro = make_rsrc(reinterpret_cast<uint16_t*>(p.out) + o0, (uint32_t)cur.mrows * ld);
+      const uint32_t c0 = (uint32_t)(cur.nt * kTN + wn * 64) * 2u;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const uint32_t row = 8u * q + row_r;
-          const u32x4 v = *reinterpret_cast<const u32x4*>(sl + row * 128u + ((ch_r ^ (row & 7u)) << 4));
-          const uint32_t col = (uint32_t)(cur.nt * kTN + wn * 64) * osz + (uint32_t)h * 128u + ch_r * 16u;   // byte
-          // a chunk past the last column, or a row past the tile's last, is outside the descriptor
-          const uint32_t at = col < ld ? (uint32_t)(wm * 16 * kI + i * 16 + row) * ld + col : 0xFFFFFFF0u;
-          __builtin_amdgcn_raw_buffer_store_b128(v, ro, at, 0, 0);
-        }
+      for (int i = 0; i < kI; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<u32x2*>(sl + er * 128u + (((uint32_t)j * 2u + (eg >> 1)) ^ (er & 7u)) * 16u + (eg & 1u) * 8u) =
+              u32x2{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
+        asm volatile("" ::: "memory");
+        store(ro, ld, c0, (uint32_t)i, 0u);
         asm volatile("" ::: "memory");
       }
     }
@@ -454,7 +513,63 @@ void blk_gemm_kernel(const BlkKArgs p) {
   wait_vmcnt<0>();
 }
 
+// The split tiles: the S parts of tile full + blockIdx.x added in their order, rows kJoinRows blockIdx.y
+// + [0, kJoinRows).  Eight parts' loads are in flight at once (one at a time, 85 parts of 12 blocks of
+// tokens took 200 us, ten times their products).
+constexpr int kJoinRows = 8;
+template <bool kWgrad, bool kWide>
+__global__ __launch_bounds__(256) void blk_join_kernel(const BlkKArgs p, int G) {
+  __shared__ BlkSched sched;
+  constexpr int kTN = kWide ? 128 : 256;
+  const int nM_w = (int)((p.N + kBM - 1) / kBM);
+  build_blk_sched<kWgrad>(sched, p, nM_w);
+  const BlkSplit sp = blk_split(sched.tile[p.E], G, sched.most, p);
+  const int tile = sp.full + (int)blockIdx.x;
+  if (sp.S < 2 || tile >= sched.tile[p.E]) return;
+  const int e = blk_find(sched, p.E, tile), units = sched.units[e];
+  int mt, nt;
+  tile_coords(tile - sched.tile[e], kWgrad ? nM_w : (units + kBM - 1) / kBM, p.nN, mt, nt);
+  const int row0 = kWgrad ? mt * kBM : sched.off[e] + mt * kBM;
+  const int mrows = min(kBM, kWgrad ? (int)p.N - row0 : units - mt * kBM);
+  const int64_t ncols = kWgrad ? p.K : p.N;
+  constexpr int kT = kTN / 4;                           // threads of a row, 4 columns each
+  const int c = (int)(threadIdx.x % kT) * 4;
+  const int64_t col = (int64_t)nt * kTN + c;
+  if (col >= ncols) return;
+  const int64_t slot = (int64_t)p.part_rows * kTN;
+  const float* src = p.part + (int64_t)blockIdx.x * sp.S * slot + c;
+  const int end = min(mrows, (int)(blockIdx.y + 1) * kJoinRows);
+  for (int m = blockIdx.y * kJoinRows + threadIdx.x / kT; m < end; m += 256 / kT) {
+    f32x4v a = {0.f, 0.f, 0.f, 0.f};
+    const float* q = src + (int64_t)m * kTN;
+    int i = 0;
+    for (; i + 8 <= sp.S; i += 8, q += 8 * slot) {
+      f32x4v v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = *reinterpret_cast<const f32x4v*>(q + u * slot);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) a += v[u];
+    }
+    for (; i < sp.S; ++i, q += slot) a += *reinterpret_cast<const f32x4v*>(q);
+    const int64_t o = ((kWgrad ? (int64_t)e * p.N : 0) + row0 + m) * ncols + col;
+    if constexpr (kWide) *reinterpret_cast<f32x4v*>(reinterpret_cast<float*>(p.out) + o) = a;
+    else *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(p.out) + o) = u32x2{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3])};
+  }
+}
+
+// Blocks per part of a split tile, at least.  A part writes its rows' fp32 sums and reads them back once:
+// a full tile's 256 rows take about as long as 10 blocks' products, a few rows next to nothing.  (18
+// blocks: 64 and 62 us at 2000 rows x 1024 x 8192 and for the gradients of 20000 tokens, 512 x 1024; 10: 54 and
+// 45; unsplit 105 and 89.)
+int min_units(int64_t rows) { return 2 + (int)(rows < kBM ? rows : kBM) / 32; }
+
 }  // namespace
+
+size_t block_gemm_part_bytes(bool wgrad, bool out_f32, int64_t rows, int64_t N, int64_t K) {
+  const int64_t prow = wgrad ? N : rows, most = (wgrad ? rows : K) / 128;
+  if (most < 2 * min_units(prow)) return 0;
+  return (size_t)kGemmGrid * (size_t)(prow < kBM ? prow : kBM) * (out_f32 ? 128 : 256) * sizeof(float);
+}
 
 hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t st) {
   BlkKArgs k{};
@@ -470,13 +585,21 @@ hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t st) {
   k.E = g.E;
   const int tn = g.out_f32 ? 128 : 256;
   k.nN = (int)(((g.wgrad ? g.K : g.N) + tn - 1) / tn);
-  if (g.wgrad) {
-    if (g.out_f32) blk_gemm_kernel<true, true><<<kGemmGrid, kBlkThreads, 0, st>>>(k);
-    else blk_gemm_kernel<true, false><<<kGemmGrid, kBlkThreads, 0, st>>>(k);
-  } else {
-    if (g.out_f32) blk_gemm_kernel<false, true><<<kGemmGrid, kBlkThreads, 0, st>>>(k);
-    else blk_gemm_kernel<false, false><<<kGemmGrid, kBlkThreads, 0, st>>>(k);
-  }
+  const int64_t prow = g.wgrad ? g.N : g.rows, most = (g.wgrad ? g.rows : g.K) / 128;
+  k.part_rows = (int)(prow < kBM ? prow : kBM);
+  k.min_units = min_units(prow);
+  const bool split = g.part && most >= 2 * k.min_units;
+  k.part = split ? g.part : nullptr;
+  auto launch = [&](auto wg, auto wide) {
+    constexpr bool kWg = decltype(wg)::value, kWd = decltype(wide)::value;
+    blk_gemm_kernel<kWg, kWd><<<kGemmGrid, kBlkThreads, 0, st>>>(k);
+    // a split tile has at least two parts, so there are at most kGemmGrid / 2 of them
+    if (split) blk_join_kernel<kWg, kWd><<<dim3(kGemmGrid / 2, (k.part_rows + kJoinRows - 1) / kJoinRows), 256, 0, st>>>(k, kGemmGrid);
+  };
+  if (g.wgrad && g.out_f32) launch(std::true_type{}, std::true_type{});
+  else if (g.wgrad) launch(std::true_type{}, std::false_type{});
+  else if (g.out_f32) launch(std::false_type{}, std::true_type{});
+  else launch(std::false_type{}, std::false_type{});
   return hipGetLastError();
 }
 

@@ -213,7 +213,10 @@ struct BlockGemm {
   int64_t rows, N, K;        // weight gradient: rows is the padded token axis
   int E;
   bool wgrad, out_f32;
+  float* part;               // block_gemm_part_bytes of scratch, or null: no tile is split
 };
+// Scratch of the split tiles' parts (0: the sizes never split).
+size_t block_gemm_part_bytes(bool wgrad, bool out_f32, int64_t rows, int64_t N, int64_t K);
 hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t st);
 
 }  // namespace moe

@@ -78,9 +78,9 @@ def test_fp8_block_weights_validation(lib):
 
 
 def test_fp8_block_products_validation(lib):
-    inv, uns, _ = _codes()
+    inv, uns, wsp = _codes()
     f = lib.fp8_block_grouped_gemm
-    good = [P, P, P, P, P, 8, 128, 128, 2, 1, P, None]
+    good = [P, P, P, P, P, 8, 128, 128, 2, 1, P, P, 1 << 30, None]
     for at, val, code in ((0, None, inv), (4, None, inv), (5, 0, inv), (8, 0, inv), (8, 257, inv), (9, 2, inv),
                           (10, None, inv), (7, 192, uns), (6, 136, uns), (0, P + 8, uns), (10, P + 8, uns),
                           (5, 1 << 31, uns), (6, 1 << 23, uns), (7, 1 << 24, uns)):
@@ -93,6 +93,21 @@ def test_fp8_block_products_validation(lib):
         a = list(good)
         a[at] = val
         assert f(*a) == code, (at, val)
+
+
+def test_fp8_block_products_workspace(lib):
+    inv, uns, wsp = _codes()
+    for f, size in ((lib.fp8_block_grouped_gemm, lib.fp8_block_grouped_gemm_workspace),
+                    (lib.fp8_block_grouped_wgrad, lib.fp8_block_grouped_wgrad_workspace)):
+        assert size(0, 128, 128, 1) == 0 and size(8, 128, 128, 2) == 0
+        n = size(8192, 512, 8192, 1)
+        assert n > 0
+        a = [P, P, P, P, P, 8192, 512, 8192, 2, 1, P, P, n - 1, None]
+        assert f(*a) == wsp
+        a[11], a[12] = None, n
+        assert f(*a) == wsp
+        a[11] = P + 4
+        assert f(*a) == uns
 
 
 def test_binding_refuses_tensors_off_the_gpu():

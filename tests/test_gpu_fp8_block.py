@@ -128,6 +128,11 @@ GEMM = [
     ("one-block", [300, 129], 128, 128),
     ("tall", [2000, 1, 700], 528, 640),
     ("experts-70", [3] * 40 + [0] * 10 + [60] * 20, 144, 256),
+    # long K: tiles split along it, few rows (parts of 3 blocks or more) and full tiles (18 or more)
+    ("split-few-rows", [3, 0, 9], 400, 8192),
+    ("split-one-row", [0, 0, 1], 48, 4224),
+    ("split-full-tiles", [600, 0, 40], 400, 5120),
+    ("split-last-round", [256, 200, 0, 256], 256 * 23, 4736),
 ]
 
 
@@ -216,7 +221,8 @@ def test_dgrad_is_the_product_with_transposed_weights():
 
 WGRAD = [("tiny", [1], 16, 16), ("ragged", [0, 1, 127, 0, 129, 300, 0], 144, 272), ("blocks", [256, 128], 256, 128),
          ("wide", [700, 50], 528, 400), ("experts-70", [3] * 40 + [0] * 10 + [60] * 20, 48, 80),
-         ("none", [0, 0, 4], 32, 32)]
+         ("none", [0, 0, 4], 32, 32), ("split-tokens", [5000, 10, 0, 900], 48, 80),
+         ("split-full-tiles", [6000, 1], 272, 400)]
 
 
 @gpu
