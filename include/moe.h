@@ -266,8 +266,9 @@ moe_status moe_route_permute(const void* logits, int logits_dtype, const void* x
  * +inf make the token's probabilities and both losses NaN.  Ids are always in
  * range.
  * 1 <= k <= min(E, 16), E <= 256.  workspace: at least
- * moe_route_balance_workspace(T, E) bytes (device, caller-owned; nothing in
- * it is read before it is written, nothing is kept from call to call).
+ * moe_route_balance_workspace(T, E) bytes (device, 16-byte aligned, caller-
+ * owned; nothing in it is read before it is written, nothing is kept from call
+ * to call).
  * ------------------------------------------------------------------------ */
 size_t moe_route_balance_workspace(int64_t T, int E);
 moe_status moe_route_balance(const void* logits, int logits_dtype, const uint8_t* token_mask, int64_t T, int E,

@@ -199,7 +199,26 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    # the handle itself: building torch's stream object first takes 1.9 us of a small call's 15
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device.index is None else device.index)
+
+
+class _Device:
+    """`with _Device(device):` makes it the current one, like torch.cuda.device; nothing is done (and
+    little spent) where it is already."""
+
+    __slots__ = ("other",)
+
+    def __init__(self, device: torch.device):
+        self.other = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.other is not None:
+            self.other.__enter__()
+
+    def __exit__(self, *args):
+        if self.other is not None:
+            self.other.__exit__(*args)
 
 
 def _io(t: torch.Tensor) -> int:
@@ -448,7 +467,7 @@ def _on(t: torch.Tensor, what: str) -> torch.device:
 
 def _shape(t: Optional[torch.Tensor], shape, dtype: torch.dtype, device: torch.device, what: str) -> None:
     """Raise unless t (if given) is a contiguous `dtype` tensor of `shape` on `device`."""
-    if t is None:
+    if t is None or (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
         return
     _need(t, dtype, device, what)
     if tuple(t.shape) != tuple(shape):
@@ -486,7 +505,7 @@ def moe_route_balance(logits: torch.Tensor, k: int, token_mask: Optional[torch.T
     dev = _on(logits, "logits")
     T, E = logits.shape
     _mask(token_mask, T, dev)
-    with torch.cuda.device(dev):
+    with _Device(dev):
         idx = torch.empty((T, k), dtype=torch.int32, device=dev)
         prob = torch.empty((T, k), dtype=torch.float32, device=dev)
         counts = torch.empty(E, dtype=torch.int32, device=dev)
@@ -516,7 +535,7 @@ def moe_route_balance_bwd(logits: torch.Tensor, topk_idx: torch.Tensor, topk_pro
     _shape(dprob, (T, k), torch.float32, dev, "dprob")
     _shape(dlosses, (2,), torch.float32, dev, "dlosses")
     _mask(token_mask, T, dev)
-    with torch.cuda.device(dev):
+    with _Device(dev):
         dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
         _check(lib.moe_route_balance_bwd(_ptr(logits), _io(logits), _ptr(token_mask), T, E, k, _ptr(topk_idx),
                                          _ptr(topk_prob), _ptr(counts), _ptr(dprob), _ptr(dlosses), _ptr(dlogits),
@@ -541,7 +560,7 @@ def fp8_block_quantize(x: torch.Tensor, axis: int = 0, group_offsets: Optional[t
     if group_offsets is not None:
         G = group_offsets.numel() - 1
         _shape(group_offsets, (G + 1,), torch.int32, dev, "group_offsets")
-    with torch.cuda.device(dev):
+    with _Device(dev):
         if axis == 0:
             q = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
             s = torch.empty((cols // 128, rows), dtype=torch.float32, device=dev)
@@ -572,7 +591,7 @@ def fp8_block_quantize_weights(w, transposed: bool = False, skip: Optional[torch
     _shape(skip, (E,), torch.int32, dev, "skip")
     n, kd = (cols, rows) if transposed else (rows, cols)
     make = torch.zeros if skip is not None else torch.empty
-    with torch.cuda.device(dev):
+    with _Device(dev):
         q = make((E, n, kd), dtype=torch.uint8, device=dev)
         s = make((E, (n + 127) // 128, kd // 128), dtype=torch.float32, device=dev)
         _check(lib.fp8_block_quantize_weights(tab, E, rows, cols, int(transposed), _ptr(skip), _ptr(q), _ptr(s),
@@ -598,7 +617,7 @@ def fp8_block_grouped_gemm(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Ten
     _shape(w, (E, N, K), torch.uint8, dev, "w")
     _shape(w_scales, (E, (N + 127) // 128, K // 128), torch.float32, dev, "w_scales")
     _shape(offsets, (E + 1,), torch.int32, dev, "offsets")
-    with torch.cuda.device(dev):
+    with _Device(dev):
         if out is None:
             out = torch.empty((R, N), dtype=out_dtype, device=dev)
         else:
@@ -627,7 +646,7 @@ def fp8_block_grouped_wgrad(dyt: torch.Tensor, dyt_scales: torch.Tensor, xt: tor
     _shape(xt_scales, (rp // 128, K), torch.float32, dev, "xt_scales")
     E = offsets.numel() - 1
     _shape(offsets, (E + 1,), torch.int32, dev, "offsets")
-    with torch.cuda.device(dev):
+    with _Device(dev):
         if out is None:
             out = torch.empty((max(E, 0), N, K), dtype=out_dtype, device=dev)
         else:

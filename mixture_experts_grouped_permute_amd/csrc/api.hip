@@ -584,12 +584,16 @@ namespace {
 struct BalanceWs {
   float* psum;
   int32_t* cnt;
+  double* prod;
+  int* arrived;
 };
 BalanceWs carve_balance(Carver& c, int64_t T, int E) {
   const size_t n = (size_t)balance_blocks(T, E) * (size_t)(E + 1);
   BalanceWs w;
   w.psum = reinterpret_cast<float*>(c.take(n * sizeof(float)));
   w.cnt = reinterpret_cast<int32_t*>(c.take(n * sizeof(int32_t)));
+  w.prod = reinterpret_cast<double*>(c.take(kBalanceFinish * sizeof(double)));
+  w.arrived = reinterpret_cast<int*>(c.take(sizeof(int)));
   return w;
 }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -610,10 +614,11 @@ moe_status moe_route_balance(const void* logits, int logits_dtype, const uint8_t
   if (s != MOE_OK) return s;
   MOE_CHECK(logits && io_ok(logits_dtype) && topk_idx && topk_prob && counts && losses, MOE_ERR_INVALID_ARG);
   MOE_CHECK(workspace && workspace_bytes >= moe_route_balance_workspace(T, E), MOE_ERR_WORKSPACE);
+  MOE_CHECK(aligned16(workspace), MOE_ERR_UNSUPPORTED);
   Carver c(workspace);
   const BalanceWs w = carve_balance(c, T, E);
   HIP_TRY(launch_route_balance(logits, logits_dtype == MOE_F32, token_mask, T, E, k, topk_idx, topk_prob, counts,
-                               losses, w.psum, w.cnt, reinterpret_cast<hipStream_t>(stream)));
+                               losses, w.psum, w.cnt, w.prod, w.arrived, reinterpret_cast<hipStream_t>(stream)));
   return MOE_OK;
 }
 

@@ -82,8 +82,17 @@ struct Key<true> {
   static __device__ __forceinline__ float value(double k) {
     return (float)__builtin_bit_cast(double, __builtin_bit_cast(uint64_t, k) & ~(uint64_t)255);
   }
-  static __device__ __forceinline__ double hi(double a, double b) { return fmax(a, b); }
-  static __device__ __forceinline__ double lo(double a, double b) { return fmin(a, b); }
+  // (keys are never NaN: the instruction itself, without the quieting that fmax puts before it)
+  static __device__ __forceinline__ double hi(double a, double b) {
+    double r;
+    asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+  }
+  static __device__ __forceinline__ double lo(double a, double b) {
+    double r;
+    asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+  }
 };
 template <>
 struct Key<false> {
@@ -171,10 +180,31 @@ __device__ __forceinline__ void merge_lanes(typename K::type* a) {
   }
 }
 
-template <bool kF32>
-__device__ __forceinline__ float logit_at(const void* lg, int64_t o) {
-  if constexpr (kF32) return reinterpret_cast<const float*>(lg)[o];
-  else return bf16_to_f32(reinterpret_cast<const uint16_t*>(lg)[o]);
+// The lane's logits of its token, one of the kG that start at t0, -inf past the last expert.  A buffer
+// descriptor over those tokens: the lane's offset is the same for all of them, the experts' 16-lane
+// strides are immediate offsets, and a token past the last reads zeros.  (64-bit addresses per load
+// were 50 of the forward's 950 instructions a token, which bound it.)
+template <bool kF32, int L, int kN, int kG>
+__device__ __forceinline__ void load_row(const void* lg, int64_t t0, int64_t T, int E, int grp, int sub,
+                                         float (&v)[kN]) {
+  constexpr int kB = kF32 ? 4 : 2;
+  const int64_t left = T - t0;
+  const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<char*>(reinterpret_cast<const char*>(lg)) + t0 * E * kB, (short)0,
+      (int)(left < kG ? left : kG) * E * kB, 0x00020000);
+  const uint32_t at = (uint32_t)(grp * E + sub) * kB;
+#pragma unroll
+  for (int c = 0; c < kN; ++c) {
+    if constexpr (kF32) {
+      const uint32_t u = __builtin_amdgcn_raw_buffer_load_b32(r, at + c * L * kB, 0, 0);
+      v[c] = __builtin_bit_cast(float, u);
+    } else {
+      v[c] = bf16_to_f32(__builtin_amdgcn_raw_buffer_load_b16(r, at + c * L * kB, 0, 0));
+    }
+  }
+  // E > L kN / 2 (kN > 1): the first half of the chunks is whole
+#pragma unroll
+  for (int c = kN / 2; c < kN; ++c) v[c] = sub + L * c < E ? v[c] : -__builtin_huge_valf();
 }
 
 constexpr int kThreads = kBalanceThreads;
@@ -190,66 +220,99 @@ struct FwdP {
   float* losses;
   float* psum;       // [nb][E] sums of p, then [nb] sums of lse^2
   int32_t* cnt;      // [nb][E] counts, then [nb] tokens that count
+  double* prod;      // [kBalanceFinish] partial sums of C_e P_e
+  int* arrived;      // workgroups of the finish that are done; the first kernel clears it
 };
 
-// Totals of nb blocks' sums -> counts and both losses.  nb rows of E: thread e + 256 s adds rows s,
-// s + 4, ... of expert e, in that order; 64 bits from there on, so the losses do not feel how many
-// blocks there were.
-__device__ __forceinline__ void finish(const FwdP& p, const float* psum, const int32_t* cnt, int nb) {
-  __shared__ double rs[kThreads / 64];
-  __shared__ int64_t rn[kThreads / 64];
-  __shared__ double zs[kThreads / 64];
-  __shared__ double es[kThreads];
-  __shared__ int32_t ec[kThreads];
-  const int tid = threadIdx.x, e = tid & 255, s = tid >> 8;
-  constexpr int kS = kThreads / 256;
-  double ps = 0.0;
-  int c = 0;
-  if (e < p.E) {
-    constexpr int kU = 8;   // loads in flight
-    int b = s;
-    for (; b + (kU - 1) * kS < nb; b += kU * kS) {
-      float v[kU];
-      int w[kU];
+// Totals of nb blocks' sums -> counts and both losses, 64-bit from here on.  Workgroup f of nf takes
+// experts 16 f + [0, 16) (one workgroup reads 64 bytes a cycle: 512 KB for 256 blocks of 256 experts would
+// take 9 us), leaves sum_e C_e P_e of them in `prod`, and the one that arrives last adds those in order.
+constexpr int kFinExperts = 16, kFinThreads = 256;
+template <int kT>
+__device__ __forceinline__ void finish(const FwdP& p, int nb, int nf) {
+  constexpr int kS = kT / kFinExperts;                  // slices of the nb rows
+  __shared__ double es[kS][kFinExperts];
+  __shared__ int ec[kS][kFinExperts];
+  __shared__ double wz[kT / 64];
+  __shared__ int64_t wn[kT / 64];
+  __shared__ int s_last;
+  const int tid = threadIdx.x, le = tid % kFinExperts, s = tid / kFinExperts;
+  double total = 0.0;
+  for (int f = blockIdx.x; f * kFinExperts < p.E; f += nf) {
+    const int e = f * kFinExperts + le;
+    double ps = 0.0;
+    int c = 0;
+    if (e < p.E) {
+      constexpr int kU = 16;                            // rows in flight
+      int b = s;
+      for (; b + (kU - 1) * kS < nb; b += kU * kS) {
+        float v[kU];
+        int w[kU];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        v[u] = psum[(int64_t)(b + u * kS) * p.E + e];
-        w[u] = cnt[(int64_t)(b + u * kS) * p.E + e];
+        for (int u = 0; u < kU; ++u) {
+          v[u] = p.psum[(int64_t)(b + u * kS) * p.E + e];
+          w[u] = p.cnt[(int64_t)(b + u * kS) * p.E + e];
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) { ps += v[u]; c += w[u]; }
       }
-#pragma unroll
-      for (int u = 0; u < kU; ++u) { ps += v[u]; c += w[u]; }
+      for (; b < nb; b += kS) {
+        ps += p.psum[(int64_t)b * p.E + e];
+        c += p.cnt[(int64_t)b * p.E + e];
+      }
     }
-    for (; b < nb; b += kS) { ps += psum[(int64_t)b * p.E + e]; c += cnt[(int64_t)b * p.E + e]; }
+    es[s][le] = ps;
+    ec[s][le] = c;
+    __syncthreads();
+    for (int h = kS / 2; h >= 1; h /= 2) {
+      if (s < h) {
+        es[s][le] += es[s + h][le];
+        ec[s][le] += ec[s + h][le];
+      }
+      __syncthreads();
+    }
+    if (tid < kFinExperts) {
+      if (e < p.E) p.counts[e] = ec[0][le];
+      double q = e < p.E ? es[0][le] * (double)ec[0][le] : 0.0;
+#pragma unroll
+      for (int d = kFinExperts / 2; d >= 1; d >>= 1) q += __shfl_xor(q, d, 64);
+      total += q;
+    }
+    __syncthreads();
   }
-  es[tid] = ps;
-  ec[tid] = c;
+  if (nf > 1) {
+    if (tid == 0) {
+      // device-wide atomics, each complete before the next: no other write has to be seen
+      __hip_atomic_store(p.prod + blockIdx.x, total, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __builtin_amdgcn_s_waitcnt(0);
+      s_last = __hip_atomic_fetch_add(p.arrived, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == nf - 1;
+    }
+    __syncthreads();
+    if (!s_last) return;
+  }
   double z = 0.0;
   int64_t n = 0;
-  for (int b = tid; b < nb; b += kThreads) {
-    z += psum[(int64_t)nb * p.E + b];
-    n += cnt[(int64_t)nb * p.E + b];
-  }
-  __syncthreads();
-  double prod = 0.0;
-  if (tid < p.E) {
-    for (int q = 1; q < kS; ++q) { ps += es[tid + 256 * q]; c += ec[tid + 256 * q]; }
-    p.counts[tid] = c;
-    prod = ps * (double)c;
+  for (int b = tid; b < nb; b += kT) {
+    z += p.psum[(int64_t)nb * p.E + b];
+    n += p.cnt[(int64_t)nb * p.E + b];
   }
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) {
-    prod += __shfl_xor(prod, d, 64);
     z += __shfl_xor(z, d, 64);
     n += __shfl_xor(n, d, 64);
   }
-  if ((tid & 63) == 0) { rs[tid >> 6] = prod; zs[tid >> 6] = z; rn[tid >> 6] = n; }
+  if ((tid & 63) == 0) { wz[tid >> 6] = z; wn[tid >> 6] = n; }
   __syncthreads();
   if (tid == 0) {
-    double b = 0.0, zz = 0.0;
+    double zz = 0.0;
     int64_t nn = 0;
-    for (int w = 0; w < kThreads / 64; ++w) { b += rs[w]; zz += zs[w]; nn += rn[w]; }
-    const double dn = nn > 0 ? (double)nn : 1.0;       // nothing counts: both losses are 0
-    p.losses[0] = (float)(b * (double)p.E / ((double)p.k * dn * dn));
+    for (int w = 0; w < kT / 64; ++w) { zz += wz[w]; nn += wn[w]; }
+    if (nf > 1) {
+      total = 0.0;
+      for (int f = 0; f < nf; ++f) total += __hip_atomic_load(p.prod + f, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    const double dn = nn > 0 ? (double)nn : 1.0;        // nothing counts: both losses are 0
+    p.losses[0] = (float)(total * (double)p.E / ((double)p.k * dn * dn));
     p.losses[1] = (float)(zz / dn);
   }
 }
@@ -276,18 +339,16 @@ __global__ __launch_bounds__(kThreads) void route_balance_kernel(const FwdP p) {
   for (int64_t t0 = (int64_t)blockIdx.x * kG; t0 < p.T; t0 += (int64_t)nb * kG) {
     const int64_t t = t0 + grp;
     const bool in = t < p.T;
-    const int64_t row = (in ? t : p.T - 1) * E;         // lanes behind the last token read its row again
     float v[kN];
-#pragma unroll
-    for (int c = 0; c < kN; ++c) {
-      const int e = sub + L * c;
-      v[c] = e < E ? logit_at<kF32>(p.logits, row + e) : -__builtin_huge_valf();
-    }
-    const bool counts = in && (!p.mask || p.mask[in ? t : 0] != 0);
+    load_row<kF32, L, kN, kG>(p.logits, t0, p.T, E, grp, sub, v);
+    const bool counts = in && (!p.mask || p.mask[in ? t : p.T - 1] != 0);
     constexpr int kA = kN > kK ? kN : kK;
     typename K::type a[kA];
 #pragma unroll
-    for (int c = 0; c < kN; ++c) a[c] = sub + L * c < E ? K::make(v[c], sub + L * c) : K::none();
+    for (int c = 0; c < kN; ++c) {
+      const typename K::type key = K::make(v[c], sub + L * c);
+      a[c] = c < kN / 2 || sub + L * c < E ? key : K::none();
+    }
     sort_top<K, kN, kK>(a);
     constexpr int kM = kN < kK ? kN : kK;
     merge_lanes<K, L, kM, kK, 0>(a);
@@ -352,12 +413,14 @@ __global__ __launch_bounds__(kThreads) void route_balance_kernel(const FwdP p) {
   }
   if (nb == 1) {
     __syncthreads();                                    // (a block sees its own global writes)
-    finish(p, p.psum, p.cnt, 1);
+    finish<kThreads>(p, 1, 1);
+  } else if (blockIdx.x == 0 && tid == 0) {
+    *p.arrived = 0;
   }
 }
 
-__global__ __launch_bounds__(kThreads) void route_balance_finish_kernel(const FwdP p, int nb) {
-  finish(p, p.psum, p.cnt, nb);
+__global__ __launch_bounds__(kFinThreads) void route_balance_finish_kernel(const FwdP p, int nb) {
+  finish<kFinThreads>(p, nb, (int)gridDim.x);
 }
 
 template <bool kF32, int L, int kN>
@@ -424,13 +487,9 @@ __global__ __launch_bounds__(kBwdThreads) void route_balance_bwd_kernel(const Bw
   for (int64_t t0 = (int64_t)blockIdx.x * kG; t0 < p.T; t0 += (int64_t)gridDim.x * kG) {
     const int64_t t = t0 + grp;
     const bool in = t < p.T;
-    const int64_t tr = in ? t : p.T - 1;                // lanes behind the last token read its row again
+    const int64_t tr = in ? t : p.T - 1;
     float v[kN], m = -__builtin_huge_valf();
-#pragma unroll
-    for (int c = 0; c < kN; ++c) {
-      const int e = sub + L * c;
-      v[c] = e < E ? logit_at<kF32>(p.logits, tr * E + e) : -__builtin_huge_valf();
-    }
+    load_row<kF32, L, kN, kG>(p.logits, t0, p.T, E, grp, sub, v);
     int e_sel = -1;
     float w = 0.f, g = 0.f;
     if (p.dprob && in && sub < k) {
@@ -501,12 +560,12 @@ int balance_blocks(int64_t T, int E) {
 
 hipError_t launch_route_balance(const void* logits, bool f32, const uint8_t* mask, int64_t T, int E, int k,
                                 int32_t* idx, float* prob, int32_t* counts, float* losses, float* psum, int32_t* cnt,
-                                hipStream_t st) {
-  const FwdP p{logits, mask, T, E, k, idx, prob, counts, losses, psum, cnt};
+                                double* prod, int* arrived, hipStream_t st) {
+  const FwdP p{logits, mask, T, E, k, idx, prob, counts, losses, psum, cnt, prod, arrived};
   const int nb = balance_blocks(T, E);
   if (f32) launch_fwd<true>(p, nb, st);
   else launch_fwd<false>(p, nb, st);
-  if (nb > 1) route_balance_finish_kernel<<<1, kThreads, 0, st>>>(p, nb);
+  if (nb > 1) route_balance_finish_kernel<<<(E + kFinExperts - 1) / kFinExperts, kFinThreads, 0, st>>>(p, nb);
   return hipGetLastError();
 }
 

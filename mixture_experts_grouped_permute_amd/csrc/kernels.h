@@ -175,13 +175,14 @@ hipError_t launch_scale_tail_zero(uint8_t* scales, int64_t rows, int64_t ld, con
 int bwd_dprob_parts(int64_t I);
 
 // ---- router with its losses (balance.hip).  psum: balance_blocks(T, E) x (E + 1) floats, cnt: as many
-// int32.  mask (optional): bytes, 0 = the token does not count.
+// int32, prod: kBalanceFinish doubles, arrived: one int.  mask (optional): bytes, 0 = the token does not count.
 constexpr int kBalanceThreads = 1024;
 constexpr int kBalanceMaxBlocks = 256;
+constexpr int kBalanceFinish = 16;
 int balance_blocks(int64_t T, int E);
 hipError_t launch_route_balance(const void* logits, bool f32, const uint8_t* mask, int64_t T, int E, int k,
                                 int32_t* idx, float* prob, int32_t* counts, float* losses, float* psum, int32_t* cnt,
-                                hipStream_t st);
+                                double* prod, int* arrived, hipStream_t st);
 hipError_t launch_route_balance_bwd(const void* logits, bool f32, const uint8_t* mask, int64_t T, int E, int k,
                                     const int32_t* idx, const float* prob, const int32_t* counts, const float* dprob,
                                     const float* dlosses, void* dlogits, hipStream_t st);
