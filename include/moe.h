@@ -60,7 +60,8 @@ typedef enum {
   MOE_F32 = 0,
   MOE_BF16 = 1,
   MOE_MXFP8_E4M3 = 2,       /* E4M3FN bytes + E8M0 scale bytes, one per 32 values */
-  MOE_FP8_E4M3 = 3          /* E4M3FN bytes + one fp32 scale per tensor (forward only) */
+  MOE_FP8_E4M3 = 3,         /* E4M3FN bytes + one fp32 scale per tensor (forward only) */
+  MOE_FP8_BLOCK = 4         /* E4M3FN bytes + one fp32 scale per 1 x 128 (weights: 128 x 128) block */
 } moe_dtype;
 
 /* Largest supported expert count and experts per token. */
@@ -426,8 +427,12 @@ moe_status fp8_block_grouped_wgrad(const uint8_t* dyt, const float* dyt_scales, 
  * first, since its scale needs the amax of the expert's whole h); it is
  * forward only (saved_* must be NULL, else MOE_ERR_UNSUPPORTED) and is not
  * offered by moe_grouped_mlp_fwd_loop.
+ * MOE_FP8_BLOCK quantizes X_perm and h as fp8_block_quantize does (axis 0, X
+ * from its own dtype) and the weights as fp8_block_quantize_weights, and runs
+ * fp8_block_grouped_gemm; the gate-up output is rounded to bf16 ahead of the
+ * SwiGLU.  Forward and backward; not offered by moe_grouped_mlp_fwd_loop.
  * Alignment: H % 64 == 0 and I % 64 == 0 (BF16); H % 128 == 0 and
- * I % 128 == 0 (MXFP8, FP8).  Any token counts per expert, including zero.
+ * I % 128 == 0 (MXFP8, FP8, FP8_BLOCK).  Any token counts per expert, including zero.
  * Permutation outputs are always written (caller buffers, device).
  * saved_*: optional (all NULL for inference, all set for training): bf16
  * copies kept for the backward -- x_perm [R, H], gu [R, 2I] (gate-up
@@ -441,8 +446,10 @@ moe_status fp8_block_grouped_wgrad(const uint8_t* dyt, const float* dyt_scales, 
  * w1q, w1_scale, w2q, w2_scale: the same for MOE_FP8_E4M3 (all four or none;
  * w1s / w2s then NULL): fp8_tensor_quantize of every W1_e and W2_e as one
  * tensor each, stacked -- w1q [E, 2I, H] and w2q [E, H, I] codes, w1_scale
- * and w2_scale [E] fp32 scales s, device (ABI version 3).  Any other mix of
- * the six cached-weight fields is MOE_ERR_INVALID_ARG.
+ * and w2_scale [E] fp32 scales s, device (ABI version 3); and for
+ * MOE_FP8_BLOCK, the same fields with w1_scale [E, 2I/128, H/128] and w2_scale
+ * [E, H/128, I/128].  Any other mix of the six cached-weight fields is
+ * MOE_ERR_INVALID_ARG.
  * error_flag: optional device int32 that receives the permutation's flag for
  * out-of-range expert ids (0 or 1) instead of the first 4 bytes of the
  * workspace, so that it stays readable after later calls reuse the workspace
@@ -470,7 +477,7 @@ moe_status fp8_block_grouped_wgrad(const uint8_t* dyt, const float* dyt_scales, 
 typedef struct {
   int64_t T, H, I;
   int32_t E, k;
-  int32_t compute;              /* moe_dtype: MOE_BF16, MOE_MXFP8_E4M3 or MOE_FP8_E4M3 */
+  int32_t compute;              /* moe_dtype: MOE_BF16, MOE_MXFP8_E4M3, MOE_FP8_E4M3 or MOE_FP8_BLOCK */
   int32_t io_dtype;             /* moe_dtype: MOE_F32 or MOE_BF16 */
   const void* x;                /* [T, H] */
   const int32_t* topk_idx;      /* [T, k] */
@@ -540,10 +547,13 @@ const char* moe_fwd_phase_name(int i);   /* NULL when out of range */
  *   dW2_e = dz_e^T . h_e ;  dW1_e = dgu_e^T . x_perm_e  (variable-K wgrad; zero-token experts get 0)
  *   dx_perm = dgu . W1_e (rounded to io_dtype);  dx[t] = sum_j dx_perm[row_id_map[t*k+j]]
  *   dprob[t, j] = dprob_perm[row_id_map[t*k+j]]
+ * Under FP8_BLOCK too, with dz, dh and dgu rounded to bf16 (dh between its
+ * product and the SwiGLU backward); w1tq..w2ts are then the codes and fp32
+ * scales of fp8_block_quantize_weights(transposed) (the scale pointers cast).
  * Under MXFP8 every GEMM operand is quantized along that GEMM's own K
  * (token-axis blocks restart per expert).  dw1/dw2 are overwritten.
  * g, u, h and x_perm are the bf16 tensors saved by the forward.
- * w1tq, w1ts, w2tq, w2ts: optional (MXFP8 only; all four or none, else
+ * w1tq, w1ts, w2tq, w2ts: optional (MXFP8, FP8_BLOCK; all four or none, else
  * MOE_ERR_INVALID_ARG): the transposed weights of the dgrad GEMMs quantized
  * once by the caller -- mxfp8_quantize_weights(w1, E, 2I, H, axis 1) and
  * mxfp8_quantize_weights(w2, E, H, I, axis 1).  Without them the backward

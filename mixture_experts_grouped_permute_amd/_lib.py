@@ -18,7 +18,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(5)
-MOE_F32, MOE_BF16, MOE_MXFP8_E4M3, MOE_FP8_E4M3 = 0, 1, 2, 3
+MOE_F32, MOE_BF16, MOE_MXFP8_E4M3, MOE_FP8_E4M3, MOE_FP8_BLOCK = 0, 1, 2, 3, 4
 MAX_EXPERTS = 256
 
 # every symbol include/moe.h declares
@@ -230,7 +230,7 @@ def _io(t: torch.Tensor) -> int:
 
 
 def _compute(c: str) -> int:
-    return {"bf16": MOE_BF16, "mxfp8": MOE_MXFP8_E4M3, "fp8": MOE_FP8_E4M3}[c]
+    return {"bf16": MOE_BF16, "mxfp8": MOE_MXFP8_E4M3, "fp8": MOE_FP8_E4M3, "fp8_block": MOE_FP8_BLOCK}[c]
 
 
 def _need(t: Optional[torch.Tensor], dtype: torch.dtype, device: torch.device, what: str) -> None:
@@ -716,7 +716,12 @@ def quantize_weights(w1, w2, compute: str = "mxfp8", transposed: bool = False):
     "mxfp8", transposed=True: the backward's dgrad operands, (w1tq [E,H,2I], w1ts [E,H,2I/32],
     w2tq [E,I,H], w2ts [E,I,H/32]) (axis 1).
     "fp8": (w1q [E,2I,H], w1_scale [E], w2q [E,H,I], w2_scale [E]), each expert's matrix one
-    tensor of fp8_tensor_quantize."""
+    tensor of fp8_tensor_quantize.
+    "fp8_block": (w1q [E,2I,H], w1_scale [E,2I/128,H/128], w2q [E,H,I], w2_scale [E,H/128,I/128]) of
+    fp8_block_quantize_weights; transposed=True: (w1tq [E,H,2I], w1ts [E,H/128,2I/128], w2tq [E,I,H],
+    w2ts [E,I/128,H/128])."""
+    if compute == "fp8_block":
+        return (*fp8_block_quantize_weights(w1, transposed), *fp8_block_quantize_weights(w2, transposed))
     if compute == "fp8":
         if transposed:
             raise ValueError("the per-tensor FP8 variant is forward only")
@@ -738,9 +743,9 @@ def moe_grouped_mlp_fwd(x: torch.Tensor, topk_idx: torch.Tensor, topk_prob: torc
                         compute: str = "bf16", save_for_backward: bool = False, workspace: Optional[torch.Tensor] = None,
                         w_quant=None, debug_h: bool = False, quantize_for_backward: Optional[bool] = None):
     """Grouped expert MLP forward.  w1: [E,2I,H] tensor or E tensors [2I,H] (bf16);
-    w2: [E,H,I] or E tensors [H,I].  compute: "bf16", "mxfp8" or "fp8" (per-tensor scales,
-    forward only).  w_quant: optional quantize_weights(w1, w2, compute) output ("mxfp8" or
-    "fp8"): the per-call weight quantization is skipped.
+    w2: [E,H,I] or E tensors [H,I].  compute: "bf16", "mxfp8", "fp8_block" (one fp32 scale per 128
+    values) or "fp8" (per-tensor scales, forward only).  w_quant: optional
+    quantize_weights(w1, w2, compute) output (not for "bf16"): the per-call weight quantization is skipped.
     quantize_for_backward (MXFP8 with save_for_backward and per-call weight quantization; the
     default there): the same read of the bf16 weights also quantizes them along the backward's K,
     into ctx["w_quant_t"], which moe_grouped_mlp_bwd then uses.
@@ -790,7 +795,7 @@ def moe_grouped_mlp_fwd(x: torch.Tensor, topk_idx: torch.Tensor, topk_prob: torc
         for t in w_quant:
             if t.device != dev:
                 raise TypeError(f"cached weights must be on {dev}")
-        if compute == "fp8":
+        if compute in ("fp8", "fp8_block"):
             a.w1q, a.w1_scale, a.w2q, a.w2_scale = (_ptr(t) for t in w_quant)
         else:
             a.w1q, a.w1s, a.w2q, a.w2s = (_ptr(t) for t in w_quant)
@@ -866,8 +871,10 @@ def _bwd_args(dy: torch.Tensor, ctx: dict, w1, w2, dw_dtype=torch.float32, w_qua
     if w_quant_t is None:
         w_quant_t = ctx.get("w_quant_t")   # quantized by the forward, if it was asked to
     if w_quant_t is not None:
-        for t in w_quant_t:
-            _need(t, torch.uint8, dev, "cached transposed weights")
+        # codes and E8M0 bytes, or (fp8_block) codes and fp32 scales
+        sd = torch.float32 if ctx["compute"] == "fp8_block" else torch.uint8
+        for t, dt in zip(w_quant_t, (torch.uint8, sd, torch.uint8, sd)):
+            _need(t, dt, dev, "cached transposed weights")
         a.w1tq, a.w1ts, a.w2tq, a.w2ts = (_ptr(t) for t in w_quant_t)
     return a, (dx, dprob, dw1, dw2), (w1t, w2t, dw1t, dw2t, w1k, w2k, w_quant_t)
 
@@ -875,8 +882,8 @@ def _bwd_args(dy: torch.Tensor, ctx: dict, w1, w2, dw_dtype=torch.float32, w_qua
 def moe_grouped_mlp_bwd(dy: torch.Tensor, ctx: dict, w1, w2, dw_dtype=torch.float32,
                         workspace: Optional[torch.Tensor] = None, w_quant_t=None, debug: Optional[dict] = None):
     """Backward of moe_grouped_mlp_fwd (needs save_for_backward=True).
-    w_quant_t: optional quantize_weights(w1, w2, "mxfp8", transposed=True) output (MXFP8): the
-    per-call quantization of the transposed weights is skipped.
+    w_quant_t: optional quantize_weights(w1, w2, compute, transposed=True) output ("mxfp8",
+    "fp8_block"): the per-call quantization of the transposed weights is skipped.
     debug: optional dict (MXFP8): filled with the FC2 dgrad epilogue's dgu in bf16 ("dgu_bf16"
     [R, 2I]) and its two quantizations ("dgu_codes", "dgu_scales" row-wise; "dgu_t_codes",
     "dgu_t_scales" along tokens, [2I, rows_pad] with rows_pad = ceil(R/128)*128 + 128 E rounded up to

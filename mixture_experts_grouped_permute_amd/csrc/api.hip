@@ -79,6 +79,8 @@ struct FwdPlan {
   // (X_perm rows, W1, h rows, W2), amax partials, and the 0x7F block scales the GEMMs read
   void* x_bf; void* h_bf;
   float *sx, *sw1, *sh, *sw2;
+  float *xs, *hs, *w1s_f, *w2s_f;   // block-scaled FP8: scales of X_perm, h, W1, W2
+  void* gu;                         // block-scaled FP8: [R, 2I] bf16 gate-up output
   float* pt_part;
   uint32_t* h_amax;    // per expert max |bf16 h| (float bits), raised by FC1's epilogue
   uint8_t* unit;
@@ -93,7 +95,25 @@ FwdPlan plan_fwd(const moe_mlp_fwd_args* a, void* ws) {
   const int E = a->E;
   const bool mx = a->compute == MOE_MXFP8_E4M3;
   p.perm = carve_perm(c, a->T, E);
-  if (a->compute == MOE_FP8_E4M3) {
+  if (a->compute == MOE_FP8_BLOCK) {
+    auto f = [&](int64_t n) { return reinterpret_cast<float*>(c.take((size_t)n * sizeof(float))); };
+    p.x_op = c.take((size_t)(R * H));
+    p.xs = f(H / 128 * R);
+    p.gu = a->saved_gu ? a->saved_gu : c.take((size_t)(R * 2 * I * 2));
+    p.h_op = c.take((size_t)(R * I));
+    p.hs = f(I / 128 * R);
+    if (a->w1q) {   // codes and block scales cached by the caller
+      p.w1q = const_cast<uint8_t*>(a->w1q);
+      p.w2q = const_cast<uint8_t*>(a->w2q);
+      p.w1s_f = const_cast<float*>(a->w1_scale);
+      p.w2s_f = const_cast<float*>(a->w2_scale);
+    } else {
+      p.w1q = reinterpret_cast<uint8_t*>(c.take((size_t)(E * 2 * I * H)));
+      p.w1s_f = f((int64_t)E * (2 * I / 128) * (H / 128));
+      p.w2q = reinterpret_cast<uint8_t*>(c.take((size_t)(E * H * I)));
+      p.w2s_f = f((int64_t)E * (H / 128) * (I / 128));
+    }
+  } else if (a->compute == MOE_FP8_E4M3) {
     auto f = [&](size_t n) { return reinterpret_cast<float*>(c.take(n * sizeof(float))); };
     p.x_bf = c.take((size_t)(R * H * 2));
     p.x_op = c.take((size_t)(R * H));
@@ -153,13 +173,21 @@ FwdPlan plan_fwd(const moe_mlp_fwd_args* a, void* ws) {
   return p;
 }
 
+// 32-bit buffer ranges of the block-scaled products over R rows: the row scales of an operand
+// [R, K], K <= max(H, 2I), and 256 rows of a [R, 2I] output or operand
+bool block_sizes_ok(int64_t R, int64_t H, int64_t I) {
+  const int64_t K = H > 2 * I ? H : 2 * I;
+  return K / 128 * R * 4 < (int64_t)UINT32_MAX && 256 * K * 4 < (int64_t)UINT32_MAX;
+}
+
 moe_status validate_fwd(const moe_mlp_fwd_args* a) {
   if (!a) return MOE_ERR_INVALID_ARG;
   moe_status s = check_common(a->T, a->H, a->E, a->k);
   if (s != MOE_OK) return s;
   if (a->I <= 0) return MOE_ERR_INVALID_ARG;
   if (!io_ok(a->io_dtype)) return MOE_ERR_INVALID_ARG;
-  if (a->compute != MOE_BF16 && a->compute != MOE_MXFP8_E4M3 && a->compute != MOE_FP8_E4M3)
+  if (a->compute != MOE_BF16 && a->compute != MOE_MXFP8_E4M3 && a->compute != MOE_FP8_E4M3 &&
+      a->compute != MOE_FP8_BLOCK)
     return MOE_ERR_INVALID_ARG;
   const int64_t align = a->compute == MOE_BF16 ? 64 : 128;
   if (a->H % align || a->I % align) return MOE_ERR_UNSUPPORTED;
@@ -170,12 +198,12 @@ moe_status validate_fwd(const moe_mlp_fwd_args* a) {
   if (!a->w1q)
     for (int e = 0; e < a->E; ++e)
       if (!a->w1[e] || !a->w2[e]) return MOE_ERR_INVALID_ARG;
-  // cached weights: MXFP8 codes with E8M0 scales (w1s, w2s), or per-tensor FP8 codes with fp32
-  // scales (w1_scale, w2_scale) -- all four of the precision's fields, or none of the six
+  // cached weights: MXFP8 codes with E8M0 scales (w1s, w2s), or per-tensor or block-scaled FP8 codes with
+  // fp32 scales (w1_scale, w2_scale) -- all four of the precision's fields, or none of the six
   const bool any_q = a->w1q || a->w1s || a->w2q || a->w2s || a->w1_scale || a->w2_scale;
   const bool mx_q = a->w1q && a->w1s && a->w2q && a->w2s && !a->w1_scale && !a->w2_scale;
   const bool f8_q = a->w1q && a->w2q && a->w1_scale && a->w2_scale && !a->w1s && !a->w2s;
-  if (any_q && !((mx_q && a->compute == MOE_MXFP8_E4M3) || (f8_q && a->compute == MOE_FP8_E4M3)))
+  if (any_q && !((mx_q && a->compute == MOE_MXFP8_E4M3) || (f8_q && (a->compute == MOE_FP8_E4M3 || a->compute == MOE_FP8_BLOCK))))
     return MOE_ERR_INVALID_ARG;
   const bool any_saved = a->saved_x_perm || a->saved_gu || a->saved_h;
   const bool all_saved = a->saved_x_perm && a->saved_gu && a->saved_h;
@@ -190,6 +218,7 @@ moe_status validate_fwd(const moe_mlp_fwd_args* a) {
   // activation or one expert's weight matrix, so the limit is on an expert's weights (in bf16),
   // not on the number of tokens
   if (2 * a->I * a->H * 2 >= (int64_t)UINT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (a->compute == MOE_FP8_BLOCK && !block_sizes_ok(a->T * a->k, a->H, a->I)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -203,6 +232,11 @@ struct BwdPlan {
   uint8_t *dzq, *dzs, *w2tq, *w2ts, *dzT, *dzTs, *hT, *hTs;
   uint8_t *dguq, *dgus, *w1tq, *w1ts, *dguT, *dguTs, *xT, *xTs;
   int64_t rows_pad;
+  // block-scaled FP8: the scales of dz, dz^T, h^T, dGU, dGU^T, X^T, W2^T, W1^T, the bf16 dh, and the experts'
+  // outputs as device tables
+  float *dzs_f, *dzTs_f, *hTs_f, *dgus_f, *dguTs_f, *xTs_f, *w2ts_f, *w1ts_f;
+  uint16_t* dh;
+  void **tab1, **tab2;
   size_t bytes;
 };
 
@@ -218,6 +252,30 @@ BwdPlan plan_bwd(const moe_mlp_bwd_args* a, void* ws) {
   p.dprob_part = reinterpret_cast<float*>(c.take((size_t)(R * bwd_dprob_parts(I) * 4)));
   p.dx_perm = c.take((size_t)(R * H) * io_size(a->io_dtype));
   p.part = reinterpret_cast<float*>(c.take(kFc2PartBytes));
+  if (a->compute == MOE_FP8_BLOCK) {
+    const int64_t Rp = block_rows_pad(R, E);
+    p.rows_pad = Rp;
+    auto take8 = [&](int64_t n) { return reinterpret_cast<uint8_t*>(c.take((size_t)n)); };
+    auto f = [&](int64_t n) { return reinterpret_cast<float*>(c.take((size_t)n * sizeof(float))); };
+    p.dzq = take8(R * H); p.dzs_f = f(H / 128 * R);
+    p.dh = reinterpret_cast<uint16_t*>(c.take((size_t)(R * I * 2)));
+    p.dzT = take8(H * Rp); p.dzTs_f = f(Rp / 128 * H);
+    p.hT = take8(I * Rp); p.hTs_f = f(Rp / 128 * I);
+    p.dguq = take8(R * 2 * I); p.dgus_f = f(2 * I / 128 * R);
+    p.dguT = take8(2 * I * Rp); p.dguTs_f = f(Rp / 128 * 2 * I);
+    p.xT = take8(H * Rp); p.xTs_f = f(Rp / 128 * H);
+    if (a->w2tq) {
+      p.w2tq = const_cast<uint8_t*>(a->w2tq);
+      p.w2ts_f = const_cast<float*>(reinterpret_cast<const float*>(a->w2ts));
+      p.w1tq = const_cast<uint8_t*>(a->w1tq);
+      p.w1ts_f = const_cast<float*>(reinterpret_cast<const float*>(a->w1ts));
+    } else {
+      p.w2tq = take8((int64_t)E * I * H); p.w2ts_f = f((int64_t)E * (I / 128) * (H / 128));
+      p.w1tq = take8((int64_t)E * H * 2 * I); p.w1ts_f = f((int64_t)E * (H / 128) * (2 * I / 128));
+    }
+    p.tab1 = reinterpret_cast<void**>(c.take(sizeof(void*) * (size_t)E));
+    p.tab2 = reinterpret_cast<void**>(c.take(sizeof(void*) * (size_t)E));
+  }
   if (mx) {
     // the token-padded layout's rows: every segment padded to 128 tokens, the row length to 512
     // (whole 16-byte E8M0 groups per row for the weight gradients' scale loads)
@@ -260,7 +318,7 @@ moe_status validate_bwd(const moe_mlp_bwd_args* a) {
   if (a->I <= 0) return MOE_ERR_INVALID_ARG;
   if (!io_ok(a->io_dtype) || !io_ok(a->dw_dtype)) return MOE_ERR_INVALID_ARG;
   if (a->compute == MOE_FP8_E4M3) return MOE_ERR_UNSUPPORTED;   // the per-tensor FP8 variant is forward only
-  if (a->compute != MOE_BF16 && a->compute != MOE_MXFP8_E4M3) return MOE_ERR_INVALID_ARG;
+  if (a->compute != MOE_BF16 && a->compute != MOE_MXFP8_E4M3 && a->compute != MOE_FP8_BLOCK) return MOE_ERR_INVALID_ARG;
   const int64_t align = a->compute == MOE_BF16 ? 64 : 128;
   if (a->H % align || a->I % align) return MOE_ERR_UNSUPPORTED;
   if (!a->dy || !a->w1 || !a->w2 || !a->dx || !a->dprob || !a->dw1 || !a->dw2) return MOE_ERR_INVALID_ARG;
@@ -268,7 +326,7 @@ moe_status validate_bwd(const moe_mlp_bwd_args* a) {
   if (!a->saved_x_perm || !a->saved_gu || !a->saved_h) return MOE_ERR_INVALID_ARG;
   const bool any_wt = a->w1tq || a->w1ts || a->w2tq || a->w2ts;
   const bool all_wt = a->w1tq && a->w1ts && a->w2tq && a->w2ts;
-  if (any_wt && (!all_wt || a->compute != MOE_MXFP8_E4M3)) return MOE_ERR_INVALID_ARG;
+  if (any_wt && (!all_wt || a->compute == MOE_BF16)) return MOE_ERR_INVALID_ARG;
   const bool any_dbg = a->dgu_bf16 || a->dgu_codes || a->dgu_scales || a->dgu_t_codes || a->dgu_t_scales;
   const bool all_dbg = a->dgu_bf16 && a->dgu_codes && a->dgu_scales && a->dgu_t_codes && a->dgu_t_scales;
   if (any_dbg && (!all_dbg || a->compute != MOE_MXFP8_E4M3)) return MOE_ERR_INVALID_ARG;
@@ -282,6 +340,10 @@ moe_status validate_bwd(const moe_mlp_bwd_args* a) {
   if (a->compute == MOE_MXFP8_E4M3) {
     const int64_t Rp = (R + 127) / 128 * 128 + 128 * (int64_t)a->E;
     if (256 * Rp >= (int64_t)UINT32_MAX) return MOE_ERR_UNSUPPORTED;
+  }
+  if (a->compute == MOE_FP8_BLOCK) {
+    const int64_t Rp = block_rows_pad(R, a->E);
+    if (!block_sizes_ok(Rp, a->H, a->I) || 256 * Rp >= (int64_t)UINT32_MAX) return MOE_ERR_UNSUPPORTED;
   }
   return MOE_OK;
 }
@@ -352,6 +414,90 @@ moe_status fwd_fp8_tail(const moe_mlp_fwd_args* a, const FwdPlan& p, hipStream_t
 
   HIP_TRY(launch_combine(p.z, x_f32, T, H, k, a->row_id_map, a->out, x_f32, st));
   MOE_CHECK(mark(7), MOE_ERR_HIP);
+  return MOE_OK;
+}
+
+// Block-scaled FP8 forward after the index pass: x quantized row by row into expert order (1 x 128
+// blocks), the weights (128 x 128), the gate-up product in bf16, ScaledSwiGLU with the quantization of h, the
+// down product, combine.
+template <typename Mark>
+moe_status fwd_block_tail(const moe_mlp_fwd_args* a, const FwdPlan& p, hipStream_t st, Mark& mark) {
+  const int64_t T = a->T, H = a->H, I = a->I, R = T * a->k;
+  const int E = a->E, k = a->k;
+  const bool x_f32 = a->io_dtype == MOE_F32;
+  const int32_t* live = a->offsets + E;                // rows that have an expert
+  uint8_t* xq = reinterpret_cast<uint8_t*>(p.x_op);
+  uint8_t* hq = reinterpret_cast<uint8_t*>(p.h_op);
+  HIP_TRY(launch_block_rows(a->x, x_f32, R, H, a->src_index, k, live, xq, p.xs, st));
+  if (a->saved_x_perm)
+    HIP_TRY(launch_permute_rows(a->x, x_f32, T, H, k, a->row_id_map, a->saved_x_perm, nullptr, false, st));
+  MOE_CHECK(mark(2), MOE_ERR_HIP);
+  if (!a->w1q) HIP_TRY(launch_block_weights(reinterpret_cast<const void* const*>(a->w1), E, 2 * I, H, false, a->split_sizes, p.w1q, p.w1s_f, st));
+  MOE_CHECK(mark(3), MOE_ERR_HIP);
+  if (!a->w1q) HIP_TRY(launch_block_weights(reinterpret_cast<const void* const*>(a->w2), E, H, I, false, a->split_sizes, p.w2q, p.w2s_f, st));
+  MOE_CHECK(mark(4), MOE_ERR_HIP);
+  const BlockGemm g1{xq, p.xs, p.w1q, p.w1s_f, a->offsets, p.gu, R, 2 * I, H, E, false, false, p.part};
+  HIP_TRY(launch_block_gemm(g1, st));
+  HIP_TRY(launch_swiglu_block(p.gu, a->prob_perm, live, R, I, hq, p.hs, a->saved_h, a->h_f32, st));
+  MOE_CHECK(mark(5), MOE_ERR_HIP);
+  const BlockGemm g2{hq, p.hs, p.w2q, p.w2s_f, a->offsets, p.z, R, H, I, E, false, x_f32, p.part};
+  HIP_TRY(launch_block_gemm(g2, st));
+  MOE_CHECK(mark(6), MOE_ERR_HIP);
+  HIP_TRY(launch_combine(p.z, x_f32, T, H, k, a->row_id_map, a->out, x_f32, st));
+  MOE_CHECK(mark(7), MOE_ERR_HIP);
+  return MOE_OK;
+}
+
+// Block-scaled FP8 backward: every product's operands quantized along that product's K -- dz along H and W2^T
+// for dh, dz and h along tokens for dW2, dGU along 2I and W1^T for dX_perm, dGU and X_perm along tokens for
+// dW1 -- with dz, dh and dGU in bf16 in between.
+template <typename Mark>
+moe_status bwd_block(const moe_mlp_bwd_args* a, const BwdPlan& p, hipStream_t st, Mark& mark) {
+  const int64_t T = a->T, H = a->H, I = a->I, R = T * a->k, Rp = p.rows_pad;
+  const int E = a->E, k = a->k;
+  const bool io_f32 = a->io_dtype == MOE_F32, dw_f32 = a->dw_dtype == MOE_F32;
+  const int32_t* live = a->offsets + E;
+  const void* const* w1 = reinterpret_cast<const void* const*>(a->w1);
+  const void* const* w2 = reinterpret_cast<const void* const*>(a->w2);
+  // dz = bf16(dy) in expert order; bf16 dy is quantized through src_index, fp32 dy is gathered first
+  const void* dz = a->dy;
+  const int32_t* src = a->src_index;
+  MOE_CHECK(mark(0), MOE_ERR_HIP);
+  if (io_f32) {
+    HIP_TRY(launch_gather_rows(a->dy, true, R, H, k, a->src_index, a->offsets, E, p.dz, st));
+    dz = p.dz;
+    src = nullptr;
+  }
+  HIP_TRY(launch_pointer_table(a->dw1, E, p.tab1, st));
+  HIP_TRY(launch_pointer_table(a->dw2, E, p.tab2, st));
+  MOE_CHECK(mark(1), MOE_ERR_HIP);
+  HIP_TRY(launch_block_rows(dz, false, R, H, src, k, live, p.dzq, p.dzs_f, st));
+  if (!a->w2tq) HIP_TRY(launch_block_weights(w2, E, H, I, true, a->split_sizes, p.w2tq, p.w2ts_f, st));
+  MOE_CHECK(mark(2), MOE_ERR_HIP);
+  const BlockGemm d2{p.dzq, p.dzs_f, p.w2tq, p.w2ts_f, a->offsets, p.dh, R, I, H, E, false, false, p.part};
+  HIP_TRY(launch_block_gemm(d2, st));
+  HIP_TRY(launch_swiglu_block_bwd(p.dh, a->saved_gu, a->prob_perm, live, R, I, p.dgu, p.dguq, p.dgus_f, p.dprob_part, st));
+  MOE_CHECK(mark(3), MOE_ERR_HIP);
+  HIP_TRY(launch_block_tokens(dz, false, R, H, a->offsets, E, Rp, src, k, p.dzT, p.dzTs_f, st));
+  HIP_TRY(launch_block_tokens(a->saved_h, false, R, I, a->offsets, E, Rp, nullptr, 1, p.hT, p.hTs_f, st));
+  MOE_CHECK(mark(4), MOE_ERR_HIP);
+  const BlockGemm w2g{p.dzT, p.dzTs_f, p.hT, p.hTs_f, a->offsets, nullptr, Rp, H, I, E, true, dw_f32, p.part, p.tab2};
+  HIP_TRY(launch_block_gemm(w2g, st));
+  MOE_CHECK(mark(5), MOE_ERR_HIP);
+  if (!a->w1tq) HIP_TRY(launch_block_weights(w1, E, 2 * I, H, true, a->split_sizes, p.w1tq, p.w1ts_f, st));
+  MOE_CHECK(mark(6), MOE_ERR_HIP);
+  const BlockGemm d1{p.dguq, p.dgus_f, p.w1tq, p.w1ts_f, a->offsets, p.dx_perm, R, H, 2 * I, E, false, io_f32, p.part};
+  HIP_TRY(launch_block_gemm(d1, st));
+  MOE_CHECK(mark(7), MOE_ERR_HIP);
+  HIP_TRY(launch_block_tokens(p.dgu, false, R, 2 * I, a->offsets, E, Rp, nullptr, 1, p.dguT, p.dguTs_f, st));
+  HIP_TRY(launch_block_tokens(a->saved_x_perm, false, R, H, a->offsets, E, Rp, nullptr, 1, p.xT, p.xTs_f, st));
+  MOE_CHECK(mark(8), MOE_ERR_HIP);
+  const BlockGemm w1g{p.dguT, p.dguTs_f, p.xT, p.xTs_f, a->offsets, nullptr, Rp, 2 * I, H, E, true, dw_f32, p.part, p.tab1};
+  HIP_TRY(launch_block_gemm(w1g, st));
+  MOE_CHECK(mark(9), MOE_ERR_HIP);
+  HIP_TRY(launch_combine(p.dx_perm, io_f32, T, H, k, a->row_id_map, a->dx, io_f32, st));
+  HIP_TRY(launch_dprob_reduce(p.dprob_part, R, 1, a->row_id_map, T, k, a->dprob, st));
+  MOE_CHECK(mark(10), MOE_ERR_HIP);
   return MOE_OK;
 }
 
@@ -644,7 +790,7 @@ moe_status fp8_block_quantize(const void* x, int x_dtype, int64_t rows, int64_t 
   const bool f32 = x_dtype == MOE_F32;
   if (axis == 0) {
     MOE_CHECK(cols % 128 == 0, MOE_ERR_UNSUPPORTED);
-    HIP_TRY(launch_block_rows(x, f32, rows, cols, nullptr, 1, q, scales, st));
+    HIP_TRY(launch_block_rows(x, f32, rows, cols, nullptr, 1, nullptr, q, scales, st));
     return MOE_OK;
   }
   MOE_CHECK(num_groups >= 1 && num_groups <= MOE_MAX_EXPERTS, MOE_ERR_INVALID_ARG);
@@ -760,6 +906,7 @@ moe_status moe_grouped_mlp_fwd_ex(const moe_mlp_fwd_args* a, void* stream, void*
                                  st));
   MOE_CHECK(mark(1), MOE_ERR_HIP);
   if (a->compute == MOE_FP8_E4M3) return fwd_fp8_tail(a, p, st, mark);
+  if (a->compute == MOE_FP8_BLOCK) return fwd_block_tail(a, p, st, mark);
   if (mx) {
     HIP_TRY(launch_permute_rows(a->x, x_f32, T, H, k, a->row_id_map, p.x_op, p.x_sc, true, st));
     if (a->saved_x_perm)
@@ -833,7 +980,7 @@ moe_status moe_grouped_mlp_fwd_loop(const moe_mlp_fwd_args* a, const int32_t* sp
   moe_status s = validate_fwd(a);
   if (s != MOE_OK) return s;
   MOE_CHECK(split_sizes_host != nullptr, MOE_ERR_INVALID_ARG);
-  MOE_CHECK(a->compute != MOE_FP8_E4M3, MOE_ERR_UNSUPPORTED);
+  MOE_CHECK(a->compute != MOE_FP8_E4M3 && a->compute != MOE_FP8_BLOCK, MOE_ERR_UNSUPPORTED);
   MOE_CHECK(!a->w1tq_out, MOE_ERR_UNSUPPORTED);   // the baseline quantizes the forward's copy only
   int64_t sum = 0;
   for (int e = 0; e < a->E; ++e) {
@@ -942,6 +1089,8 @@ moe_status moe_grouped_mlp_bwd_ex(const moe_mlp_bwd_args* a, void* stream, void*
   auto mark = [&](int i) -> bool {
     return !events || hipEventRecord(reinterpret_cast<hipEvent_t>(events[i]), st) == hipSuccess;
   };
+
+  if (a->compute == MOE_FP8_BLOCK) return bwd_block(a, p, st, mark);
 
   // dz = bf16(dy) gathered into expert order.  MXFP8 with bf16 dy needs dz only as the two
   // quantized operands, which are made from dy directly (below): no gather.

@@ -1,40 +1,13 @@
 // FP8 quantization with one fp32 scale per block of 128 for gfx950: rows (1 x 128), tokens (128 x 1,
 // transposed) and weights (128 x 128).
 //
-// A block's scale is d = amax / 448, its codes E4M3(v * (448 / amax)) rounded to nearest even, so the
-// largest magnitude takes the largest code.  Both quotients are fp32 divisions rounded to nearest and
-// kept to normal numbers (d >= 2^-126, factor <= 2^126: a smaller amax uses fewer of the codes); a
-// block of zeros has d = 1.  The amax is taken on the bit patterns, whose order is that of the
-// magnitudes with infinity and NaN on top: a block that holds either gets a scale that makes all of
-// its values infinite or NaN instead of hiding them.
-//
-// One read of x and one write of the codes bound all three.
+// The rule of a block's scale and codes is block_scale.h's.  One read of x and one write of the codes bound all three.
 #include "common.h"
 #include "kernels.h"
+#include "block_scale.h"
 
 namespace moe {
 namespace {
-
-struct Scale {
-  float factor, d;
-};
-// amax as bits of a non-negative float
-__device__ __forceinline__ Scale block_scale(uint32_t amax_bits) {
-  const float amax = __builtin_bit_cast(float, amax_bits);
-  if (amax_bits == 0) return {1.0f, 1.0f};
-  const float f = 448.0f / amax, d = amax / 448.0f;
-  return {f > 0x1p126f ? 0x1p126f : f, d < 0x1p-126f ? 0x1p-126f : d};   // (a NaN passes)
-}
-
-// codes of a and b times f in the low (hi == false) or high half of old.  |v f| <= 448 (1 + 2^-22),
-// which rounds to 448, so nothing has to be clamped.
-template <bool hi>
-__device__ __forceinline__ uint32_t codes2(float a, float b, float f, uint32_t old) {
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a * f, b * f, (int)old, hi);
-}
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float f) {
-  return codes2<true>(c, d, f, codes2<false>(a, b, f, 0u));
-}
 
 // 8 values of a row as loaded: bf16 in 4 words, fp32 in 8.
 template <bool kF32>
@@ -61,8 +34,6 @@ struct Raw8 {
   __device__ __forceinline__ uint32_t mag(int i) const { return __builtin_bit_cast(uint32_t, at(i)) & 0x7FFFFFFFu; }
 };
 
-__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
-
 // ---- rows.  A wave takes 4 blocks (512 columns) of kRowsPerWave rows, 16 lanes per block: all its
 // loads are in flight at once, and a load covers 1 KB (bf16) of one row.  The scales leave block-major
 // ([cols / 128, rows], the layout a product's stages read), so the workgroup gathers those of its
@@ -73,22 +44,20 @@ constexpr int kRowTile = 4 * kRowsPerWave;
 template <bool kF32>
 __global__ __launch_bounds__(256) void block_rows_kernel(const void* __restrict__ x, int64_t rows, int64_t cols,
                                                            const int32_t* __restrict__ src_index, int src_k,
-                                                           uint8_t* __restrict__ q, float* __restrict__ scales) {
+                                                           const int32_t* live, uint8_t* __restrict__ q,
+                                                           float* __restrict__ scales) {
   __shared__ float sc[4][kRowTile];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t r0 = (int64_t)blockIdx.x * kRowTile;
+  const int64_t r0 = (int64_t)blockIdx.x * kRowTile, n = live ? min((int64_t)*live, rows) : rows;
+  if (r0 >= n) return;
   const int64_t col = (int64_t)blockIdx.y * 512 + lane * 8;
   const bool in_c = col < cols;                          // uniform over the 16 lanes of a block
   Raw8<kF32> v[kRowsPerWave];
 #pragma unroll
   for (int i = 0; i < kRowsPerWave; ++i) {
     const int64_t r = r0 + wave * kRowsPerWave + i;
-    const bool ok = in_c && r < rows;
-    int64_t src = ok ? r : 0;
-    if (src_index) {
-      const int s = src_index[src];
-      src = s < 0 ? 0 : s / src_k;
-    }
+    int64_t src = r < n ? r : 0;
+    if (src_index) src = src_index[src] / src_k;
     v[i].load(x, src * cols + (in_c ? col : 0));
   }
 #pragma unroll
@@ -97,13 +66,9 @@ __global__ __launch_bounds__(256) void block_rows_kernel(const void* __restrict_
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) m = umax(m, v[i].mag(j));
-    m = umax(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, true));    // lanes ^ 1
-    m = umax(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xF, 0xF, true));    // lanes ^ 2
-    m = umax(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x141, 0xF, 0xF, true));   // mirror of 8
-    m = umax(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x140, 0xF, 0xF, true));   // mirror of 16
-    const Scale s = block_scale(m);
+    const BlockScale s = block_scale(max16(m));
     if ((lane & 15) == 0) sc[lane >> 4][wave * kRowsPerWave + i] = s.d;
-    if (in_c && r < rows) {
+    if (in_c && r < n) {
       u32x2 o;
       o[0] = codes4(v[i].at(0), v[i].at(1), v[i].at(2), v[i].at(3), s.factor);
       o[1] = codes4(v[i].at(4), v[i].at(5), v[i].at(6), v[i].at(7), s.factor);
@@ -114,7 +79,7 @@ __global__ __launch_bounds__(256) void block_rows_kernel(const void* __restrict_
   if (tid < 4 * kRowTile) {
     const int b = tid / kRowTile, rr = tid % kRowTile;
     const int64_t kb = (int64_t)blockIdx.y * 4 + b;
-    if (kb < cols / 128 && r0 + rr < rows) scales[kb * rows + r0 + rr] = sc[b][rr];
+    if (kb < cols / 128 && r0 + rr < n) scales[kb * rows + r0 + rr] = sc[b][rr];
   }
 }
 
@@ -272,7 +237,7 @@ __global__ __launch_bounds__(256) void block_tile_kernel(const TileP p, const WT
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < 16; ++i) m = umax(m, s_max[i][tid]);
-        const Scale s = block_scale(m);
+        const BlockScale s = block_scale(m);
         s_f[tid] = s.factor;
         if (c0 + tid < p.cols) p.scales[(int64_t)blockIdx.x * p.cols + c0 + tid] = s.d;
       }
@@ -290,7 +255,7 @@ __global__ __launch_bounds__(256) void block_tile_kernel(const TileP p, const WT
       if (lane == 0) s_max[wave][0] = m;
       __syncthreads();
       m = umax(umax(s_max[0][0], s_max[1][0]), umax(s_max[2][0], s_max[3][0]));
-      const Scale s = block_scale(m);
+      const BlockScale s = block_scale(m);
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = s.factor;
       const int64_t nb = (p.rows + 127) / 128, kb = (p.cols + 127) / 128;
@@ -337,10 +302,10 @@ __global__ __launch_bounds__(256) void block_tile_kernel(const TileP p, const WT
 }  // namespace
 
 hipError_t launch_block_rows(const void* x, bool x_f32, int64_t rows, int64_t cols, const int32_t* src_index, int src_k,
-                             uint8_t* q, float* scales, hipStream_t st) {
+                             const int32_t* live, uint8_t* q, float* scales, hipStream_t st) {
   const dim3 grid((unsigned)((rows + kRowTile - 1) / kRowTile), (unsigned)((cols + 511) / 512));
-  if (x_f32) block_rows_kernel<true><<<grid, 256, 0, st>>>(x, rows, cols, src_index, src_k, q, scales);
-  else block_rows_kernel<false><<<grid, 256, 0, st>>>(x, rows, cols, src_index, src_k, q, scales);
+  if (x_f32) block_rows_kernel<true><<<grid, 256, 0, st>>>(x, rows, cols, src_index, src_k, live, q, scales);
+  else block_rows_kernel<false><<<grid, 256, 0, st>>>(x, rows, cols, src_index, src_k, live, q, scales);
   return hipGetLastError();
 }
 

@@ -38,6 +38,7 @@ struct BlkKArgs {
   const float* b_s;
   const int32_t* offsets;
   uint8_t* out;
+  void* const* tab;  // weight gradient: the experts' outputs, in place of out, or null
   int64_t rows;      // product: R; weight gradient: rows_pad (the token axis' length)
   int64_t N, K;      // outputs per row, and product: the contracted length / weight gradient: columns
   int E, nN;
@@ -132,6 +133,13 @@ __device__ __forceinline__ int blk_find(const BlkSched& s, int E, int t) {
     if (s.tile[mid] <= t) lo = mid; else hi = mid - 1;
   }
   return lo;
+}
+
+// Row 0 of what tiles of expert e write: the product's one output, or the expert's weight gradient.
+template <bool kWgrad>
+__device__ __forceinline__ uint8_t* blk_out(const BlkKArgs& p, int e, int esz) {
+  if (!kWgrad) return p.out;
+  return p.tab ? reinterpret_cast<uint8_t*>(p.tab[e]) : p.out + (int64_t)e * p.N * p.K * esz;
 }
 
 struct BlkItem {
@@ -453,6 +461,7 @@ void blk_gemm_kernel(const BlkKArgs p) {
     // Through the wave's LDS slot 16 rows x 128 bytes at a time, so that stores move whole lines;
     // the slot's 16-byte chunks are placed at chunk ^ (row & 7).
     const int64_t ncols = kWgrad ? K : N;
+    uint8_t* const out = blk_out<kWgrad>(p, cur.e, kWide ? 4 : 2);
     uint8_t* sl = smem + kBlkEpOff + wave * 2048;
     // (the lane is laundered, so that its addresses are not worked out ahead of the stages and kept)
     int el = lane;
@@ -474,8 +483,8 @@ void blk_gemm_kernel(const BlkKArgs p) {
     if (kWide || cur.part >= 0) {
       const bool whole = cur.part < 0;
       const uint32_t ld = whole ? (uint32_t)ncols * 4u : kTN * 4u;
-      const int64_t o0 = ((kWgrad ? (int64_t)cur.e * N : 0) + cur.row0) * ncols;
-      const rsrc_t ro = make_rsrc(whole ? reinterpret_cast<float*>(p.out) + o0
+      const int64_t o0 = (int64_t)cur.row0 * ncols;
+      const rsrc_t ro = make_rsrc(whole ? reinterpret_cast<float*>(out) + o0
                                         : p.part + (int64_t)(cur.t - sp.full) * p.part_rows * kTN,
                                   (uint32_t)cur.mrows * ld);
       const uint32_t c0 = ((whole ? (uint32_t)cur.nt * kTN : 0u) + (uint32_t)wn * 64u) * 4u;
@@ -493,8 +502,8 @@ void blk_gemm_kernel(const BlkKArgs p) {
       }
     } else {
       const uint32_t ld = (uint32_t)ncols * 2u;
-      const int64_t o0 = ((kWgrad ? (int64_t)cur.e * N : 0) + cur.row0) * ncols;
-      const rsrc_t ro = make_rsrc(reinterpret_cast<uint16_t*>(p.out) + o0, (uint32_t)cur.mrows * ld);
+      const int64_t o0 = (int64_t)cur.row0 * ncols;
+      const rsrc_t ro = make_rsrc(reinterpret_cast<uint16_t*>(out) + o0, (uint32_t)cur.mrows * ld);
       const uint32_t c0 = (uint32_t)(cur.nt * kTN + wn * 64) * 2u;
 #pragma unroll
       for (int i = 0; i < kI; ++i) {
@@ -536,6 +545,7 @@ __global__ __launch_bounds__(256) void blk_join_kernel(const BlkKArgs p, int G) 
   const int c = (int)(threadIdx.x % kT) * 4;
   const int64_t col = (int64_t)nt * kTN + c;
   if (col >= ncols) return;
+  uint8_t* const out = blk_out<kWgrad>(p, e, kWide ? 4 : 2);
   const int64_t slot = (int64_t)p.part_rows * kTN;
   const float* src = p.part + (int64_t)blockIdx.x * sp.S * slot + c;
   const int end = min(mrows, (int)(blockIdx.y + 1) * kJoinRows);
@@ -551,9 +561,9 @@ __global__ __launch_bounds__(256) void blk_join_kernel(const BlkKArgs p, int G) 
       for (int u = 0; u < 8; ++u) a += v[u];
     }
     for (; i < sp.S; ++i, q += slot) a += *reinterpret_cast<const f32x4v*>(q);
-    const int64_t o = ((kWgrad ? (int64_t)e * p.N : 0) + row0 + m) * ncols + col;
-    if constexpr (kWide) *reinterpret_cast<f32x4v*>(reinterpret_cast<float*>(p.out) + o) = a;
-    else *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(p.out) + o) = u32x2{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3])};
+    const int64_t o = (int64_t)(row0 + m) * ncols + col;
+    if constexpr (kWide) *reinterpret_cast<f32x4v*>(reinterpret_cast<float*>(out) + o) = a;
+    else *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(out) + o) = u32x2{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3])};
   }
 }
 
@@ -579,6 +589,7 @@ hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t st) {
   k.b_s = g.b_scales;
   k.offsets = g.offsets;
   k.out = reinterpret_cast<uint8_t*>(g.out);
+  k.tab = g.tab;
   k.rows = g.rows;
   k.N = g.N;
   k.K = g.K;

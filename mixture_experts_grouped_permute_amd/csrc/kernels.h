@@ -189,9 +189,10 @@ hipError_t launch_route_balance_bwd(const void* logits, bool f32, const uint8_t*
 
 // ---- FP8 with one fp32 scale per block of 128 (blockq.hip).  src_index (optional): row r is row
 // src_index[r] / src_k of x.
-// rows: codes [rows, cols], scales [cols / 128, rows]; cols % 128 == 0.
+// rows: codes [rows, cols], scales [cols / 128, rows]; cols % 128 == 0.  live (optional, device): only the
+// first *live rows are read and written.
 hipError_t launch_block_rows(const void* x, bool x_f32, int64_t rows, int64_t cols, const int32_t* src_index, int src_k,
-                             uint8_t* q, float* scales, hipStream_t st);
+                             const int32_t* live, uint8_t* q, float* scales, hipStream_t st);
 // tokens: segments padded to 128 rows, codes [cols, rows_pad], scales [rows_pad / 128, cols]; cols % 8 == 0.
 inline int64_t block_rows_pad(int64_t rows, int groups) { return (rows + 127) / 128 * 128 + 128 * (int64_t)groups; }
 hipError_t launch_block_tokens(const void* x, bool x_f32, int64_t rows, int64_t cols, const int32_t* offsets, int groups,
@@ -202,6 +203,16 @@ hipError_t launch_block_tokens(const void* x, bool x_f32, int64_t rows, int64_t 
 // rows % 128 == 0.  The other dimension % 8 == 0.
 hipError_t launch_block_weights(const void* const* w, int E, int64_t rows, int64_t cols, bool transposed,
                                 const int32_t* skip, uint8_t* q, float* scales, hipStream_t st);
+
+// ---- ScaledSwiGLU around them (swiglu_block.hip), of the first *live rows.
+// h = silu(g) u p of gu [R, 2I] bf16 -> codes [R, I], scales [I / 128, R]; save_h (bf16) and h_f32 optional.
+hipError_t launch_swiglu_block(const void* gu, const float* prob, const int32_t* live, int64_t R, int64_t I, uint8_t* q,
+                               float* scales, void* save_h, float* h_f32, hipStream_t st);
+// dh [R, I] bf16 -> dgu [R, 2I] bf16, its codes and scales [2I / 128, R], dprob [R].
+hipError_t launch_swiglu_block_bwd(const void* dh, const void* gu, const float* prob, const int32_t* live, int64_t R,
+                                   int64_t I, void* dgu, uint8_t* q, float* scales, float* dprob, hipStream_t st);
+// a host table of E pointers -> out (device)
+hipError_t launch_pointer_table(void* const* ptrs, int E, void** out, hipStream_t st);
 
 // ---- grouped products of such operands (gemm_block.hip)
 struct BlockGemm {
@@ -215,6 +226,7 @@ struct BlockGemm {
   int E;
   bool wgrad, out_f32;
   float* part;               // block_gemm_part_bytes of scratch, or null: no tile is split
+  void* const* tab = nullptr;  // weight gradient: device table of the E outputs, in place of out
 };
 // Scratch of the split tiles' parts (0: the sizes never split).
 size_t block_gemm_part_bytes(bool wgrad, bool out_f32, int64_t rows, int64_t N, int64_t K);

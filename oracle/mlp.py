@@ -27,7 +27,8 @@ Readings where the pages are silent (all listed with the design notes):
     scale: every W1_e and W2_e, and each expert's rows of X_perm and of h --
     the operands of that expert's GEMM -- with h rounded to bf16 first (the
     scale needs the amax of the whole tensor, so h exists in bf16 before it is
-    quantized); "exact" applies no rounding at all (the derivative checks).
+    quantized); "fp8_block" quantizes rows in blocks of 128 and weights in blocks
+    of 128 x 128, with the gate-up output and the backward's dh in bf16; "exact" applies no rounding at all (the derivative checks).
   * Each grouped GEMM writes its output in the layer's I/O dtype (bf16, or f32
     for f32 I/O) -- the down projection's z before the combine, the FC1 dgrad
     output before the un-permute sum; the combine sums in high precision and
@@ -41,6 +42,7 @@ from typing import Optional
 
 import numpy as np
 
+from . import block
 from . import numerics as nm
 from .permute import Permutation, permute
 
@@ -77,6 +79,8 @@ def activation_operand(x, precision: str):
         return nm.round_bf16(x)
     if precision == "mxfp8":
         return nm.fake_quant_mxfp8(x, axis=1)
+    if precision == "fp8_block":
+        return block.values_rows(*block.quantize_rows(x.astype(np.float32)))
     if precision == "fp8":          # x: the rows of one expert (one tensor)
         return nm.fake_quant_fp8_tensor(nm.round_bf16(x))
     raise ValueError(precision)
@@ -88,6 +92,8 @@ def weight_operand(w_e, precision: str, k_axis: int = 1):
         return w_e
     if precision == "fp8":
         return nm.fake_quant_fp8_tensor(w_e)
+    if precision == "fp8_block":    # 128 x 128 blocks: the same either way
+        return block.values_matrix(*block.quantize_matrix(w_e))
     return nm.fake_quant_mxfp8(w_e, axis=k_axis)
 
 
@@ -96,6 +102,8 @@ def expert_forward(xq, p, w1q, w2q, precision: str, io_dtype: str):
     w1q [2I, H], w2q [H, I]: the expert's weights as the GEMMs consume them."""
     I = w2q.shape[1]
     gu = xq @ w1q.T                                  # [M, 2I]
+    if precision == "fp8_block":                     # bf16 between the product and the SwiGLU
+        gu = nm.round_bf16(gu)
     g, u = gu[:, :I], gu[:, I:]
     h = silu(g) * u * p[:, None]
     hq = activation_operand(h, precision)
@@ -210,6 +218,9 @@ class Backward:
 def _col_operand(a, precision):
     """Operand whose K is the token axis (one expert's segment): MXFP8 blocks of
     32 rows per column, the last block zero-padded."""
+    if precision == "fp8_block":
+        off = np.array([0, a.shape[0]])
+        return block.values_tokens(*block.quantize_tokens(a, off), off)
     if precision != "mxfp8":
         return a
     M = a.shape[0]
@@ -252,10 +263,11 @@ def backward(fw: Forward, x, dy, w1, w2, experts=None) -> Backward:
     dz = dys[tok] if prec == "exact" else nm.round_bf16(dys[tok])
     rnd = (lambda v: v) if prec == "exact" else nm.round_bf16
     gu_s = rnd(fw.gu)
-    h_s = fw.h_op if prec != "mxfp8" else nm.round_bf16(fw.h)
+    quant = prec in ("mxfp8", "fp8_block")
+    h_s = fw.h_op if not quant else nm.round_bf16(fw.h)
     xs = f64(x)
     # saved X_perm is bf16 (under MXFP8 it is re-quantized along tokens for the dW1 GEMM)
-    x_s = fw.x_perm if prec != "mxfp8" else nm.round_bf16(xs[tok])
+    x_s = fw.x_perm if not quant else nm.round_bf16(xs[tok])
     dgu = np.zeros((R, 2 * I))
     dx_perm = np.zeros((R, H))
     dprob_perm = np.zeros(R)
@@ -275,9 +287,11 @@ def backward(fw: Forward, x, dy, w1, w2, experts=None) -> Backward:
             continue
         w1e, w2e = f64(w1[e]), f64(w2[e])
         dz_e = dz[lo:hi]
-        dzq = activation_operand(dz_e, prec) if prec == "mxfp8" else dz_e
+        dzq = activation_operand(dz_e, prec) if quant else dz_e
         w2q = weight_operand(w2e, prec, k_axis=0)        # K = H (rows of W2)
         dh = dzq @ w2q                                   # [M, I]
+        if prec == "fp8_block":
+            dh = nm.round_bf16(dh)
         g, u = gu_s[lo:hi, :I], gu_s[lo:hi, I:]
         s = sigmoid(g)
         sl = g * s
@@ -289,7 +303,7 @@ def backward(fw: Forward, x, dy, w1, w2, experts=None) -> Backward:
         dg = da * u * (s * (1.0 + g * (1.0 - s)))
         dgu_e = rnd(np.concatenate([dg, du], axis=1))
         dgu[lo:hi] = dgu_e
-        dguq = activation_operand(dgu_e, prec) if prec == "mxfp8" else dgu_e
+        dguq = activation_operand(dgu_e, prec) if quant else dgu_e
         w1q = weight_operand(w1e, prec, k_axis=0)        # K = 2I (rows of W1)
         dx_perm[lo:hi] = round_io(dguq @ w1q, io, prec)
         dw1[e] = _col_operand(dgu_e, prec).T @ _col_operand(x_s[lo:hi], prec)
