@@ -163,37 +163,34 @@ struct Frag;
 template <>
 struct Frag<false> {
   i32x8 v;
-  __device__ __forceinline__ void set(const i32x8& c) { v = c; }
+  __device__ __forceinline__ void set(const i32x8& r) { v = r; }
+  __device__ __forceinline__ void part(const i32x8&, int) {}
 };
 template <>
 struct Frag<true> {
   bf16x8 v[4];
-  __device__ __forceinline__ void set(const i32x8& c) {
+  __device__ __forceinline__ void set(const i32x8&) {}
+  __device__ __forceinline__ void part(const i32x8& r, int c) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const bf16x2w lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * i + w], 1.0f, false);
-        const bf16x2w hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * i + w], 1.0f, true);
-        v[i][4 * w] = lo[0];
-        v[i][4 * w + 1] = lo[1];
-        v[i][4 * w + 2] = hi[0];
-        v[i][4 * w + 3] = hi[1];
-      }
+    for (int w = 0; w < 2; ++w) {
+      const bf16x2w lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r[2 * c + w], 1.0f, false);
+      const bf16x2w hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r[2 * c + w], 1.0f, true);
+      v[c][4 * w] = lo[0];
+      v[c][4 * w + 1] = lo[1];
+      v[c][4 * w + 2] = hi[0];
+      v[c][4 * w + 3] = hi[1];
+    }
   }
 };
-// t[j] = the block's products of B fragment j and A fragment a, j < 4
-__device__ __forceinline__ void blk_mma(const Frag<false> (&b)[4], const Frag<false>& a, f32x4v (&t)[4]) {
+// Quarter q of the block's products of four B fragments and one A fragment: those of B fragment q, or
+// (bf16) those of group q of the codes.
+__device__ __forceinline__ void blk_mma(const Frag<false> (&b)[4], const Frag<false>& a, f32x4v (&t)[4], int q) {
+  t[q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[q].v, a.v, f32x4v{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ void blk_mma(const Frag<true> (&b)[4], const Frag<true>& a, f32x4v (&t)[4], int q) {
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    t[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j].v, a.v, f32x4v{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-}
-__device__ __forceinline__ void blk_mma(const Frag<true> (&b)[4], const Frag<true>& a, f32x4v (&t)[4]) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      t[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j].v[c], a.v[c], c == 0 ? f32x4v{0.f, 0.f, 0.f, 0.f} : t[j], 0, 0, 0);
+    t[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j].v[q], a.v[q], q == 0 ? f32x4v{0.f, 0.f, 0.f, 0.f} : t[j], 0, 0, 0);
 }
 
 // kWide (fp32 output): bf16 products
@@ -364,18 +361,20 @@ void blk_gemm_kernel(const BlkKArgs p) {
   issue(dc, cur.n, 1, 1, 0);
 
   // The stage being multiplied is in buffer `b`, its B fragments and first A fragment in registers.
-  // Stage schedule: the products of A fragment i are issued while the sums of fragment i - 1 are added
-  // and fragment i + 1 is read; once the last A fragment is in registers the buffer is free, and the
-  // barrier there -- after which the next stage has landed -- lets the loads of the stage after next
-  // into it and the next stage's first fragments out of the other one, both under the last products.
+  // Stage schedule: the products of A fragment i run in four quarters, behind each of which a quarter of
+  // the sums of fragment i - 1 is added (and of the conversions to bf16 done): a wave's VALU work hides
+  // behind its own matrix instructions only if it comes between them (8 instructions of 32 cycles with
+  // 32 fused multiply-adds took 292 cycles so, 384 in groups of 4 and 16).  The B rows' buffer is free
+  // once every wave holds its B fragments (the first barrier, after which the B rows of the stage after
+  // next are loaded), the A rows' once the last A fragment is in registers (the second, after which the
+  // next stage has landed and its first fragments are read under the last products).
   int b = 0;
-  Frag<kWide> fbv[4];
-  i32x8 raw;
+  i32x8 rb[4], ra;
   auto first_frags = [&](int buf) {
     const uint8_t* st = smem + buf * kStageBytes;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) fbv[j].set(frag(st, fb, j));
-    raw = frag(st, fa, 0);
+    for (int j = 0; j < 4; ++j) rb[j] = frag(st, fb, j);
+    ra = frag(st, fa, 0);
   };
   first_frags(0);
   for (int round = 0; cur.t < total; ++round) {
@@ -392,7 +391,7 @@ void blk_gemm_kernel(const BlkKArgs p) {
       const uint8_t* st = smem + b * kStageBytes;
       const float* sc = reinterpret_cast<const float*>(smem + kBlkScOff + b * kScaleBytes);
       // the stage after next, of this item or the next one, into this stage's buffer
-      auto issue_ahead = [&](int s, int ns, int part) {
+      auto issue_ahead = [&](int part) {
         const bool in = s + 2 < ns;
         Desc l;
         l.va = in ? dc.va : dn.va;
@@ -405,55 +404,75 @@ void blk_gemm_kernel(const BlkKArgs p) {
       f32x4v t[2][4];
       float sa[2], sal = 0.f;
       f32x4v sbv[kWgrad ? 4 : 1];
-      auto add = [&](int u) {
+      // a quarter of the sums of A fragment u: its products with B fragment j
+      auto add = [&](int u, int j) {
+        const float sv = u == kI - 1 ? sal : sa[u & 1];
+        if constexpr (kWgrad) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (kWgrad) {
+          for (int r = 0; r < 4; ++r) acc[u][j][r] += (sv * sbv[j][r]) * t[u & 1][j][r];
+        } else {
+          const float sw = sv * sbv[0][0];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[u][j][r] += ((u == kI - 1 ? sal : sa[u & 1]) * sbv[j][r]) * t[u & 1][j][r];
-          } else {
-            const float sv = (u == kI - 1 ? sal : sa[u & 1]) * sbv[0][0];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[u][j][r] += sv * t[u & 1][j][r];
-          }
+          for (int r = 0; r < 4; ++r) acc[u][j][r] += sw * t[u & 1][j][r];
         }
       };
+      Frag<kWide> bf[4], af[2];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        bf[j].set(rb[j]);
+        bf[j].part(rb[j], 0);
+      }
+      af[0].set(ra);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) af[0].part(ra, c);
 #pragma unroll
       for (int i = 0; i < kI; ++i) {
         if (i == kAt) {                                 // every wave holds the stage's B fragments
           barrier();
-          issue_ahead(s, ns, 1);
+          issue_ahead(1);
         }
         if (i == kI - 1) {
           wait_vmcnt<kQB>();                            // the next stage landed: all but the kQB loads above
           barrier();
         }
-        Frag<kWide> fav;
-        fav.set(raw);
-        blk_mma(fbv, fav, t[i & 1]);
-        __builtin_amdgcn_sched_barrier(0);
-        // scales: all of the stage's are read ahead of the barrier
-        if (i + 1 < kI) sa[i & 1] = sc[wm * 16 * kI + i * 16 + r16];
-        if (i + 2 == kI) sal = sc[wm * 16 * kI + (kI - 1) * 16 + r16];
-        if (i == 0) {
-          if constexpr (kWgrad) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sbv[j] = *reinterpret_cast<const f32x4v*>(sc + 256 + wn * 64 + j * 16 + g * 4);
-          } else {
-            sbv[0][0] = sc[256 + wn * 64];
+        for (int q = 0; q < 4; ++q) {
+          blk_mma(bf, af[i & 1], t[i & 1], q);
+          __builtin_amdgcn_sched_barrier(0);
+          if (q == 0) {
+            // scales: all of the stage's are read ahead of the second barrier
+            if (i + 1 < kI) {
+              ra = frag(st, fa, i + 1);
+              sa[i & 1] = sc[wm * 16 * kI + i * 16 + r16];
+            }
+            if (i + 2 == kI) sal = sc[wm * 16 * kI + (kI - 1) * 16 + r16];
+            if (i == 0) {
+              if constexpr (kWgrad) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sbv[j] = *reinterpret_cast<const f32x4v*>(sc + 256 + wn * 64 + j * 16 + g * 4);
+              } else {
+                sbv[0][0] = sc[256 + wn * 64];
+              }
+            }
+            if (i == kI - 1) issue_ahead(0);
           }
+          if (i > 0) add(i - 1, q);
+          if (i == 0 && q < 3) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) bf[j].part(rb[j], q + 1);
+          }
+          if (i + 1 < kI && q >= 2) {                   // (ra has had two quarters to arrive)
+            af[(i + 1) & 1].part(ra, 2 * (q - 2));
+            af[(i + 1) & 1].part(ra, 2 * (q - 2) + 1);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
-        if (i + 1 < kI) {
-          raw = frag(st, fa, i + 1);
-        } else {
-          issue_ahead(s, ns, 0);
-        }
-        if (i > 0) add(i - 1);
-        __builtin_amdgcn_sched_barrier(0);
+        if (i + 1 < kI) af[(i + 1) & 1].set(ra);
       }
       first_frags(b ^ 1);
       __builtin_amdgcn_sched_barrier(0);
-      add(kI - 1);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) add(kI - 1, j);
       b ^= 1;
     }
 
