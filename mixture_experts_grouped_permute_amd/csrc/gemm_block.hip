@@ -164,15 +164,14 @@ template <>
 struct Frag<false> {
   i32x8 v;
   __device__ __forceinline__ void set(const i32x8& r) { v = r; }
-  __device__ __forceinline__ void part(const i32x8&, int) {}
+  __device__ __forceinline__ void half(const i32x8&, int, int) {}
 };
 template <>
 struct Frag<true> {
   bf16x8 v[4];
   __device__ __forceinline__ void set(const i32x8&) {}
-  __device__ __forceinline__ void part(const i32x8& r, int c) {
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
+  __device__ __forceinline__ void half(const i32x8& r, int c, int w) {   // 4 codes of group c
+    {
       const bf16x2w lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r[2 * c + w], 1.0f, false);
       const bf16x2w hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r[2 * c + w], 1.0f, true);
       v[c][4 * w] = lo[0];
@@ -182,15 +181,13 @@ struct Frag<true> {
     }
   }
 };
-// Quarter q of the block's products of four B fragments and one A fragment: those of B fragment q, or
-// (bf16) those of group q of the codes.
-__device__ __forceinline__ void blk_mma(const Frag<false> (&b)[4], const Frag<false>& a, f32x4v (&t)[4], int q) {
-  t[q] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[q].v, a.v, f32x4v{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+// One matrix instruction of the block's products of B fragment j and an A fragment: all of them, or
+// (bf16) those of group c of the codes, c = 0 first.
+__device__ __forceinline__ void blk_mma(const Frag<false>& b, const Frag<false>& a, f32x4v& t, int) {
+  t = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, f32x4v{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
-__device__ __forceinline__ void blk_mma(const Frag<true> (&b)[4], const Frag<true>& a, f32x4v (&t)[4], int q) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    t[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j].v[q], a.v[q], q == 0 ? f32x4v{0.f, 0.f, 0.f, 0.f} : t[j], 0, 0, 0);
+__device__ __forceinline__ void blk_mma(const Frag<true>& b, const Frag<true>& a, f32x4v& t, int c) {
+  t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.v[c], a.v[c], c == 0 ? f32x4v{0.f, 0.f, 0.f, 0.f} : t, 0, 0, 0);
 }
 
 // kWide (fp32 output): bf16 products
@@ -404,27 +401,22 @@ void blk_gemm_kernel(const BlkKArgs p) {
       f32x4v t[2][4];
       float sa[2], sal = 0.f;
       f32x4v sbv[kWgrad ? 4 : 1];
-      // a quarter of the sums of A fragment u: its products with B fragment j
-      auto add = [&](int u, int j) {
+      // sums of A fragment u: element r of its products with B fragment j
+      auto add = [&](int u, int j, int r) {
         const float sv = u == kI - 1 ? sal : sa[u & 1];
-        if constexpr (kWgrad) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[u][j][r] += (sv * sbv[j][r]) * t[u & 1][j][r];
-        } else {
-          const float sw = sv * sbv[0][0];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[u][j][r] += sw * t[u & 1][j][r];
-        }
+        if constexpr (kWgrad) acc[u][j][r] += (sv * sbv[j][r]) * t[u & 1][j][r];
+        else acc[u][j][r] += (sv * sbv[0][0]) * t[u & 1][j][r];
       };
       Frag<kWide> bf[4], af[2];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         bf[j].set(rb[j]);
-        bf[j].part(rb[j], 0);
+        bf[j].half(rb[j], 0, 0);
+        bf[j].half(rb[j], 0, 1);
       }
       af[0].set(ra);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) af[0].part(ra, c);
+      for (int c = 0; c < 8; ++c) af[0].half(ra, c / 2, c & 1);
 #pragma unroll
       for (int i = 0; i < kI; ++i) {
         if (i == kAt) {                                 // every wave holds the stage's B fragments
@@ -435,11 +427,12 @@ void blk_gemm_kernel(const BlkKArgs p) {
           wait_vmcnt<kQB>();                            // the next stage landed: all but the kQB loads above
           barrier();
         }
+        constexpr int kM = kWide ? 16 : 4;              // matrix instructions of a fragment
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          blk_mma(bf, af[i & 1], t[i & 1], q);
+        for (int n = 0; n < kM; ++n) {
+          blk_mma(bf[n & 3], af[i & 1], t[i & 1][n & 3], n >> 2);
           __builtin_amdgcn_sched_barrier(0);
-          if (q == 0) {
+          if (n == 0) {
             // scales: all of the stage's are read ahead of the second barrier
             if (i + 1 < kI) {
               ra = frag(st, fa, i + 1);
@@ -456,14 +449,17 @@ void blk_gemm_kernel(const BlkKArgs p) {
             }
             if (i == kI - 1) issue_ahead(0);
           }
-          if (i > 0) add(i - 1, q);
-          if (i == 0 && q < 3) {
+          if constexpr (kWide) {
+            if (i > 0) add(i - 1, n >> 2, n & 3);
+            if (i == 0 && n < 12) {                     // the B fragments' next group, one fragment at a time
+              bf[n & 3].half(rb[n & 3], (n >> 2) + 1, 0);
+              bf[n & 3].half(rb[n & 3], (n >> 2) + 1, 1);
+            }
+            if (i + 1 < kI && n >= 8) af[(i + 1) & 1].half(ra, (n - 8) / 2, n & 1);   // (ra has arrived)
+          } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) bf[j].part(rb[j], q + 1);
-          }
-          if (i + 1 < kI && q >= 2) {                   // (ra has had two quarters to arrive)
-            af[(i + 1) & 1].part(ra, 2 * (q - 2));
-            af[(i + 1) & 1].part(ra, 2 * (q - 2) + 1);
+            for (int r = 0; r < 4; ++r)
+              if (i > 0) add(i - 1, n, r);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -472,7 +468,7 @@ void blk_gemm_kernel(const BlkKArgs p) {
       first_frags(b ^ 1);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) add(kI - 1, j);
+      for (int n = 0; n < 16; ++n) add(kI - 1, n >> 2, n & 3);
       b ^= 1;
     }
 
