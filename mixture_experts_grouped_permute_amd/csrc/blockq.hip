@@ -14,13 +14,15 @@ template <bool kF32>
 struct Raw8 {
   u32x4 w[kF32 ? 2 : 1];
   __device__ __forceinline__ void load(const void* x, int64_t off) {
-    if constexpr (kF32) {
-      const u32x4* s = reinterpret_cast<const u32x4*>(reinterpret_cast<const float*>(x) + off);
-      w[0] = s[0];
-      w[1] = s[1];
-    } else {
-      w[0] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(x) + off);
-    }
+    const u32x4* s = reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(x) + off * (kF32 ? 4 : 2));
+    w[0] = s[0];
+    if constexpr (kF32) w[1] = s[1];
+  }
+  // the same past the caches, for values that are read once
+  __device__ __forceinline__ void load_once(const void* x, int64_t off) {
+    const u32x4* s = reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(x) + off * (kF32 ? 4 : 2));
+    w[0] = __builtin_nontemporal_load(s);
+    if constexpr (kF32) w[1] = __builtin_nontemporal_load(s + 1);
   }
   __device__ __forceinline__ void zero() {
     w[0] = u32x4{0u, 0u, 0u, 0u};
@@ -37,8 +39,10 @@ struct Raw8 {
 // ---- rows.  A wave takes 4 blocks (512 columns) of kRowsPerWave rows, 16 lanes per block: all its
 // loads are in flight at once, and a load covers 1 KB (bf16) of one row.  The scales leave block-major
 // ([cols / 128, rows], the layout a product's stages read), so the workgroup gathers those of its
-// rows in LDS and writes them as runs of consecutive rows.
-constexpr int kRowsPerWave = 8;
+// rows in LDS and writes them as runs of consecutive rows.  Workgroups run along a row's columns first, so
+// that those in flight together cover whole rows: 51 us at 16384 x 4096 bf16 with the rows first, 34 so, 33
+// with 4 rows a wave instead of 8.
+constexpr int kRowsPerWave = 4;
 constexpr int kRowTile = 4 * kRowsPerWave;
 
 template <bool kF32>
@@ -48,9 +52,11 @@ __global__ __launch_bounds__(256) void block_rows_kernel(const void* __restrict_
                                                            float* __restrict__ scales) {
   __shared__ float sc[4][kRowTile];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t r0 = (int64_t)blockIdx.x * kRowTile, n = live ? min((int64_t)*live, rows) : rows;
+  const int nc = (int)((cols + 511) / 512);
+  const int64_t bx = blockIdx.x / nc, by = blockIdx.x % nc;
+  const int64_t r0 = bx * kRowTile, n = live ? min((int64_t)*live, rows) : rows;
   if (r0 >= n) return;
-  const int64_t col = (int64_t)blockIdx.y * 512 + lane * 8;
+  const int64_t col = by * 512 + lane * 8;
   const bool in_c = col < cols;                          // uniform over the 16 lanes of a block
   Raw8<kF32> v[kRowsPerWave];
 #pragma unroll
@@ -78,7 +84,7 @@ __global__ __launch_bounds__(256) void block_rows_kernel(const void* __restrict_
   __syncthreads();
   if (tid < 4 * kRowTile) {
     const int b = tid / kRowTile, rr = tid % kRowTile;
-    const int64_t kb = (int64_t)blockIdx.y * 4 + b;
+    const int64_t kb = by * 4 + b;
     if (kb < cols / 128 && r0 + rr < n) scales[kb * rows + r0 + rr] = sc[b][rr];
   }
 }
@@ -86,7 +92,8 @@ __global__ __launch_bounds__(256) void block_rows_kernel(const void* __restrict_
 // ---- tiles of 128 rows x 128 columns: a thread holds 8 rows x 8 columns, so that a column's 8 codes
 // are packed straight from its registers -- the transpose costs no data movement there -- and each
 // thread's 8 bytes of a column meet those of the 15 other row groups in LDS, to leave as whole
-// 128-byte lines.
+// 128-byte lines.  Loads and stores pass the caches by: 131072 x 1408 tokens 120 -> 105 us, 8 matrices of
+// 4096 x 14336 275 -> 247 (the rows' kernel, whose codes a product reads next, gains nothing by it).
 //   kTokens  blocks of 128 rows x 1 column; the rows are the padded rows of expert segments
 //   kPlain   one 128 x 128 block of a weight matrix, codes in its own layout
 //   kTrans   the same, codes transposed
@@ -194,8 +201,6 @@ __global__ __launch_bounds__(256) void block_tile_kernel(const TileP p, const WT
     }
     __syncthreads();
   }
-  const int64_t out_rows = kMode == kTokens ? p.cols : p.rows;
-  (void)out_rows;
   for (int64_t ct = blockIdx.y; ct * 128 < p.cols; ct += gridDim.y) {
     const int64_t c0 = ct * 128, col = c0 + 8 * ck;
     const bool in_c = col < p.cols;
@@ -214,7 +219,7 @@ __global__ __launch_bounds__(256) void block_tile_kernel(const TileP p, const WT
           src = p0 + 8 * g + i;
           ok[i] = in_c && src < p.rows;
         }
-        v[i].load(x, ok[i] ? src * p.cols + col : 0);
+        v[i].load_once(x, ok[i] ? src * p.cols + col : 0);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -270,7 +275,7 @@ __global__ __launch_bounds__(256) void block_tile_kernel(const TileP p, const WT
             u32x2 o;
             o[0] = codes4(v[i].at(0), v[i].at(1), v[i].at(2), v[i].at(3), s.factor);
             o[1] = codes4(v[i].at(4), v[i].at(5), v[i].at(6), v[i].at(7), s.factor);
-            *reinterpret_cast<u32x2*>(qe + r * p.cols + col) = o;
+            __builtin_nontemporal_store(o, reinterpret_cast<u32x2*>(qe + r * p.cols + col));
           }
         }
         __syncthreads();                                  // s_max is used again by the next tile
@@ -292,7 +297,8 @@ __global__ __launch_bounds__(256) void block_tile_kernel(const TileP p, const WT
         const int id = tid + 256 * it, lc = id >> 3, pc = id & 7;
         const u32x2* s2 = reinterpret_cast<const u32x2*>(stage + lc * kPitch + 16 * pc);
         const u32x2 a = s2[0], b = s2[1];
-        if (c0 + lc < p.cols) *reinterpret_cast<u32x4*>(qe + (c0 + lc) * ld + p0 + 16 * pc) = u32x4{a[0], a[1], b[0], b[1]};
+        if (c0 + lc < p.cols)
+          __builtin_nontemporal_store(u32x4{a[0], a[1], b[0], b[1]}, reinterpret_cast<u32x4*>(qe + (c0 + lc) * ld + p0 + 16 * pc));
       }
       __syncthreads();                                    // the stage and s_max are used again
     }
@@ -303,7 +309,7 @@ __global__ __launch_bounds__(256) void block_tile_kernel(const TileP p, const WT
 
 hipError_t launch_block_rows(const void* x, bool x_f32, int64_t rows, int64_t cols, const int32_t* src_index, int src_k,
                              const int32_t* live, uint8_t* q, float* scales, hipStream_t st) {
-  const dim3 grid((unsigned)((rows + kRowTile - 1) / kRowTile), (unsigned)((cols + 511) / 512));
+  const dim3 grid((unsigned)((rows + kRowTile - 1) / kRowTile * ((cols + 511) / 512)));
   if (x_f32) block_rows_kernel<true><<<grid, 256, 0, st>>>(x, rows, cols, src_index, src_k, live, q, scales);
   else block_rows_kernel<false><<<grid, 256, 0, st>>>(x, rows, cols, src_index, src_k, live, q, scales);
   return hipGetLastError();
