@@ -369,7 +369,7 @@ moe_status fp8_block_quantize_weights(const void* const* w, int E, int64_t rows,
  * 0 for some sizes, then NULL will do): fp32 sums of tiles that are split
  * along K.  Nothing is read before it is written or kept from call to call.
  * ------------------------------------------------------------------------ */
-size_t fp8_block_grouped_gemm_workspace(int64_t R, int64_t N, int64_t K, int out_dtype);
+size_t fp8_block_grouped_gemm_workspace(int64_t R, int64_t N, int64_t K, int E, int out_dtype);
 moe_status fp8_block_grouped_gemm(const uint8_t* a, const float* a_scales, const uint8_t* w, const float* w_scales,
                                   const int32_t* offsets, int64_t R, int64_t N, int64_t K, int E, int out_dtype,
                                   void* out, void* workspace, size_t workspace_bytes, void* stream);
@@ -390,7 +390,7 @@ moe_status fp8_block_grouped_gemm(const uint8_t* a, const float* a_scales, const
  * rows_pad K / 32 below 2^32.  workspace: fp8_block_grouped_wgrad_workspace
  * bytes, as above (tiles split along the tokens).
  * ------------------------------------------------------------------------ */
-size_t fp8_block_grouped_wgrad_workspace(int64_t rows_pad, int64_t N, int64_t K, int out_dtype);
+size_t fp8_block_grouped_wgrad_workspace(int64_t rows_pad, int64_t N, int64_t K, int E, int out_dtype);
 moe_status fp8_block_grouped_wgrad(const uint8_t* dyt, const float* dyt_scales, const uint8_t* xt,
                                    const float* xt_scales, const int32_t* offsets, int64_t rows_pad, int64_t N,
                                    int64_t K, int E, int out_dtype, void* dw, void* workspace,

@@ -168,7 +168,7 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     for name in ("fp8_block_grouped_gemm", "fp8_block_grouped_wgrad"):
         f = getattr(lib, name + "_workspace")
         f.restype = ctypes.c_size_t
-        f.argtypes = [_i64, _i64, _i64, ctypes.c_int]
+        f.argtypes = [_i64, _i64, _i64, ctypes.c_int, ctypes.c_int]
         f = getattr(lib, name)
         f.restype = ctypes.c_int
         f.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, _vp, _vp,
@@ -623,7 +623,7 @@ def fp8_block_grouped_gemm(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Ten
         else:
             _shape(out, (R, N), out.dtype, dev, "out")
         od = _io(out)
-        ws = _scratch(lib.fp8_block_grouped_gemm_workspace(R, N, K, od), dev)
+        ws = _scratch(lib.fp8_block_grouped_gemm_workspace(R, N, K, E, od), dev)
         _check(lib.fp8_block_grouped_gemm(_ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), _ptr(offsets), R, N, K, E,
                                           od, _ptr(out), _ptr(ws), _nbytes(ws), _stream(dev)),
                "fp8_block_grouped_gemm")
@@ -652,7 +652,7 @@ def fp8_block_grouped_wgrad(dyt: torch.Tensor, dyt_scales: torch.Tensor, xt: tor
         else:
             _shape(out, (E, N, K), out.dtype, dev, "out")
         od = _io(out)
-        ws = _scratch(lib.fp8_block_grouped_wgrad_workspace(rp, N, K, od), dev)
+        ws = _scratch(lib.fp8_block_grouped_wgrad_workspace(rp, N, K, E, od), dev)
         _check(lib.fp8_block_grouped_wgrad(_ptr(dyt), _ptr(dyt_scales), _ptr(xt), _ptr(xt_scales), _ptr(offsets), rp, N,
                                            K, E, od, _ptr(out), _ptr(ws), _nbytes(ws), _stream(dev)),
                "fp8_block_grouped_wgrad")

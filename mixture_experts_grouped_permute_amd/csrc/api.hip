@@ -88,6 +88,19 @@ struct FwdPlan {
   size_t bytes;
 };
 
+// Scratch for any of the layer's block-scaled products over R rows and weight gradients over rows_pad padded
+// tokens (0: none): either output type, each contracted length.
+size_t block_part_bytes(int64_t R, int64_t rows_pad, int64_t H, int64_t I, int E) {
+  size_t n = 0;
+  for (int f = 0; f < 2; ++f) {
+    for (const int64_t K : {H, I, 2 * I})
+      if (const size_t b = block_gemm_part_bytes(false, f != 0, R, 256, K, E); b > n) n = b;
+    for (const int64_t N : {H, 2 * I})
+      if (const size_t b = block_gemm_part_bytes(true, f != 0, rows_pad, N, 256, E); b > n) n = b;
+  }
+  return n;
+}
+
 FwdPlan plan_fwd(const moe_mlp_fwd_args* a, void* ws) {
   FwdPlan p{};
   Carver c(ws);
@@ -167,7 +180,7 @@ FwdPlan plan_fwd(const moe_mlp_fwd_args* a, void* ws) {
     else p.h_op = a->saved_h;
   }
   p.z = c.take((size_t)(R * H) * io_size(a->io_dtype));
-  p.part = reinterpret_cast<float*>(c.take(kFc2PartBytes));
+  p.part = reinterpret_cast<float*>(c.take(a->compute == MOE_FP8_BLOCK ? block_part_bytes(R, 0, H, I, E) : kFc2PartBytes));
   p.bytes = c.used;
   if (a->error_flag) p.perm.err = a->error_flag;
   return p;
@@ -251,7 +264,8 @@ BwdPlan plan_bwd(const moe_mlp_bwd_args* a, void* ws) {
   p.dgu = mx ? a->dgu_bf16 : reinterpret_cast<uint16_t*>(c.take((size_t)(R * 2 * I * 2)));
   p.dprob_part = reinterpret_cast<float*>(c.take((size_t)(R * bwd_dprob_parts(I) * 4)));
   p.dx_perm = c.take((size_t)(R * H) * io_size(a->io_dtype));
-  p.part = reinterpret_cast<float*>(c.take(kFc2PartBytes));
+  p.part = reinterpret_cast<float*>(
+      c.take(a->compute == MOE_FP8_BLOCK ? block_part_bytes(R, block_rows_pad(R, E), H, I, E) : kFc2PartBytes));
   if (a->compute == MOE_FP8_BLOCK) {
     const int64_t Rp = block_rows_pad(R, E);
     p.rows_pad = Rp;
@@ -817,14 +831,14 @@ moe_status fp8_block_quantize_weights(const void* const* w, int E, int64_t rows,
   return MOE_OK;
 }
 
-size_t fp8_block_grouped_gemm_workspace(int64_t R, int64_t N, int64_t K, int out_dtype) {
-  if (R <= 0 || N <= 0 || K <= 0 || !io_ok(out_dtype)) return 0;
-  return align_up(block_gemm_part_bytes(false, out_dtype == MOE_F32, R, N, K));
+size_t fp8_block_grouped_gemm_workspace(int64_t R, int64_t N, int64_t K, int E, int out_dtype) {
+  if (R <= 0 || N <= 0 || K <= 0 || E < 1 || E > MOE_MAX_EXPERTS || !io_ok(out_dtype)) return 0;
+  return align_up(block_gemm_part_bytes(false, out_dtype == MOE_F32, R, N, K, E));
 }
 
-size_t fp8_block_grouped_wgrad_workspace(int64_t rows_pad, int64_t N, int64_t K, int out_dtype) {
-  if (rows_pad <= 0 || N <= 0 || K <= 0 || !io_ok(out_dtype)) return 0;
-  return align_up(block_gemm_part_bytes(true, out_dtype == MOE_F32, rows_pad, N, K));
+size_t fp8_block_grouped_wgrad_workspace(int64_t rows_pad, int64_t N, int64_t K, int E, int out_dtype) {
+  if (rows_pad <= 0 || N <= 0 || K <= 0 || E < 1 || E > MOE_MAX_EXPERTS || !io_ok(out_dtype)) return 0;
+  return align_up(block_gemm_part_bytes(true, out_dtype == MOE_F32, rows_pad, N, K, E));
 }
 
 moe_status fp8_block_grouped_gemm(const uint8_t* a, const float* a_scales, const uint8_t* w, const float* w_scales,
@@ -839,7 +853,7 @@ moe_status fp8_block_grouped_gemm(const uint8_t* a, const float* a_scales, const
   MOE_CHECK(under_4g(256 * K) && under_4g(256 * N * 4) && under_4g(K / 128 * R * 4), MOE_ERR_UNSUPPORTED);
   MOE_CHECK(under_4g((N + 127) / 128 * (K / 128) * 4), MOE_ERR_UNSUPPORTED);
   MOE_CHECK((R / 256 + E) * ((N + 127) / 128) < (int64_t)INT32_MAX, MOE_ERR_UNSUPPORTED);
-  const size_t need = fp8_block_grouped_gemm_workspace(R, N, K, out_dtype);
+  const size_t need = fp8_block_grouped_gemm_workspace(R, N, K, E, out_dtype);
   MOE_CHECK(!need || (workspace && workspace_bytes >= need), MOE_ERR_WORKSPACE);
   MOE_CHECK(!need || aligned16(workspace), MOE_ERR_UNSUPPORTED);
   BlockGemm g{a, a_scales, w, w_scales, offsets, out, R, N, K, E, false, out_dtype == MOE_F32,
@@ -860,7 +874,7 @@ moe_status fp8_block_grouped_wgrad(const uint8_t* dyt, const float* dyt_scales, 
   MOE_CHECK(under_4g(256 * rows_pad) && under_4g(256 * K * 4) && under_4g(rows_pad / 128 * N * 4) &&
                 under_4g(rows_pad / 128 * K * 4), MOE_ERR_UNSUPPORTED);
   MOE_CHECK(((N + 255) / 256) * ((K + 127) / 128) * E < (int64_t)INT32_MAX, MOE_ERR_UNSUPPORTED);
-  const size_t need = fp8_block_grouped_wgrad_workspace(rows_pad, N, K, out_dtype);
+  const size_t need = fp8_block_grouped_wgrad_workspace(rows_pad, N, K, E, out_dtype);
   MOE_CHECK(!need || (workspace && workspace_bytes >= need), MOE_ERR_WORKSPACE);
   MOE_CHECK(!need || aligned16(workspace), MOE_ERR_UNSUPPORTED);
   BlockGemm g{dyt, dyt_scales, xt, xt_scales, offsets, dw, rows_pad, N, K, E, true, out_dtype == MOE_F32,

@@ -31,6 +31,8 @@ using namespace gemm;
 
 typedef float f32x4v __attribute__((ext_vector_type(4)));
 
+constexpr int kPartRounds = 2;   // rounds of parts of the split tiles, at most
+
 struct BlkKArgs {
   const uint8_t* a;
   const float* a_s;
@@ -44,7 +46,7 @@ struct BlkKArgs {
   int E, nN;
   float* part;       // fp32 sums of the split tiles' parts, or null: no tile is split
   int part_rows;     // rows of a part's slot
-  int min_units;     // blocks per part, at least
+  int part_cost;     // of a part, in blocks' products
 };
 
 // Row offsets, K units (weight gradient) and tile prefix of the experts.
@@ -148,8 +150,10 @@ __device__ __forceinline__ int blk_expert(const BlkSched& s, const BlkKArgs& p, 
 }
 
 // The tiles of the last, partly filled round -- of all of them, where there are fewer than workgroups --
-// are split along the contracted axis into S parts each, so that every workgroup has one: tiles
-// [full, total) as (total - full) S items.  S = 1: none are split.
+// are split along the contracted axis into S parts each: tiles [full, total) as (total - full) S items, which
+// the workgroups take in one round, or in two where that is shorter (more than half of the workgroups had a
+// tile).  A part has more blocks than part_cost, which is what writing and reading it takes, in blocks'
+// products.  S = 1: none are split.
 struct BlkSplit {
   int full, S;
 };
@@ -159,7 +163,13 @@ __device__ __forceinline__ BlkSplit blk_split(const BlkSched& s, const BlkKArgs&
   if (!p.part || rem == 0) return {total, 1};
   int local, units = (int)(p.K / 128);
   if (kWgrad) units = s.units[blk_expert<true>(s, p, nM, total - rem, local)];   // (the longest of them)
-  const int S = min(G / rem, units / p.min_units);
+  int best = units, S = 1;
+  for (int k = 1; k <= kPartRounds; ++k) {
+    const int n = min(k * G / rem, units / (1 + p.part_cost));
+    if (n < 2) continue;
+    const int cost = k * ((units + n - 1) / n + p.part_cost);
+    if (cost < best) { best = cost; S = n; }
+  }
   return S < 2 ? BlkSplit{total, 1} : BlkSplit{total - rem, S};
 }
 
@@ -218,8 +228,8 @@ __device__ __forceinline__ void blk_mma(const Frag<true>& b, const Frag<true>& a
   t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.v[c], a.v[c], c == 0 ? f32x4v{0.f, 0.f, 0.f, 0.f} : t, 0, 0, 0);
 }
 
-// kWide (fp32 output): bf16 products
-template <bool kWgrad, bool kWide>
+// kWide (fp32 output): bf16 products.  kPartial: waves past a tile's last row or column skip its products.
+template <bool kWgrad, bool kWide, bool kPartial>
 __global__ __launch_bounds__(kBlkThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void blk_gemm_kernel(const BlkKArgs p) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[kBlkLds];
@@ -409,6 +419,10 @@ void blk_gemm_kernel(const BlkKArgs p) {
     decode(round + 1, nxt);
     descs(nxt, dn);
     const int ns = max(cur.n, 2);
+    // kPartial: a wave whose rows or columns are all past the tile's last only loads and keeps the barriers: its
+    // SIMD's other wave, which holds rows of the tile's other half, has the matrix core to itself.
+    const bool active =
+        !kPartial || (wm * 16 * kI < cur.mrows && (int64_t)cur.nt * kTN + wn * 64 < (kWgrad ? K : N));
     f32x4v acc[kI][4];
 #pragma unroll
     for (int i = 0; i < kI; ++i)
@@ -429,6 +443,16 @@ void blk_gemm_kernel(const BlkKArgs p) {
         l.s0 = in ? dc.s0 : dn.s0;
         issue(l, in ? cur.n : nxt.n, in ? s + 2 : s + 2 - ns, b, part);
       };
+      if (!active) {
+        barrier();
+        issue_ahead(1);
+        wait_vmcnt<kQB>();
+        barrier();
+        issue_ahead(0);
+        first_frags(b ^ 1);
+        b ^= 1;
+        continue;
+      }
       f32x4v t[2][4];
       float sa[2], sal = 0.f;
       f32x4v sbv[kWgrad ? 4 : 1];
@@ -568,10 +592,11 @@ void blk_gemm_kernel(const BlkKArgs p) {
   wait_vmcnt<0>();
 }
 
-// The split tiles: the S parts of tile full + blockIdx.x added in their order, rows kJoinRows blockIdx.y
-// + [0, kJoinRows).  Eight parts' loads are in flight at once (one at a time, 85 parts of 12 blocks of
-// tokens took 200 us, ten times their products).
-constexpr int kJoinRows = 8;
+// The split tiles' parts, added in their order: kJoinRows rows of a tile at a time, at most kJoinGrid
+// workgroups going over them.  (2000 rows x 1024 x 8192: 44 us with 2048 workgroups, 46 with 1024, 50 with
+// 512; with one for each 8 rows of every tile that could be split, 8160, building their schedules took 8 us.)
+// Eight parts' loads are in flight at once.
+constexpr int kJoinRows = 8, kJoinGrid = 2048;
 template <bool kWgrad, bool kWide>
 __global__ __launch_bounds__(256) void blk_join_kernel(const BlkKArgs p, int G) {
   __shared__ BlkSched sched;
@@ -579,52 +604,58 @@ __global__ __launch_bounds__(256) void blk_join_kernel(const BlkKArgs p, int G) 
   const int nM_w = (int)((p.N + kBM - 1) / kBM);
   build_blk_sched<kWgrad>(sched, p, nM_w);
   const BlkSplit sp = blk_split<kWgrad>(sched, p, nM_w, G);
-  const int tile = sp.full + (int)blockIdx.x;
-  if (sp.S < 2 || tile >= sched.total) return;
-  int local, mt, nt;
-  const int e = blk_expert<kWgrad>(sched, p, nM_w, tile, local), units = sched.units[e];
-  tile_coords(local, kWgrad ? nM_w : (units + kBM - 1) / kBM, p.nN, mt, nt);
-  const int row0 = kWgrad ? mt * kBM : sched.off[e] + mt * kBM;
-  const int mrows = min(kBM, kWgrad ? (int)p.N - row0 : units - mt * kBM);
+  if (sp.S < 2) return;
   const int64_t ncols = kWgrad ? p.K : p.N;
   constexpr int kT = kTN / 4;                           // threads of a row, 4 columns each
-  const int c = (int)(threadIdx.x % kT) * 4;
-  const int64_t col = (int64_t)nt * kTN + c;
-  if (col >= ncols) return;
-  uint8_t* const out = blk_out<kWgrad>(p, e, kWide ? 4 : 2);
+  const int c = (int)(threadIdx.x % kT) * 4, mr = (int)threadIdx.x / kT;
   const int64_t slot = (int64_t)p.part_rows * kTN;
-  const float* src = p.part + (int64_t)blockIdx.x * sp.S * slot + c;
-  const int end = min(mrows, (int)(blockIdx.y + 1) * kJoinRows);
-  for (int m = blockIdx.y * kJoinRows + threadIdx.x / kT; m < end; m += 256 / kT) {
-    f32x4v a = {0.f, 0.f, 0.f, 0.f};
-    const float* q = src + (int64_t)m * kTN;
-    int i = 0;
-    for (; i + 8 <= sp.S; i += 8, q += 8 * slot) {
-      f32x4v v[8];
+  const int tiles = sched.total - sp.full;
+  for (int item = blockIdx.x;; item += gridDim.x) {
+    // rows 0..7 of all tiles first: a tile of few rows ends early
+    const int m0 = item / tiles * kJoinRows, at = item - m0 / kJoinRows * tiles;
+    if (m0 >= p.part_rows) return;
+    int local, mt, nt;
+    const int e = blk_expert<kWgrad>(sched, p, nM_w, sp.full + at, local), units = sched.units[e];
+    tile_coords(local, kWgrad ? nM_w : (units + kBM - 1) / kBM, p.nN, mt, nt);
+    const int row0 = kWgrad ? mt * kBM : sched.off[e] + mt * kBM;
+    const int end = min(min(kBM, kWgrad ? (int)p.N - row0 : units - mt * kBM), m0 + kJoinRows);
+    const int64_t col = (int64_t)nt * kTN + c;
+    if (col >= ncols) continue;
+    uint8_t* const out = blk_out<kWgrad>(p, e, kWide ? 4 : 2);
+    const float* src = p.part + (int64_t)at * sp.S * slot + c;
+    for (int m = m0 + mr; m < end; m += 256 / kT) {
+      f32x4v a = {0.f, 0.f, 0.f, 0.f};
+      const float* q = src + (int64_t)m * kTN;
+      int i = 0;
+      for (; i + 8 <= sp.S; i += 8, q += 8 * slot) {
+        f32x4v v[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = *reinterpret_cast<const f32x4v*>(q + u * slot);
+        for (int u = 0; u < 8; ++u) v[u] = *reinterpret_cast<const f32x4v*>(q + u * slot);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) a += v[u];
+        for (int u = 0; u < 8; ++u) a += v[u];
+      }
+      for (; i < sp.S; ++i, q += slot) a += *reinterpret_cast<const f32x4v*>(q);
+      const int64_t o = (int64_t)(row0 + m) * ncols + col;
+      if constexpr (kWide) *reinterpret_cast<f32x4v*>(reinterpret_cast<float*>(out) + o) = a;
+      else *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(out) + o) = u32x2{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3])};
     }
-    for (; i < sp.S; ++i, q += slot) a += *reinterpret_cast<const f32x4v*>(q);
-    const int64_t o = (int64_t)(row0 + m) * ncols + col;
-    if constexpr (kWide) *reinterpret_cast<f32x4v*>(reinterpret_cast<float*>(out) + o) = a;
-    else *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(out) + o) = u32x2{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3])};
   }
 }
 
-// Blocks per part of a split tile, at least.  A part writes its rows' fp32 sums and reads them back once:
-// a full tile's 256 rows take about as long as 10 blocks' products, a few rows next to nothing.  (18
-// blocks: 64 and 62 us at 2000 rows x 1024 x 8192 and for the gradients of 20000 tokens, 512 x 1024; 10: 54 and
-// 45; unsplit 105 and 89.)
-int min_units(int64_t rows) { return 2 + (int)(rows < kBM ? rows : kBM) / 32; }
+// A part writes its rows' fp32 sums and reads them back once: a full tile's 256 rows take about as long as
+// 9 blocks' products, a few rows next to nothing.  rows: of a tile, on average.  (At 2000 rows x 1024 x 8192
+// and for the gradients of 20000 tokens, 512 x 1024, parts of 18 blocks or more took 64 and 62 us, of 10
+// 54 and 45; unsplit 105 and 89.)
+int part_cost(int64_t rows) { return 1 + (int)(rows < kBM ? rows : kBM) / 32; }
+// Whether tiles of `most` blocks are ever split.
+bool may_split(int64_t most, int cost) { return most >= 2 * (1 + cost); }
 
 }  // namespace
 
-size_t block_gemm_part_bytes(bool wgrad, bool out_f32, int64_t rows, int64_t N, int64_t K) {
+size_t block_gemm_part_bytes(bool wgrad, bool out_f32, int64_t rows, int64_t N, int64_t K, int E) {
   const int64_t prow = wgrad ? N : rows, most = (wgrad ? rows : K) / 128;
-  if (most < 2 * min_units(prow)) return 0;
-  return (size_t)kGemmGrid * (size_t)(prow < kBM ? prow : kBM) * (out_f32 ? 128 : 256) * sizeof(float);
+  if (!may_split(most, part_cost(wgrad ? N : rows / E))) return 0;
+  return (size_t)(kPartRounds * kGemmGrid) * (size_t)(prow < kBM ? prow : kBM) * (out_f32 ? 128 : 256) * sizeof(float);
 }
 
 hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t st) {
@@ -644,14 +675,19 @@ hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t st) {
   k.nN = (int)(((g.wgrad ? g.K : g.N) + tn - 1) / tn);
   const int64_t prow = g.wgrad ? g.N : g.rows, most = (g.wgrad ? g.rows : g.K) / 128;
   k.part_rows = (int)(prow < kBM ? prow : kBM);
-  k.min_units = min_units(prow);
-  const bool split = g.part && most >= 2 * k.min_units;
+  k.part_cost = part_cost(g.wgrad ? g.N : g.rows / g.E);
+  const bool split = g.part && may_split(most, k.part_cost);
+  const int join_grid = std::min(kJoinGrid, (kGemmGrid - 1) * ((k.part_rows + kJoinRows - 1) / kJoinRows));
   k.part = split ? g.part : nullptr;
+  // Products whose experts have two tiles of rows or fewer, on average, are mostly edges: skipping the
+  // empty halves took 8 rows x 28672 x 4096 from 129 to 116 us, 500 x 2048 x 4096 (8 experts) from 45 to
+  // 36; the branch costs the full tiles 1 % (16384 x 4096 x 14336: 843 and 852 us).
+  const bool partial = !g.wgrad && g.rows < 2 * kBM * (int64_t)g.E;
   auto launch = [&](auto wg, auto wide) {
     constexpr bool kWg = decltype(wg)::value, kWd = decltype(wide)::value;
-    blk_gemm_kernel<kWg, kWd><<<kGemmGrid, kBlkThreads, 0, st>>>(k);
-    // a split tile has at least two parts, so there are at most kGemmGrid / 2 of them
-    if (split) blk_join_kernel<kWg, kWd><<<dim3(kGemmGrid / 2, (k.part_rows + kJoinRows - 1) / kJoinRows), 256, 0, st>>>(k, kGemmGrid);
+    if (partial) blk_gemm_kernel<kWg, kWd, !kWg><<<kGemmGrid, kBlkThreads, 0, st>>>(k);
+    else blk_gemm_kernel<kWg, kWd, false><<<kGemmGrid, kBlkThreads, 0, st>>>(k);
+    if (split) blk_join_kernel<kWg, kWd><<<join_grid, 256, 0, st>>>(k, kGemmGrid);
   };
   if (g.wgrad && g.out_f32) launch(std::true_type{}, std::true_type{});
   else if (g.wgrad) launch(std::true_type{}, std::false_type{});

@@ -229,7 +229,7 @@ struct BlockGemm {
   void* const* tab = nullptr;  // weight gradient: device table of the E outputs, in place of out
 };
 // Scratch of the split tiles' parts (0: the sizes never split).
-size_t block_gemm_part_bytes(bool wgrad, bool out_f32, int64_t rows, int64_t N, int64_t K);
+size_t block_gemm_part_bytes(bool wgrad, bool out_f32, int64_t rows, int64_t N, int64_t K, int E);
 hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t st);
 
 }  // namespace moe

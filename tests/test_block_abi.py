@@ -99,8 +99,8 @@ def test_fp8_block_products_workspace(lib):
     inv, uns, wsp = _codes()
     for f, size in ((lib.fp8_block_grouped_gemm, lib.fp8_block_grouped_gemm_workspace),
                     (lib.fp8_block_grouped_wgrad, lib.fp8_block_grouped_wgrad_workspace)):
-        assert size(0, 128, 128, 1) == 0 and size(8, 128, 128, 2) == 0
-        n = size(8192, 512, 8192, 1)
+        assert size(0, 128, 128, 1, 1) == 0 and size(8, 128, 128, 1, 2) == 0 and size(8, 128, 128, 0, 1) == 0
+        n = size(8192, 512, 8192, 2, 1)
         assert n > 0
         a = [P, P, P, P, P, 8192, 512, 8192, 2, 1, P, P, n - 1, None]
         assert f(*a) == wsp
