@@ -22,7 +22,8 @@
 //
 // A stage is one block of K: 128 bytes of 256 A rows and 256 B rows, loaded straight to LDS into one
 // of two buffers while the other is multiplied, with the stage's 512 scales beside them.  Tiles are
-// dealt to a persistent grid of one workgroup per CU from the expert offsets on the device.
+// dealt to a persistent grid of one workgroup per CU from the expert offsets on the device.  Products of
+// few rows an expert (blk_few_kernel) only read the weights, with 16-row tiles and no LDS stages.
 #include "gemm_core.h"
 
 namespace moe {
@@ -59,12 +60,12 @@ struct BlkSched {
 };
 
 // One wave scans the offsets, 64 experts at a time.  They are device data: clamped into [0, rows] and
-// made non-decreasing, so that no access leaves the buffers whatever they hold.
+// made non-decreasing, so that no access leaves the buffers whatever they hold.  kRows: of a tile.
 // Every expert has the same number of weight-gradient tiles, but tiles of its own length; in falling order
 // of length, and dealt to the workgroups in alternating directions, their sums come out even (64 experts of
 // Zipf popularity, 176 tiles each: the longest workgroup has 1.08 times the mean, 1.22 in the experts' own
 // order; 1769 -> 1682 us).
-template <bool kWgrad>
+template <bool kWgrad, int kRows = kBM>
 __device__ __forceinline__ void build_blk_sched(BlkSched& s, const BlkKArgs& p, int nM) {
   const int lane = threadIdx.x & 63;
   if (threadIdx.x < 64) {
@@ -83,7 +84,7 @@ __device__ __forceinline__ void build_blk_sched(BlkSched& s, const BlkKArgs& p, 
       if (lane == 0) lo = top;
       const int cnt = e < p.E ? hi - lo : 0;
       const int nblk = (cnt + 127) / 128;
-      int t = (cnt + kBM - 1) / kBM * p.nN;
+      int t = (cnt + kRows - 1) / kRows * p.nN;
       int inc = kWgrad ? nblk : 0;
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
@@ -642,6 +643,101 @@ __global__ __launch_bounds__(256) void blk_join_kernel(const BlkKArgs p, int G) 
   }
 }
 
+// 32 codes of a lane: 16 bytes, and 16 that lie 64 bytes further, half a block of 128.
+__device__ __forceinline__ i32x8 load256(const rsrc_t& r, uint32_t off) {
+  const i32x4 a = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+  const i32x4 b = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off + 64, 0, 0));
+  return i32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+
+// Products of few rows an expert, decoding's: their time is that of reading the weights, once each, so
+// nothing is shared through LDS.  A tile is 16 rows of a by 16 kCols of w; the four waves of a workgroup
+// take a quarter of K each and their sums meet in LDS, in the waves' order.  A lane loads its 32 codes of
+// a fragment as the matrix instructions take them, 64 consecutive bytes of 16 rows at a time, kUnroll
+// blocks ahead of their products.  The persistent workgroups (six of four waves fit a CU) take
+// consecutive tiles at the same time, so the weights are read as they lie; with each XCD in a stretch of
+// its own, and with a workgroup for each of min(R, E) N / (16 kCols) possible tiles, 8 rows of 8 experts
+// (28672 x 4096) took 99 and 90 us, against 91; rows that crowd on one expert, 38 and 128.
+// Measured: 8 rows, 28672 x 4096, 4.3 experts chosen: 91 us (5.6 TB/s of weights), 117 in the kernel above;
+// one row, 4096 x 14336: 16, was 22.
+constexpr int kFewRows = 16, kFewWaves = 4, kFewGrid = 6 * kGemmGrid;
+template <bool kWide, int kCols, int kUnroll>
+__global__ __launch_bounds__(64 * kFewWaves) void blk_few_kernel(const BlkKArgs p) {
+  __shared__ BlkSched sched;
+  __shared__ f32x4v sums[2][kCols][kFewWaves][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  build_blk_sched<false, kFewRows>(sched, p, 0);
+  const int total = __builtin_amdgcn_readfirstlane(sched.total);
+  const int R = (int)p.rows, N = (int)p.N, nb = (int)(p.K / 128), r = lane & 15;
+  const int b0 = wave * nb / kFewWaves, b1 = (wave + 1) * nb / kFewWaves;
+  const uint32_t K = (uint32_t)p.K, off0 = (uint32_t)r * K + (uint32_t)(lane >> 4) * 16;
+  constexpr uint32_t kOut = 0xffffff00u;                // past every range: reads zeros
+  const rsrc_t rs = make_rsrc(p.a_s, (uint32_t)((int64_t)nb * R * 4));
+  int buf = 0;
+  for (int t = blockIdx.x; t < total; t += gridDim.x, buf ^= 1) {
+    const int e = __builtin_amdgcn_readfirstlane(blk_find(sched, p.E, t));
+    const int units = __builtin_amdgcn_readfirstlane(sched.units[e]), groups = (units + kFewRows - 1) / kFewRows;
+    const int local = t - __builtin_amdgcn_readfirstlane(sched.tile[e]), g = local % groups;
+    const int n0 = local / groups * 16 * kCols, m0 = __builtin_amdgcn_readfirstlane(sched.off[e]) + g * kFewRows;
+    const int rows = min(kFewRows, units - g * kFewRows);
+    const rsrc_t ra = make_rsrc(p.a + (int64_t)m0 * K, (uint32_t)rows * K);
+    const rsrc_t rw = make_rsrc(p.b + ((int64_t)e * N + n0) * K, (uint32_t)min(16 * kCols, N - n0) * K);
+    const float* ws = p.b_s + ((int64_t)e * ((N + 127) / 128) + n0 / 128) * nb;
+    f32x4v acc[kCols];
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) acc[j] = f32x4v{0.f, 0.f, 0.f, 0.f};
+    for (int b = b0; b < b1; b += kUnroll) {
+      i32x8 x[kUnroll], w[kUnroll][kCols];
+      float sc[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const bool in = b + u < b1;
+        const uint32_t o = off0 + (uint32_t)(b + u) * 128;
+        x[u] = load256(ra, in ? o : kOut);
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) w[u][j] = load256(rw, in ? o + 16 * j * K : kOut);
+        const uint32_t so = in ? (uint32_t)((b + u) * R + m0 + r) * 4 : kOut;
+        sc[u] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, so, 0, 0)) * (in ? ws[b + u] : 0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+          Frag<kWide> fx, fw;
+          fx.set(x[u]);
+          fw.set(w[u][j]);
+          f32x4v v;
+#pragma unroll
+          for (int c = 0; c < (kWide ? 4 : 1); ++c) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) { fx.half(x[u], c, h); fw.half(w[u][j], c, h); }
+            blk_mma(fw, fx, v, c);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[j][i] = fmaf(sc[u], v[i], acc[j][i]);
+        }
+      }
+    }
+    // one barrier a tile: a wave is past the reads of one tile's sums before it meets the next one's barrier
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) sums[buf][j][wave][lane] = acc[j];
+    __syncthreads();
+    if (wave < kCols && r < rows && n0 + 16 * wave < N) {
+      f32x4v a = sums[buf][wave][0][lane];
+#pragma unroll
+      for (int i = 1; i < kFewWaves; ++i) a += sums[buf][wave][i][lane];
+      const int64_t o = (int64_t)(m0 + r) * N + n0 + 16 * wave + 4 * (lane >> 4);
+      if constexpr (kWide) *reinterpret_cast<f32x4v*>(reinterpret_cast<float*>(p.out) + o) = a;
+      else *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(p.out) + o) = u32x2{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3])};
+    }
+  }
+}
+
+// Whether a product of so many rows is one of few: 8 an expert on average (64 rows of 8 experts, 4096 x 14336:
+// 89 us here, 96 in the kernel of 256-row tiles; 100 rows: 111 and 97), or 16 in all (one expert's 16
+// rows, 4096 x 14336: 20 and 24).
+bool few_rows(int64_t R, int E) { return R <= kFewRows || R <= 8 * (int64_t)E; }
+
 // A part writes its rows' fp32 sums and reads them back once: a full tile's 256 rows take about as long as
 // 9 blocks' products, a few rows next to nothing.  rows: of a tile, on average.  (At 2000 rows x 1024 x 8192
 // and for the gradients of 20000 tokens, 512 x 1024, parts of 18 blocks or more took 64 and 62 us, of 10
@@ -654,6 +750,7 @@ bool may_split(int64_t most, int cost) { return most >= 2 * (1 + cost); }
 
 size_t block_gemm_part_bytes(bool wgrad, bool out_f32, int64_t rows, int64_t N, int64_t K, int E) {
   const int64_t prow = wgrad ? N : rows, most = (wgrad ? rows : K) / 128;
+  if (!wgrad && few_rows(rows, E)) return 0;
   if (!may_split(most, part_cost(wgrad ? N : rows / E))) return 0;
   return (size_t)(kPartRounds * kGemmGrid) * (size_t)(prow < kBM ? prow : kBM) * (out_f32 ? 128 : 256) * sizeof(float);
 }
@@ -671,6 +768,20 @@ hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t st) {
   k.N = g.N;
   k.K = g.K;
   k.E = g.E;
+  if (!g.wgrad && few_rows(g.rows, g.E)) {
+    // Two fragments of columns share one of a's, unless the tiles are then fewer than two a CU: with one, twice
+    // as many tiles, and as many loads in flight (one row, 4096 x 14336: 16 and 25 us; 8 rows, 28672 x 4096: 97 and 91).
+    const bool two = std::min<int64_t>(g.rows, g.E) * (g.N / 32) >= 2 * kGemmGrid;
+    k.nN = (int)(two ? (g.N + 31) / 32 : g.N / 16);
+    auto few = [&](auto wide) {
+      constexpr bool kWd = decltype(wide)::value;
+      if (two) blk_few_kernel<kWd, 2, 2><<<kFewGrid, 64 * kFewWaves, 0, st>>>(k);
+      else blk_few_kernel<kWd, 1, 4><<<kFewGrid, 64 * kFewWaves, 0, st>>>(k);
+    };
+    if (g.out_f32) few(std::true_type{});
+    else few(std::false_type{});
+    return hipGetLastError();
+  }
   const int tn = g.out_f32 ? 128 : 256;
   k.nN = (int)(((g.wgrad ? g.K : g.N) + tn - 1) / tn);
   const int64_t prow = g.wgrad ? g.N : g.rows, most = (g.wgrad ? g.rows : g.K) / 128;
@@ -680,7 +791,7 @@ hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t st) {
   const int join_grid = std::min(kJoinGrid, (kGemmGrid - 1) * ((k.part_rows + kJoinRows - 1) / kJoinRows));
   k.part = split ? g.part : nullptr;
   // Products whose experts have two tiles of rows or fewer, on average, are mostly edges: skipping the
-  // empty halves took 8 rows x 28672 x 4096 from 129 to 116 us, 500 x 2048 x 4096 (8 experts) from 45 to
+  // empty halves took 100 rows x 4096 x 14336 (8 experts) from 109 to 94 us, 500 x 2048 x 4096 from 45 to
   // 36; the branch costs the full tiles 1 % (16384 x 4096 x 14336: 843 and 852 us).
   const bool partial = !g.wgrad && g.rows < 2 * kBM * (int64_t)g.E;
   auto launch = [&](auto wg, auto wide) {

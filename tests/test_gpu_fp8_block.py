@@ -133,6 +133,14 @@ GEMM = [
     ("split-one-row", [0, 0, 1], 48, 4224),
     ("split-full-tiles", [600, 0, 40], 400, 5120),
     ("split-last-round", [256, 200, 0, 256], 256 * 23, 4736),
+    ("split-29-rows", [20, 0, 9], 400, 8192),
+    ("split-two-rounds", [25], 128 * 140, 2048),
+    # few rows an expert: several groups of one expert, K's blocks uneven among the waves, a last odd column
+    # fragment, every column width
+    ("few-crowded", [35, 0, 0, 0, 1], 144, 640),
+    ("few-sixteen", [16], 48, 384),
+    ("few-wide", [0, 3, 17] * 20 + [0, 60], 1040, 896),
+    ("few-one-block", [1, 0, 2] * 50, 336, 128),
 ]
 
 
