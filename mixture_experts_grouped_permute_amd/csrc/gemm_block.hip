@@ -455,11 +455,12 @@ void blk_gemm_kernel(const BlkKArgs p) {
         continue;
       }
       f32x4v t[2][4];
-      float sa[2], sal = 0.f;
+      float sa[2], sal[2] = {0.f, 0.f};
+      i32x8 rl;
       f32x4v sbv[kWgrad ? 4 : 1];
       // sums of A fragment u: element r of its products with B fragment j
       auto add = [&](int u, int j, int r) {
-        const float sv = u == kI - 1 ? sal : sa[u & 1];
+        const float sv = u >= kI - 2 ? sal[u - kI + 2] : sa[u & 1];
         if constexpr (kWgrad) acc[u][j][r] += (sv * sbv[j][r]) * t[u & 1][j][r];
         else acc[u][j][r] += (sv * sbv[0][0]) * t[u & 1][j][r];
       };
@@ -479,7 +480,7 @@ void blk_gemm_kernel(const BlkKArgs p) {
           barrier();
           issue_ahead(1);
         }
-        if (i == kI - 1) {
+        if (i == kI - 2) {
           wait_vmcnt<kQB>();                            // the next stage landed: all but the kQB loads above
           barrier();
         }
@@ -490,11 +491,15 @@ void blk_gemm_kernel(const BlkKArgs p) {
           __builtin_amdgcn_sched_barrier(0);
           if (n == 0) {
             // scales: all of the stage's are read ahead of the second barrier
-            if (i + 1 < kI) {
+            if (i + 2 < kI) {
               ra = frag(st, fa, i + 1);
               sa[i & 1] = sc[wm * 16 * kI + i * 16 + r16];
             }
-            if (i + 2 == kI) sal = sc[wm * 16 * kI + (kI - 1) * 16 + r16];
+            if (i + 3 == kI) {
+              rl = frag(st, fa, kI - 1);
+              sal[0] = sc[wm * 16 * kI + (kI - 2) * 16 + r16];
+              sal[1] = sc[wm * 16 * kI + (kI - 1) * 16 + r16];
+            }
             if (i == 0) {
               if constexpr (kWgrad) {
 #pragma unroll
@@ -503,7 +508,12 @@ void blk_gemm_kernel(const BlkKArgs p) {
                 sbv[0][0] = sc[256 + wn * 64];
               }
             }
-            if (i == kI - 1) issue_ahead(0);
+            if (i == kI - 2) issue_ahead(0);
+          }
+          if (i == kI - 1) {                            // the next stage's first fragments, where these were
+            const uint8_t* const nst = smem + (b ^ 1) * kStageBytes;
+            if (kWide ? (n & 3) == 0 : true) rb[kWide ? n >> 2 : n] = frag(nst, fb, kWide ? n >> 2 : n);
+            if (n == (kWide ? 1 : 3)) ra = frag(nst, fa, 0);
           }
           if constexpr (kWide) {
             if (i > 0) add(i - 1, n >> 2, n & 3);
@@ -511,7 +521,7 @@ void blk_gemm_kernel(const BlkKArgs p) {
               bf[n & 3].half(rb[n & 3], (n >> 2) + 1, 0);
               bf[n & 3].half(rb[n & 3], (n >> 2) + 1, 1);
             }
-            if (i + 1 < kI && n >= 8) af[(i + 1) & 1].half(ra, (n - 8) / 2, n & 1);   // (ra has arrived)
+            if (i + 1 < kI && n >= 8) af[(i + 1) & 1].half(i + 2 == kI ? rl : ra, (n - 8) / 2, n & 1);   // (ra has arrived)
           } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
@@ -519,10 +529,8 @@ void blk_gemm_kernel(const BlkKArgs p) {
           }
           __builtin_amdgcn_sched_barrier(0);
         }
-        if (i + 1 < kI) af[(i + 1) & 1].set(ra);
+        if (i + 1 < kI) af[(i + 1) & 1].set(i + 2 == kI ? rl : ra);
       }
-      first_frags(b ^ 1);
-      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int n = 0; n < 16; ++n) add(kI - 1, n >> 2, n & 3);
       b ^= 1;
