@@ -11,8 +11,9 @@
 // 16 x 16 x 128 is the shape whose K is exactly one block: a 32 x 32 x 64 pair would need 16 temporary
 // registers per tile instead of 4.  The running sums have to be in registers the VALU reads, so a wave
 // owns 128 x 64 outputs (128 registers) and 8 waves, two per SIMD, share a 256 x 256 tile: while one
-// wave's VALU adds a block, the other's MFMAs run.  Per stage and SIMD the MFMAs take 2048 cycles, the
-// adds 1024 (weight gradient, whose scale differs in every column as well: 2048).
+// wave's VALU adds a block, the other's MFMAs run.  An MFMA takes 32 cycles and 16 of the VALU's issue: four
+// adds fit beside it (measured 33 cycles), the weight gradient's eight instructions, whose scale differs
+// in every column as well, make it 48.
 //
 // fp32 outputs take another path (kWide).  The E4M3 matrix instructions align the products of a group to
 // its largest one and drop what falls below about 2^-16 of it: 1.3e-5 (normwise) off on Gaussian
@@ -405,8 +406,11 @@ void blk_gemm_kernel(const BlkKArgs p) {
   // behind its own matrix instructions only if it comes between them (8 instructions of 32 cycles with
   // 32 fused multiply-adds took 292 cycles so, 384 in groups of 4 and 16).  The B rows' buffer is free
   // once every wave holds its B fragments (the first barrier, after which the B rows of the stage after
-  // next are loaded), the A rows' once the last A fragment is in registers (the second, after which the
-  // next stage has landed and its first fragments are read under the last products).
+  // next are loaded), the A rows' once the last two A fragments are in registers (the second, ahead of
+  // the products of the last but one, after which the next stage has landed).  The next stage's B fragments
+  // and first A fragment are read behind the last products, into the registers that these free: read
+  // after them, with the second barrier a fragment later, the matrix cores waited some 600 cycles a stage
+  // for LDS (16384 x 4096 x 14336: 871 -> 849 us, the earlier barrier 847 -> 826).
   int b = 0;
   i32x8 rb[4], ra;
   auto first_frags = [&](int buf) {
