@@ -21,6 +21,10 @@ CASES = [
     (257, 512, 640, 5, 3, "bf16", None),
     (300, 256, 128, 6, 1, "bf16", [0, 33, 0, 255, 12, 0]),
     (700, 384, 256, 3, 1, "f32", [600, 100, 0]),
+    # few rows an expert, as in decoding
+    (3, 256, 384, 8, 2, "bf16", None),
+    (20, 128, 256, 16, 4, "f32", None),
+    (100, 640, 1152, 16, 1, "bf16", [90] + [0] * 13 + [4, 6]),
 ]
 IDS = [f"T{c[0]}-H{c[1]}-I{c[2]}-E{c[3]}-k{c[4]}-{c[5]}{'-counts' if c[6] else ''}" for c in CASES]
 
