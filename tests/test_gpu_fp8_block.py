@@ -270,7 +270,9 @@ def test_wgrad_bad_offsets_stay_inside():
 def test_products_in_graphs_and_on_streams():
     m = need_gpu()
     runs = []
-    for sizes, N, K in (([4, 0, 2], 512, 512), ([300, 40, 513], 400, 384)):
+    # few rows, whole tiles, tiles split along K, along the tokens
+    for sizes, N, K in (([4, 0, 2], 512, 512), ([300, 40, 513], 400, 384), ([20, 0, 9], 400, 8192),
+                        ([5000, 10, 0, 900], 48, 128)):
         off, a, s, w, ws = _gemm_inputs(m, sizes, N, K)
         o = torch.from_numpy(off).cuda()
         xt = m.fp8_block_quantize(_x((int(off[-1]), 64), torch.bfloat16, 4).cuda(), axis=1, group_offsets=o)
