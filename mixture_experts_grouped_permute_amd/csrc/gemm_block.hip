@@ -129,13 +129,14 @@ __device__ __forceinline__ void build_blk_sched(BlkSched& s, const BlkKArgs& p, 
   }
 }
 
+// Largest e with tile[e] <= t, for the whole wave: the prefix does not fall, and of experts without
+// tiles, which share a value, that is the last, which has the tiles.  (One LDS read in place of log2 E
+// dependent ones.)
 __device__ __forceinline__ int blk_find(const BlkSched& s, int E, int t) {
-  int lo = 0, hi = E - 1;   // largest e with tile[e] <= t; experts without tiles share a prefix value,
-  while (lo < hi) {         // and the last of them, which has the tiles, is found
-    const int mid = (lo + hi + 1) >> 1;
-    if (s.tile[mid] <= t) lo = mid; else hi = mid - 1;
-  }
-  return lo;
+  const int lane = threadIdx.x & 63;
+  int n = -1;
+  for (int e0 = 0; e0 < E; e0 += 64) n += __popcll(__ballot(e0 + lane < E && s.tile[e0 + lane] <= t));
+  return n;
 }
 
 // Expert of a tile, and the tile's index among the expert's.
