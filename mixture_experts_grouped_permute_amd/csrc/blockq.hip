@@ -93,7 +93,7 @@ __global__ __launch_bounds__(256) void block_rows_kernel(const void* __restrict_
 // are packed straight from its registers -- the transpose costs no data movement there -- and each
 // thread's 8 bytes of a column meet those of the 15 other row groups in LDS, to leave as whole
 // 128-byte lines.  Loads and stores pass the caches by: 131072 x 1408 tokens 120 -> 105 us, 8 matrices of
-// 4096 x 14336 275 -> 247 (the rows' kernel, whose codes a product reads next, gains nothing by it).
+// 4096 x 14336 275 -> 245 (the rows' kernel, whose codes a product reads next, gains nothing by it).
 //   kTokens  blocks of 128 rows x 1 column; the rows are the padded rows of expert segments
 //   kPlain   one 128 x 128 block of a weight matrix, codes in its own layout
 //   kTrans   the same, codes transposed
@@ -114,6 +114,12 @@ struct TileP {
   uint8_t* q;
   float* scales;
 };
+
+// The order of a weight matrix's tiles.  kPlain: along the rows, which it reads and writes (28672 x 4096, 8
+// matrices: 485 us; down the columns, 256 bytes of every 8 KB at a time, 669).  kTrans reads along the rows and
+// writes along the columns: 8 tiles of a row, then the next row's (28672 x 4096: 526 us, 587 down
+// the columns, 535 along the rows; 4096 x 14336: 245, 251, 281; 64 of 2816 x 2048: 201, 193, 208).
+__host__ __device__ constexpr int64_t walk_cols(int64_t tiles) { return tiles < 8 ? tiles : 8; }
 
 constexpr int kPitch = 128 + 8;   // LDS bytes per output row
 
@@ -139,7 +145,17 @@ __global__ __launch_bounds__(256) void block_tile_kernel(const TileP p, const WT
     x = tab.w[e];
 #endif
   }
-  const int64_t p0 = (int64_t)blockIdx.x * 128;
+  const int64_t nct = (p.cols + 127) / 128;
+  int64_t rb = blockIdx.x, ct0 = blockIdx.y;
+  if constexpr (kMode == kPlain) {
+    rb = blockIdx.x / nct;
+    ct0 = blockIdx.x % nct;
+  } else if constexpr (kMode == kTrans) {
+    const int64_t n = walk_cols(nct), per = (p.rows + 127) / 128 * n, in = blockIdx.x % per;
+    rb = in / n;
+    ct0 = blockIdx.x / per * n + in % n;
+  }
+  const int64_t p0 = rb * 128;
   bool dead = false;                                      // kTokens: no row of this tile has a token
   if constexpr (kMode == kTokens) {
     // padded segment starts, one wave scanning 64 groups at a time.  The offsets are device data:
@@ -201,7 +217,7 @@ __global__ __launch_bounds__(256) void block_tile_kernel(const TileP p, const WT
     }
     __syncthreads();
   }
-  for (int64_t ct = blockIdx.y; ct * 128 < p.cols; ct += gridDim.y) {
+  for (int64_t ct = ct0; ct < nct; ct += kMode == kTokens ? gridDim.y : nct) {
     const int64_t c0 = ct * 128, col = c0 + 8 * ck;
     const bool in_c = col < p.cols;
     Raw8<kF32> v[8];
@@ -244,7 +260,7 @@ __global__ __launch_bounds__(256) void block_tile_kernel(const TileP p, const WT
         for (int i = 0; i < 16; ++i) m = umax(m, s_max[i][tid]);
         const BlockScale s = block_scale(m);
         s_f[tid] = s.factor;
-        if (c0 + tid < p.cols) p.scales[(int64_t)blockIdx.x * p.cols + c0 + tid] = s.d;
+        if (c0 + tid < p.cols) p.scales[rb * p.cols + c0 + tid] = s.d;
       }
       __syncthreads();
 #pragma unroll
@@ -265,7 +281,7 @@ __global__ __launch_bounds__(256) void block_tile_kernel(const TileP p, const WT
       for (int j = 0; j < 8; ++j) f[j] = s.factor;
       const int64_t nb = (p.rows + 127) / 128, kb = (p.cols + 127) / 128;
       if (tid == 0)
-        p.scales[e * nb * kb + (kMode == kPlain ? (int64_t)blockIdx.x * kb + ct : ct * nb + (int64_t)blockIdx.x)] = s.d;
+        p.scales[e * nb * kb + (kMode == kPlain ? rb * kb + ct : ct * nb + rb)] = s.d;
       if constexpr (kMode == kPlain) {
         uint8_t* qe = p.q + e * p.rows * p.cols;
 #pragma unroll
@@ -348,7 +364,8 @@ hipError_t launch_block_weights(const void* const* w, int E, int64_t rows, int64
   WTab tab{};
   for (int e = 0; e < E; ++e) tab.w[e] = reinterpret_cast<const uint16_t*>(w[e]);
   const int64_t ct = (cols + 127) / 128;
-  const dim3 grid((unsigned)((rows + 127) / 128), (unsigned)(ct < 65535 ? ct : 65535), (unsigned)E);
+  const int64_t n = walk_cols(ct), walk = transposed ? (ct + n - 1) / n * n : ct;
+  const dim3 grid((unsigned)((rows + 127) / 128 * walk), 1, (unsigned)E);
   if (transposed) block_tile_kernel<false, kTrans><<<grid, 256, 0, st>>>(p, tab);
   else block_tile_kernel<false, kPlain><<<grid, 256, 0, st>>>(p, tab);
   return hipGetLastError();
