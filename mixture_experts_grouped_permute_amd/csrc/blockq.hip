@@ -93,7 +93,7 @@ __global__ __launch_bounds__(256) void block_rows_kernel(const void* __restrict_
 // are packed straight from its registers -- the transpose costs no data movement there -- and each
 // thread's 8 bytes of a column meet those of the 15 other row groups in LDS, to leave as whole
 // 128-byte lines.  Loads and stores pass the caches by: 131072 x 1408 tokens 120 -> 105 us, 8 matrices of
-// 4096 x 14336 275 -> 245 (the rows' kernel, whose codes a product reads next, gains nothing by it).
+// 4096 x 14336 transposed 275 -> 245 (the rows' kernel, whose codes a product reads next, gains nothing by it).
 //   kTokens  blocks of 128 rows x 1 column; the rows are the padded rows of expert segments
 //   kPlain   one 128 x 128 block of a weight matrix, codes in its own layout
 //   kTrans   the same, codes transposed
