@@ -86,7 +86,7 @@ def test_quantize_tokens_bad_offsets_stay_inside():
 
 
 @gpu
-@pytest.mark.parametrize("E,rows,cols", [(1, 16, 128), (3, 128, 256), (2, 144, 384), (70, 256, 128)])
+@pytest.mark.parametrize("E,rows,cols", [(1, 16, 128), (3, 128, 256), (2, 144, 384), (70, 256, 128), (2, 384, 1408)])
 def test_quantize_weights_both_ways(E, rows, cols):
     m = need_gpu()
     w = _x((E, rows, cols), torch.bfloat16, E)
