@@ -65,9 +65,23 @@ __device__ __forceinline__ float group_max(float v) {
 // is a max and a min.  fp32 logits: the double of the same value, whose 29 free mantissa bits take the
 // expert (its complement where a larger mantissa means a larger number); infinities become +-2^1000,
 // since their mantissa has no room, and a NaN, which no order holds, comes first.  bf16 logits: their
-// sortable 16 bits above the expert, in 32.
+// rank above the expert, in 32 bits.
 template <bool kF32>
 struct Key;
+
+// The magnitude's bits on either side of 0x7F800000: an unsigned number in the order of the logits, with -inf
+// at 0, both zeros in the middle and +inf at 0xFF000000.  What lies beyond, above (a NaN) or wrapped around
+// from below (one with its sign set, what a host's conversion to bf16 writes), becomes the one NaN on top.
+template <uint32_t kStep>   // the lowest bit that a logit uses
+__device__ __forceinline__ uint32_t rank_of(float v) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v), s = (uint32_t)((int32_t)u >> 31);
+  const uint32_t x = ((u & 0x7FFFFFFFu) ^ s) - s + 0x7F800000u;
+  return x < 0xFF000000u + kStep ? x : 0xFF000000u + kStep;
+}
+__device__ __forceinline__ float value_of(uint32_t rank) {
+  const uint32_t x = rank - 0x7F800000u, s = (uint32_t)((int32_t)x >> 31);
+  return __builtin_bit_cast(float, ((x ^ s) - s) | (s & 0x80000000u));
+}
 template <>
 struct Key<true> {
   using type = double;
@@ -101,17 +115,11 @@ struct Key<true> {
 template <>
 struct Key<false> {
   using type = uint32_t;
+  // (no expert: also the key of -inf at expert 255, but of 256 experts none is missing)
   static __device__ __forceinline__ uint32_t none() { return 0u; }
-  static __device__ __forceinline__ uint32_t make(float v, int e) {
-    const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.0f) >> 16;
-    const uint32_t s = (b & 0x8000u) ? (~b & 0xFFFFu) : (b | 0x8000u);
-    return s << 8 | (uint32_t)(255 - e);
-  }
+  static __device__ __forceinline__ uint32_t make(float v, int e) { return rank_of<0x10000u>(v) | (uint32_t)(255 - e); }
   static __device__ __forceinline__ int expert(uint32_t k) { return 255 - (int)(k & 255u); }
-  static __device__ __forceinline__ float value(uint32_t k) {
-    const uint32_t s = k >> 8;
-    return bf16_to_f32((uint16_t)((s & 0x8000u) ? (s & 0x7FFFu) : (~s & 0xFFFFu)));
-  }
+  static __device__ __forceinline__ float value(uint32_t k) { return value_of(k & 0xFFFF0000u); }
   static __device__ __forceinline__ uint32_t hi(uint32_t a, uint32_t b) { return a > b ? a : b; }
   static __device__ __forceinline__ uint32_t lo(uint32_t a, uint32_t b) { return a < b ? a : b; }
 };

@@ -213,3 +213,40 @@ def test_refusals_on_the_gpu():
         m.moe_route_balance_bwd(lg, idx.long(), prob, counts)
     with pytest.raises(ValueError):
         m.moe_route_balance_bwd(lg, idx, prob, counts, dlosses=torch.ones(1, device="cuda"))
+
+
+# bit patterns of NaN: quiet with either sign, and all ones, what a host's conversion to bf16 writes
+NANS = {torch.bfloat16: [0x7FC0, -0x0040, -0x0001, 0x7F81], torch.float32: [0x7FC00000, -0x00400000, -0x00000001, 0x7FC00001]}
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("E,k", [(7, 2), (10, 3), (30, 4), (64, 8), (256, 8)])
+def test_a_nan_of_either_sign_is_selected_first(E, k, dtype):
+    """Ahead of everything finite, also at an expert that would be chosen last; the lower id first among
+    several, whatever their bits.  The token's weights and both losses are NaN, other tokens as they were."""
+    m = need_gpu()
+    T = 40
+    lg = _logits(T, E, "normal", dtype)
+    want, _, _, _ = balance.forward(lg, k)
+    bits = lg.view(torch.int16 if dtype == torch.bfloat16 else torch.int32)
+    first = {}
+    for i, pat in enumerate(NANS[dtype]):
+        e = int(lg[i].float().argmin())
+        bits[i, e] = pat
+        first[i] = [e]
+    bits[5, E - 1], bits[5, 1] = NANS[dtype][0], NANS[dtype][1]
+    bits[6, E - 1], bits[6, 1] = NANS[dtype][2], NANS[dtype][0]
+    first[5] = first[6] = [1, E - 1]
+    idx, prob, counts, losses = m.moe_route_balance(lg.cuda(), k)
+    torch.cuda.synchronize()
+    idx, prob = idx.cpu(), prob.cpu()
+    for t, ids in first.items():
+        assert idx[t, :len(ids)].tolist() == ids, t
+        assert torch.isnan(prob[t]).all(), t
+    ok = [t for t in range(T) if t not in first]
+    np.testing.assert_array_equal(idx[ok].numpy(), want[ok])
+    assert torch.isfinite(prob[ok]).all() and torch.isnan(losses).all() and int(counts.sum()) == T * k
+    # the gradient of such a token is NaN and stays with it
+    d = m.moe_route_balance_bwd(lg.cuda(), idx.cuda(), prob.cuda(), counts, None, torch.ones(2, device="cuda")).cpu()
+    assert torch.isnan(d[list(first)]).all() and torch.isfinite(d[ok]).all()
