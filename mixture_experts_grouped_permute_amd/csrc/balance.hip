@@ -63,9 +63,10 @@ __device__ __forceinline__ float group_max(float v) {
 
 // ---- keys that order (logit descending, expert ascending) as one number, so that a compare-exchange
 // is a max and a min.  fp32 logits: the double of the same value, whose 29 free mantissa bits take the
-// expert (its complement where a larger mantissa means a larger number); infinities become +-2^1000,
-// since their mantissa has no room, and a NaN, which no order holds, comes first.  bf16 logits: their
-// rank above the expert, in 32 bits.
+// expert (its complement where a larger mantissa means a larger number).  An fp32 number's exponent field is 0 or
+// within 0x369 .. 0x47E there, 0x7FF for infinities and NaN: without its bit 0x100 it is 0, 0x269 .. 0x2FF,
+// 0x400 .. 0x47E, 0x6FF, in the same order, so that infinities and NaN become numbers as well, a NaN
+// (one pattern for all, its sign clear) the largest.  bf16 logits: their rank above the expert, in 32 bits.
 template <bool kF32>
 struct Key;
 
@@ -87,9 +88,9 @@ struct Key<true> {
   using type = double;
   static __device__ __forceinline__ double none() { return -__builtin_huge_val(); }
   static __device__ __forceinline__ double make(float v, int e) {
-    double d = (double)(v + 0.0f);                     // -0 -> +0: equal logits tie
-    d = fmax(fmin(d, 0x1p1000), -0x1p1000);
-    const uint64_t u = __builtin_bit_cast(uint64_t, d);
+    const uint32_t w = v != v ? 0x7FC00000u : __builtin_bit_cast(uint32_t, v);
+    const double d = (double)(__builtin_bit_cast(float, w) + 0.0f);   // -0 -> +0: equal logits tie
+    const uint64_t u = __builtin_bit_cast(uint64_t, d) & ~(1ull << 60);
     return __builtin_bit_cast(double, u | (uint64_t)((u >> 63) ? e : 255 - e));
   }
   static __device__ __forceinline__ int expert(double k) {
@@ -98,7 +99,8 @@ struct Key<true> {
     return (u >> 63) ? low : 255 - low;
   }
   static __device__ __forceinline__ float value(double k) {
-    return (float)__builtin_bit_cast(double, __builtin_bit_cast(uint64_t, k) & ~(uint64_t)255);
+    const uint64_t u = __builtin_bit_cast(uint64_t, k) & ~(uint64_t)255;
+    return (float)__builtin_bit_cast(double, u | (u >> 1 & 1ull << 60));   // (fields with 0x200 had 0x100 as well)
   }
   // (keys are never NaN: the instruction itself, without the quieting that fmax puts before it)
   static __device__ __forceinline__ double hi(double a, double b) {

@@ -250,3 +250,18 @@ def test_a_nan_of_either_sign_is_selected_first(E, k, dtype):
     # the gradient of such a token is NaN and stays with it
     d = m.moe_route_balance_bwd(lg.cuda(), idx.cuda(), prob.cuda(), counts, None, torch.ones(2, device="cuda")).cpu()
     assert torch.isnan(d[list(first)]).all() and torch.isfinite(d[ok]).all()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_a_nan_is_selected_ahead_of_infinity(dtype):
+    m = need_gpu()
+    nan, inf = float("nan"), float("inf")
+    lg = torch.zeros((3, 20), dtype=dtype)
+    lg[0, 2], lg[0, 9] = inf, nan
+    lg[1, 0], lg[1, 3], lg[1, 18], lg[1, 19] = inf, nan, inf, -nan
+    lg[2, 1], lg[2, 4], lg[2, 5] = inf, float(torch.finfo(dtype).max), inf
+    idx, prob, _, losses = m.moe_route_balance(lg.cuda(), 4)
+    torch.cuda.synchronize()
+    assert idx.tolist() == [[9, 2, 0, 1], [3, 19, 0, 18], [1, 5, 4, 0]]
+    assert torch.isnan(prob).all() and torch.isnan(losses).all()
