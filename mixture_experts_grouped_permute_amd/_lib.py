@@ -476,6 +476,21 @@ def _shape(t: Optional[torch.Tensor], shape, dtype: torch.dtype, device: torch.d
         raise ValueError(f"{what} must be contiguous")
 
 
+def _cached(w_quant, compute: str, transposed: bool, E: int, H: int, I: int, device: torch.device) -> None:
+    """Raise unless w_quant is quantize_weights(w1, w2, compute, transposed)'s output for these sizes.  (The
+    library gets bare pointers: scales of another precision have other sizes, and would be read past their end.)"""
+    u8, f32 = torch.uint8, torch.float32
+    what = "cached transposed weights" if transposed else "cached weights"
+    if len(w_quant) != 4:
+        raise ValueError(f"{what}: 4 tensors, got {len(w_quant)}")
+    for t, name, (n, k) in zip((w_quant[:2], w_quant[2:]), ("w1", "w2"),
+                               ((H, 2 * I), (I, H)) if transposed else ((2 * I, H), (H, I))):
+        scales = {"mxfp8": ((E, n, k // 32), u8), "fp8": ((E,), f32),
+                  "fp8_block": ((E, (n + 127) // 128, k // 128), f32)}[compute]
+        _shape(t[0], (E, n, k), u8, device, f"{what} ({compute}): codes of {name}")
+        _shape(t[1], *scales, device, f"{what} ({compute}): scales of {name}")
+
+
 def _scratch(nbytes: int, device: torch.device) -> Optional[torch.Tensor]:
     """A workspace of the call's own (None for 0 bytes): a captured call keeps it in its graph's memory."""
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
@@ -792,9 +807,8 @@ def moe_grouped_mlp_fwd(x: torch.Tensor, topk_idx: torch.Tensor, topk_prob: torc
         wqt = (u8(E, Hh, 2 * I), u8(E, Hh, 2 * I // 32), u8(E, I, Hh), u8(E, I, Hh // 32))
         a.w1tq_out, a.w1ts_out, a.w2tq_out, a.w2ts_out = (t.data_ptr() for t in wqt)
     if w_quant is not None:
-        for t in w_quant:
-            if t.device != dev:
-                raise TypeError(f"cached weights must be on {dev}")
+        if compute != "bf16":                # (which has none: the library refuses them)
+            _cached(w_quant, compute, False, E, H, I, dev)
         if compute in ("fp8", "fp8_block"):
             a.w1q, a.w1_scale, a.w2q, a.w2_scale = (_ptr(t) for t in w_quant)
         else:
@@ -871,10 +885,8 @@ def _bwd_args(dy: torch.Tensor, ctx: dict, w1, w2, dw_dtype=torch.float32, w_qua
     if w_quant_t is None:
         w_quant_t = ctx.get("w_quant_t")   # quantized by the forward, if it was asked to
     if w_quant_t is not None:
-        # codes and E8M0 bytes, or (fp8_block) codes and fp32 scales
-        sd = torch.float32 if ctx["compute"] == "fp8_block" else torch.uint8
-        for t, dt in zip(w_quant_t, (torch.uint8, sd, torch.uint8, sd)):
-            _need(t, dt, dev, "cached transposed weights")
+        if ctx["compute"] != "bf16":
+            _cached(w_quant_t, ctx["compute"], True, E, H, I, dev)
         a.w1tq, a.w1ts, a.w2tq, a.w2ts = (_ptr(t) for t in w_quant_t)
     return a, (dx, dprob, dw1, dw2), (w1t, w2t, dw1t, dw2t, w1k, w2k, w_quant_t)
 

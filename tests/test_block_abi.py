@@ -126,3 +126,58 @@ def test_binding_refuses_tensors_off_the_gpu():
         m.fp8_block_grouped_gemm(u8, f4, u8[None], f4, i4)
     with pytest.raises(TypeError):
         m.fp8_block_grouped_wgrad(u8, f4, u8, f4, i4)
+
+
+def _weights(compute, transposed, E=3, H=256, I=384):
+    """Tensors of quantize_weights' shapes."""
+    out = []
+    for n, k in ((H, 2 * I), (I, H)) if transposed else ((2 * I, H), (H, I)):
+        out.append(torch.zeros((E, n, k), dtype=torch.uint8))
+        out.append({"mxfp8": torch.zeros((E, n, k // 32), dtype=torch.uint8), "fp8": torch.zeros(E),
+                    "fp8_block": torch.zeros((E, n // 128, k // 128))}[compute])
+    return tuple(out)
+
+
+@pytest.mark.parametrize("compute", ["mxfp8", "fp8", "fp8_block"])
+def test_cached_weights_of_another_precision_are_refused(compute):
+    """Ahead of the library, which sees pointers only: the scales' sizes differ between the precisions."""
+    import mixture_experts_grouped_permute_amd as m
+    from mixture_experts_grouped_permute_amd import _lib as L
+    T, H, I, E, k = 4, 256, 384, 3, 1
+    x = torch.zeros((T, H), dtype=torch.bfloat16)
+    idx, prob = torch.zeros((T, k), dtype=torch.int32), torch.ones((T, k))
+    w1, w2 = torch.zeros((E, 2 * I, H), dtype=torch.bfloat16), torch.zeros((E, H, I), dtype=torch.bfloat16)
+    good = _weights(compute, False)
+    L._cached(good, compute, False, E, H, I, x.device)
+    wrong = [_weights(c, False) for c in ("mxfp8", "fp8", "fp8_block") if c != compute]
+    if compute != "fp8":
+        wrong.append(_weights(compute, True))
+    wrong += [good[2:] + good[:2], good[:3], good[:1] + (good[1][1:],) + good[2:], tuple(t[:2].contiguous() for t in good),
+              good[:3] + (good[3].double(),)]
+    for w in wrong:
+        with pytest.raises((TypeError, ValueError), match="cached weights"):
+            m.moe_grouped_mlp_fwd(x, idx, prob, w1, w2, compute, w_quant=w)
+
+
+@pytest.mark.parametrize("compute", ["mxfp8", "fp8_block"])
+def test_cached_transposed_weights_of_another_form_are_refused(compute):
+    import mixture_experts_grouped_permute_amd as m
+    from mixture_experts_grouped_permute_amd import _lib as L
+    T, H, I, E = 4, 256, 384, 3
+    dy = torch.zeros((T, H), dtype=torch.bfloat16)
+    w1, w2 = torch.zeros((E, 2 * I, H), dtype=torch.bfloat16), torch.zeros((E, H, I), dtype=torch.bfloat16)
+    perm = {n: torch.zeros(c, dtype=torch.int32) for n, c in
+            (("split_sizes", E), ("offsets", E + 1), ("row_id_map", T), ("src_index", T))}
+    perm["prob_perm"] = torch.zeros(T)
+    saved = {n: torch.zeros((T, c), dtype=torch.bfloat16) for n, c in (("x_perm", H), ("gu", 2 * I), ("h", I))}
+    ctx = {"perm": perm, "saved": saved, "compute": compute, "E": E, "I": I}
+    good = _weights(compute, True)
+    L._cached(good, compute, True, E, H, I, dy.device)
+    other = "mxfp8" if compute == "fp8_block" else "fp8_block"
+    for w in (_weights(compute, False), _weights(other, True), good[2:] + good[:2], good[:2]):
+        with pytest.raises((TypeError, ValueError), match="cached transposed weights"):
+            m.moe_grouped_mlp_bwd(dy, ctx, w1, w2, w_quant_t=w)
+    # square sizes (2 I = H): the second pair still tells the two forms apart
+    for a, b in ((True, False), (False, True)):
+        with pytest.raises(ValueError, match="cached"):
+            L._cached(_weights(compute, a, H=256, I=128), compute, b, E, 256, 128, dy.device)
