@@ -181,3 +181,15 @@ def test_cached_transposed_weights_of_another_form_are_refused(compute):
     for a, b in ((True, False), (False, True)):
         with pytest.raises(ValueError, match="cached"):
             L._cached(_weights(compute, a, H=256, I=128), compute, b, E, 256, 128, dy.device)
+
+
+def test_stream_handles_without_the_private_accessor(monkeypatch):
+    from types import SimpleNamespace
+    from mixture_experts_grouped_permute_amd import _lib as L
+    dev = torch.device("cuda", 1)
+    asked = []
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: asked.append(d) or SimpleNamespace(cuda_stream=7))
+    monkeypatch.setattr(L, "_raw_stream", None)
+    assert L._stream(dev) == 7 and asked == [dev]
+    monkeypatch.setattr(L, "_raw_stream", lambda index: 100 + index)
+    assert L._stream(dev) == 101
