@@ -321,7 +321,8 @@ moe_status moe_route_balance_bwd(const void* logits, int logits_dtype, const uin
  *          Padding, also behind the last segment, is code 0x00 and (where a
  *          whole block is padding) scale 1.  Offsets outside [0, rows] or
  *          decreasing are clamped on the device.
- * x and q 16-byte aligned, rows < 2^31, 1 <= num_groups <= 256.
+ * x and q 16-byte aligned, 1 <= rows < 2^31 (axis 0: also ceil(rows/16) ceil(cols/512) < 2^24, one launch),
+ * 1 <= num_groups <= 256.
  * ------------------------------------------------------------------------ */
 moe_status fp8_block_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int axis,
                               const int32_t* group_offsets, int num_groups, uint8_t* q, float* scales,

@@ -187,10 +187,11 @@ FwdPlan plan_fwd(const moe_mlp_fwd_args* a, void* ws) {
 }
 
 // 32-bit buffer ranges of the block-scaled products over R rows: the row scales of an operand
-// [R, K], K <= max(H, 2I), and 256 rows of a [R, 2I] output or operand
+// [R, K], K <= max(H, 2I), and 256 rows of a [R, 2I] output or operand; and the row quantizer's launch (the
+// SwiGLU kernels' 32 and, backward, 4 rows a workgroup fit a launch wherever these ranges hold)
 bool block_sizes_ok(int64_t R, int64_t H, int64_t I) {
   const int64_t K = H > 2 * I ? H : 2 * I;
-  return K / 128 * R * 4 < (int64_t)UINT32_MAX && 256 * K * 4 < (int64_t)UINT32_MAX;
+  return K / 128 * R * 4 < (int64_t)UINT32_MAX && 256 * K * 4 < (int64_t)UINT32_MAX && block_rows_fits(R, H);
 }
 
 moe_status validate_fwd(const moe_mlp_fwd_args* a) {
@@ -803,7 +804,7 @@ moe_status fp8_block_quantize(const void* x, int x_dtype, int64_t rows, int64_t 
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   const bool f32 = x_dtype == MOE_F32;
   if (axis == 0) {
-    MOE_CHECK(cols % 128 == 0, MOE_ERR_UNSUPPORTED);
+    MOE_CHECK(cols % 128 == 0 && block_rows_fits(rows, cols), MOE_ERR_UNSUPPORTED);
     HIP_TRY(launch_block_rows(x, f32, rows, cols, nullptr, 1, nullptr, q, scales, st));
     return MOE_OK;
   }

@@ -323,9 +323,15 @@ __global__ __launch_bounds__(256) void block_tile_kernel(const TileP p, const WT
 
 }  // namespace
 
+namespace {
+int64_t block_rows_groups(int64_t rows, int64_t cols) { return (rows + kRowTile - 1) / kRowTile * ((cols + 511) / 512); }
+}  // namespace
+
+bool block_rows_fits(int64_t rows, int64_t cols) { return block_rows_groups(rows, cols) < ((int64_t)1 << 32) / 256; }
+
 hipError_t launch_block_rows(const void* x, bool x_f32, int64_t rows, int64_t cols, const int32_t* src_index, int src_k,
                              const int32_t* live, uint8_t* q, float* scales, hipStream_t st) {
-  const dim3 grid((unsigned)((rows + kRowTile - 1) / kRowTile * ((cols + 511) / 512)));
+  const dim3 grid((unsigned)block_rows_groups(rows, cols));
   if (x_f32) block_rows_kernel<true><<<grid, 256, 0, st>>>(x, rows, cols, src_index, src_k, live, q, scales);
   else block_rows_kernel<false><<<grid, 256, 0, st>>>(x, rows, cols, src_index, src_k, live, q, scales);
   return hipGetLastError();

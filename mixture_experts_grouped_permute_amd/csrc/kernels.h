@@ -191,6 +191,8 @@ hipError_t launch_route_balance_bwd(const void* logits, bool f32, const uint8_t*
 // src_index[r] / src_k of x.
 // rows: codes [rows, cols], scales [cols / 128, rows]; cols % 128 == 0.  live (optional, device): only the
 // first *live rows are read and written.
+// (a launch takes fewer than 2^32 threads: whether these sizes keep to it)
+bool block_rows_fits(int64_t rows, int64_t cols);
 hipError_t launch_block_rows(const void* x, bool x_f32, int64_t rows, int64_t cols, const int32_t* src_index, int src_k,
                              const int32_t* live, uint8_t* q, float* scales, hipStream_t st);
 // tokens: segments padded to 128 rows, codes [cols, rows_pad], scales [rows_pad / 128, cols]; cols % 8 == 0.

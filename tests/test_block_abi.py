@@ -193,3 +193,17 @@ def test_stream_handles_without_the_private_accessor(monkeypatch):
     assert L._stream(dev) == 7 and asked == [dev]
     monkeypatch.setattr(L, "_raw_stream", lambda index: 100 + index)
     assert L._stream(dev) == 101
+
+
+def test_rows_past_one_launch_are_refused(lib):
+    """2^32 threads or more: refused with the sizes, not by the launch."""
+    _, uns, _ = _codes()
+    f = lib.fp8_block_quantize
+    for rows, cols in ((1 << 28, 128), ((1 << 27) + 1, 640), ((1 << 31) - 1, 512)):
+        assert f(P, 1, rows, cols, 0, None, 0, P, P, None) == uns, (rows, cols)
+    from mixture_experts_grouped_permute_amd._lib import FwdArgs
+    tab = (ctypes.c_void_p * 2)(P, P)
+    for T, want in ((1 << 28, False), ((1 << 28) - 16, True)):
+        a = FwdArgs(T=T, H=128, I=128, E=2, k=1, compute=4, io_dtype=1, x=P, topk_idx=P, topk_prob=P, w1=tab, w2=tab,
+                    out=P, split_sizes=P, offsets=P, row_id_map=P, src_index=P, prob_perm=P)
+        assert (lib.moe_grouped_mlp_fwd_workspace(ctypes.byref(a)) > 0) == want, T
