@@ -747,9 +747,16 @@ __global__ __launch_bounds__(64 * kFewWaves) void blk_few_kernel(const BlkKArgs 
 }
 
 // Whether a product of so many rows is one of few: 8 an expert on average (64 rows of 8 experts, 4096 x 14336:
-// 89 us here, 96 in the kernel of 256-row tiles; 100 rows: 111 and 97), or 16 in all (one expert's 16
-// rows, 4096 x 14336: 20 and 24).
-bool few_rows(int64_t R, int E) { return R <= kFewRows || R <= 8 * (int64_t)E; }
+// 91 us here, 94 in the kernel of 256-row tiles; 100 rows: 111 and 97), or 16 in all (one expert's 16
+// rows, 4096 x 14336: 20 and 24), but 512 at most.  The host does not know how the rows spread, and each 16 of an
+// expert's read its weights again.  Measured here and there, in us, with 2816 x 2048 weights of 256 experts, rows
+// spread evenly, by Zipf's law (exponent 1.2), over 8 experts, on one:
+//    512 rows  222 246 | 124 140 |  43 34 |  38 39
+//   1024 rows  254 282 | 180 174 |  73 40 |  68 41
+//   2048 rows  287 284 | 279 234 | 133 47 | 129 48
+// (64 rows all on one of 8 experts, 28672 x 4096, which nothing here rules out: 80 and 36; evenly 169 and 218.)
+constexpr int64_t kFewMost = 512;
+bool few_rows(int64_t R, int E) { return R <= kFewRows || R <= std::min(8 * (int64_t)E, kFewMost); }
 
 // A part writes its rows' fp32 sums and reads them back once: a full tile's 256 rows take about as long as
 // 9 blocks' products, a few rows next to nothing.  rows: of a tile, on average.  (At 2000 rows x 1024 x 8192

@@ -207,3 +207,12 @@ def test_rows_past_one_launch_are_refused(lib):
         a = FwdArgs(T=T, H=128, I=128, E=2, k=1, compute=4, io_dtype=1, x=P, topk_idx=P, topk_prob=P, w1=tab, w2=tab,
                     out=P, split_sizes=P, offsets=P, row_id_map=P, src_index=P, prob_perm=P)
         assert (lib.moe_grouped_mlp_fwd_workspace(ctypes.byref(a)) > 0) == want, T
+
+
+def test_products_of_few_rows_end_at_512(lib):
+    """Products of few rows, which read the weights once for 16 rows of an expert and need no scratch, are
+    bounded in rows as well as in rows an expert."""
+    size = lib.fp8_block_grouped_gemm_workspace
+    for R, E, few in ((512, 256, True), (513, 256, False), (2048, 256, False), (512, 64, True), (513, 64, False),
+                      (16, 1, True), (17, 1, False), (64, 8, True), (65, 8, False)):
+        assert (size(R, 512, 8192, E, 1) == 0) == few, (R, E)

@@ -331,3 +331,15 @@ def test_block_refusals_on_the_gpu():
     qa, sa = m.fp8_block_quantize(x, axis=1, group_offsets=o)
     with pytest.raises(ValueError):
         m.fp8_block_grouped_wgrad(qa, sa, qa, sa[:2].contiguous(), o)
+
+
+# both sides of the limit on products of few rows, over all 256 experts
+FEW_LIMIT = [("few-512", [2] * 250 + [0] * 4 + [5, 7], 272, 640), ("tiles-768", [3] * 250 + [0] * 4 + [11, 7], 272, 640),
+             ("tiles-crowded", [0] * 100 + [520] + [0] * 155, 272, 640)]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("name,sizes,N,K", FEW_LIMIT, ids=[c[0] for c in FEW_LIMIT])
+def test_grouped_gemm_of_many_experts(name, sizes, N, K, dtype):
+    test_grouped_gemm(name, sizes, N, K, dtype)
