@@ -343,3 +343,34 @@ FEW_LIMIT = [("few-512", [2] * 250 + [0] * 4 + [5, 7], 272, 640), ("tiles-768", 
 @pytest.mark.parametrize("name,sizes,N,K", FEW_LIMIT, ids=[c[0] for c in FEW_LIMIT])
 def test_grouped_gemm_of_many_experts(name, sizes, N, K, dtype):
     test_grouped_gemm(name, sizes, N, K, dtype)
+
+
+# More tiles than the persistent grid's 256 workgroups, in either output type: workgroups take a second and third
+# tile, whole rounds are followed by a split one, the weight gradient's rounds alternate in direction.
+GEMM_ROUNDS = [
+    ("two-rounds", [4500], 4144, 384),                     # 306 tiles (fp32: 594)
+    ("round-then-split", [4500], 4144, 2560),              # the last 50 (82) in two parts each
+    ("partial-then-split", [(7 * i) % 41 for i in range(30)], 2320, 1024),   # edges of few rows, 4 parts
+    ("join-walk-bf16", [2560], 2000, 2560),                # 80 split tiles of 32 row groups: the join's
+    ("join-walk-f32", [2560], 1008, 2560),                 # 2048 workgroups go round, past an odd last column
+]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("name,sizes,N,K", GEMM_ROUNDS, ids=[c[0] for c in GEMM_ROUNDS])
+def test_grouped_gemm_of_several_rounds(name, sizes, N, K, dtype):
+    test_grouped_gemm(name, sizes, N, K, dtype)
+
+
+WGRAD_ROUNDS = [
+    ("rounds", [700, 0, 129, 300, 1], 1040, 2816),         # 275 tiles (fp32: 550) of 0 to 6 blocks
+    ("rounds-then-split", [385 + (i * 53) % 400 for i in range(130)], 16, 512),   # the last 4 (8) in two parts each
+]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("name,sizes,N,K", WGRAD_ROUNDS, ids=[c[0] for c in WGRAD_ROUNDS])
+def test_grouped_wgrad_of_several_rounds(name, sizes, N, K, dtype):
+    test_grouped_wgrad(name, sizes, N, K, dtype)

@@ -169,3 +169,30 @@ def test_router_and_experts_together():
         _step(*args)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((o2, l2, dx2, a2, b2, c2), want))
+
+
+@gpu
+@pytest.mark.parametrize("dw", [torch.float32, torch.bfloat16], ids=["dw-f32", "dw-bf16"])
+def test_weight_gradients_split_along_the_tokens(dw):
+    """Few, long tiles: the layer's weight gradients are split into parts and joined through its table of
+    outputs and its own scratch, to the bits of the operators called one by one."""
+    m = need_gpu()
+    case = (6000, 128, 128, 2, 1, "bf16", [5900, 100])
+    cfg, inp = _inputs(case)
+    log(f"fp8_block mlp {case} {dw}")
+    d = inp.to("cuda")
+    w1, w2 = [w.clone() for w in d.w1], [w.clone() for w in d.w2]
+    out, ctx = m.moe_grouped_mlp_fwd(d.x, d.topk_idx, d.topk_prob, w1, w2, "fp8_block", save_for_backward=True)
+    dx, dprob, dw1, dw2 = m.moe_grouped_mlp_bwd(d.dy, ctx, w1, w2, dw_dtype=dw)
+    off = ctx["perm"]["offsets"]
+    dz = d.dy[ctx["perm"]["src_index"].long()].contiguous()
+    dzt = m.fp8_block_quantize(dz, axis=1, group_offsets=off)
+    ht = m.fp8_block_quantize(ctx["saved"]["h"], axis=1, group_offsets=off)
+    alone = m.fp8_block_grouped_wgrad(*dzt, *ht, off, out_dtype=dw)
+    torch.cuda.synchronize()
+    fw, bw = _oracle(cfg, inp)
+    errs = {n: mlp.normwise_rel_err(to_np(g), r) for n, g, r in
+            (("out", out, fw.out), ("dx", dx, bw.dx), ("dprob", dprob, bw.dprob), ("dw1", dw1, bw.dw1), ("dw2", dw2, bw.dw2))}
+    log(" ".join(f"{k}={v:.2e}" for k, v in errs.items()))
+    assert all(v < MXFP8_TOL for v in errs.values()), errs
+    assert torch.equal(dw2, alone)

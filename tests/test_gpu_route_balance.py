@@ -265,3 +265,26 @@ def test_a_nan_is_selected_ahead_of_infinity(dtype):
     torch.cuda.synchronize()
     assert idx.tolist() == [[9, 2, 0, 1], [3, 19, 0, 18], [1, 5, 4, 0]]
     assert torch.isnan(prob).all() and torch.isnan(losses).all()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_wide_rows_of_several_turns(dtype):
+    """More tokens than the widest rows' kernels hold at once, forward (16384) and backward (20480)."""
+    m = need_gpu()
+    T, E, k = 20993, 131, 7
+    lg, mask = _logits(T, E, "normal", dtype), _mask(T, True)
+    idx, prob, counts, losses = m.moe_route_balance(lg.cuda(), k, token_mask=_gpu(mask))
+    dprob = torch.from_numpy(np.random.default_rng(1).standard_normal((T, k)).astype(np.float32))
+    dl = torch.tensor([0.8, 0.05])
+    out = m.moe_route_balance_bwd(lg.cuda(), idx, prob, counts, dprob.cuda(), dl.cuda(), token_mask=_gpu(mask))
+    torch.cuda.synchronize()
+    ri, rp, rc, rl = balance.forward(lg, k, mask.numpy())
+    np.testing.assert_array_equal(idx.cpu().numpy(), ri)
+    np.testing.assert_array_equal(counts.cpu().numpy(), rc)
+    assert np.abs(prob.cpu().double().numpy() - rp).max() <= 40 * U
+    assert (np.abs(losses.cpu().double().numpy() - rl) <= 80 * U * np.abs(rl)).all()
+    want, mag = balance.backward(lg, ri, prob.cpu().numpy(), rc, dprob.numpy(), dl.numpy(), mask.numpy())
+    err = np.abs(out.cpu().double().numpy() - want)
+    tol = 48 * U * mag + np.abs(want) * float(torch.finfo(dtype).eps) / 2 + 1e-37
+    assert (err <= tol).all(), float((err / tol).max())
