@@ -68,7 +68,7 @@ typedef enum {
 #define MOE_MAX_EXPERTS 256
 #define MOE_MAX_TOPK 16
 
-/* Version of this ABI (bumped on any incompatible change). */
+/* Version of this ABI (bumped on any incompatible change; entry points and enum values may be added to one). */
 int moe_abi_version(void);
 
 /* ------------------------------------------------------------------------
@@ -263,9 +263,9 @@ moe_status moe_route_permute(const void* logits, int logits_dtype, const void* x
  *               losses[1] = 1/n sum_t (log sum_e exp logits[t, e])^2
  *             0 when nothing counts.
  * A token without a logit above -inf gets expert ids 0 .. k-1 with
- * probability 0 and does not count.  A NaN logit is selected first; NaN and
- * +inf make the token's probabilities and both losses NaN.  Ids are always in
- * range.
+ * probability 0 and does not count.  A NaN logit, of either sign, is selected
+ * first, ahead of +inf (several: lower expert id first); NaN and +inf make the
+ * token's probabilities and both losses NaN.  Ids are always in range.
  * 1 <= k <= min(E, 16), E <= 256.  workspace: at least
  * moe_route_balance_workspace(T, E) bytes (device, 16-byte aligned, caller-
  * owned; nothing in it is read before it is written, nothing is kept from call
@@ -302,9 +302,9 @@ moe_status moe_route_balance_bwd(const void* logits, int logits_dtype, const uin
  *
  * x        [rows, cols] in x_dtype (MOE_F32 or MOE_BF16), device.
  * Per block: amax = max |v|; d = amax / 448 and f = 448 / amax as fp32
- *          divisions rounded to nearest, d not below and 1 / f not above the
- *          smallest normal number's range (d >= 2^-126, f <= 2^126); amax = 0
- *          gives d = f = 1.  code = E4M3FN(fp32(v f)), nearest even; a code
+ *          divisions rounded to nearest, neither d nor 1 / f below the smallest
+ *          normal number (d >= 2^-126, f <= 2^126); amax = 0 gives d = f = 1.
+ *          code = E4M3FN(fp32(v f)), nearest even; a code
  *          stands for decode(code) * d.  A block with an infinite or NaN value
  *          decodes to infinities and NaN only.
  * axis 0:  blocks of 128 consecutive values along cols (cols % 128 == 0).
@@ -364,7 +364,7 @@ moe_status fp8_block_quantize_weights(const void* const* w, int E, int64_t rows,
  *          instructions, which are twice as fast and align the products of a
  *          group to its largest one (about 1e-5 normwise, under the rounding
  *          of the output).
- * K % 128 == 0, N % 16 == 0 (else MOE_ERR_UNSUPPORTED); pointers of codes and
+ * R >= 1; K % 128 == 0, N % 16 == 0 (else MOE_ERR_UNSUPPORTED); pointers of codes and
  * out 16-byte aligned; 256 K, 256 N * 4 and R K / 32 below 2^32.
  * workspace: fp8_block_grouped_gemm_workspace bytes (device, 16-byte aligned;
  * 0 for some sizes, then NULL will do): fp32 sums of tiles that are split
@@ -450,7 +450,8 @@ moe_status fp8_block_grouped_wgrad(const uint8_t* dyt, const float* dyt_scales, 
  * and w2_scale [E] fp32 scales s, device (ABI version 3); and for
  * MOE_FP8_BLOCK, the same fields with w1_scale [E, 2I/128, H/128] and w2_scale
  * [E, H/128, I/128].  Any other mix of the six cached-weight fields is
- * MOE_ERR_INVALID_ARG.
+ * MOE_ERR_INVALID_ARG.  These are pointers: that the scales are of the call's
+ * precision and sizes is the caller's to see to.
  * error_flag: optional device int32 that receives the permutation's flag for
  * out-of-range expert ids (0 or 1) instead of the first 4 bytes of the
  * workspace, so that it stays readable after later calls reuse the workspace

@@ -13,9 +13,10 @@
 // experts s, s + L, ... in registers: the row's statistics, its top-k and its gradient need no second
 // read and no LDS, and the lanes of a load cover whole 64-byte pieces of a row for any E.
 //
-// Measured: forward 131072 x 256 f32, k = 8: 45 us and 4 for the totals, of 28 that its bytes take; the VALU
-// issues 74 % of the time, most of it the selection (sorting networks, 16 of a lane's 16 logits into
-// lists of 8, four merges).  256 x 4: 6.3 us, a launch.  Backward 131072 x 256 f32: 50 us, 5.6 TB/s.
+// Measured: forward 131072 x 256 f32, k = 8: 46 us and 4 for the totals, of 28 that its bytes take; the VALU
+// issues 76 % of the time, most of it the selection (sorting networks, 16 of a lane's 16 logits into
+// lists of 8, four merges); bf16 44 us with the totals, of 15.  256 x 4: 6.4 us, a launch.  Backward
+// 131072 x 256 f32: 49 us, 5.6 TB/s; bf16 36.
 #include "common.h"
 #include "kernels.h"
 
@@ -554,8 +555,9 @@ template <bool kF32>
 void launch_bwd(const BwdP& p, hipStream_t st) {
   const int L = p.E <= 8 ? 8 : 16;
   const int64_t need = (p.T * L + kBwdThreads - 1) / kBwdThreads;
-  // 8 workgroups of 4 waves per CU; of the widest rows' kernel, whose 73 registers leave room for 6, 5, so that
-  // none waits for a second turn (131072 x 256 f32: 53.5 -> 49.9 us; 131072 x 64 bf16: 14.2 us with 8, 14.7 with 5)
+  // 8 workgroups of 4 waves per CU; of the widest rows' kernel, whose 73 registers leave room for 6, 5: with 8 some
+  // would wait for a second turn (131072 x 256 f32: 53.5 us, 49.9 with 5; 5 and 6 are alike: f32 48.9 and 48.5, bf16
+  // 35.8 and 36.1; 131072 x 64 bf16: 14.2 us with 8, 14.7 with 5)
   const int64_t most = p.E > 128 ? 1280 : 2048;
   const int nb = (int)(need < most ? need : most);
   if (p.E <= 8) route_balance_bwd_kernel<kF32, 8, 1><<<nb, kBwdThreads, 0, st>>>(p);

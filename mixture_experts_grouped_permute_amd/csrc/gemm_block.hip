@@ -20,6 +20,7 @@
 // codes, under a bf16 output's own 1.7e-3, but not what an fp32 output promises.  The same codes,
 // converted to bf16 (exact) and multiplied by v_mfma_f32_16x16x32_bf16, gave 1e-8.  That costs twice the
 // matrix cycles and 16 registers per converted fragment, so its waves own 64 x 64 of a 256 x 128 tile.
+// (16384 x 4096 x 14336: 1627 us, of 1607 at a large bf16 library product's rate, where bf16 outputs take 810-840.)
 //
 // A stage is one block of K: 128 bytes of 256 A rows and 256 B rows, loaded straight to LDS into one
 // of two buffers while the other is multiplied, with the stage's 512 scales beside them.  Tiles are
@@ -672,7 +673,7 @@ __device__ __forceinline__ i32x8 load256(const rsrc_t& r, uint32_t off) {
 // its own, and with a workgroup for each of min(R, E) N / (16 kCols) possible tiles, 8 rows of 8 experts
 // (28672 x 4096) took 99 and 90 us, against 91; rows that crowd on one expert, 38 and 128.
 // Measured: 8 rows, 28672 x 4096, 4.3 experts chosen: 91 us (5.6 TB/s of weights), 117 in the kernel above;
-// one row, 4096 x 14336: 16, was 22.
+// one row, 4096 x 14336: 16, was 22.  fp32 outputs, on one box: 83 us (bf16 82; 4 experts) and 17 (15).
 constexpr int kFewRows = 16, kFewWaves = 4, kFewGrid = 6 * kGemmGrid;
 template <bool kWide, int kCols, int kUnroll>
 __global__ __launch_bounds__(64 * kFewWaves) void blk_few_kernel(const BlkKArgs p) {
@@ -811,8 +812,9 @@ hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t st) {
   const int join_grid = std::min(kJoinGrid, (kGemmGrid - 1) * ((k.part_rows + kJoinRows - 1) / kJoinRows));
   k.part = split ? g.part : nullptr;
   // Products whose experts have two tiles of rows or fewer, on average, are mostly edges: skipping the
-  // empty halves took 100 rows x 4096 x 14336 (8 experts) from 109 to 94 us, 500 x 2048 x 4096 from 45 to
-  // 36; the branch costs the full tiles 1 % (16384 x 4096 x 14336: 843 and 852 us).
+  // empty halves takes 100 rows x 4096 x 14336 (8 experts) from 100 to 94 us, 500 x 2048 x 4096 (8) from 31 to
+  // 28, and 500 rows of one or two experts nowhere (34-36); the branch costs the full tiles 1 % (16384 x 4096 x
+  // 14336: 843 and 852 us).  The join runs wherever these sizes could be split: 4-5 us where nothing was.
   const bool partial = !g.wgrad && g.rows < 2 * kBM * (int64_t)g.E;
   auto launch = [&](auto wg, auto wide) {
     constexpr bool kWg = decltype(wg)::value, kWd = decltype(wide)::value;
