@@ -673,7 +673,7 @@ __device__ __forceinline__ i32x8 load256(const rsrc_t& r, uint32_t off) {
 // its own, and with a workgroup for each of min(R, E) N / (16 kCols) possible tiles, 8 rows of 8 experts
 // (28672 x 4096) took 99 and 90 us, against 91; rows that crowd on one expert, 38 and 128.
 // Measured: 8 rows, 28672 x 4096, 4.3 experts chosen: 91 us (5.6 TB/s of weights), 117 in the kernel above;
-// one row, 4096 x 14336: 16, was 22.  fp32 outputs, on one box: 83 us (bf16 82; 4 experts) and 17 (15).
+// one row, 4096 x 14336: 16, was 22.  fp32 outputs 83 us where bf16 took 82 (4 experts), and 17 (15).
 constexpr int kFewRows = 16, kFewWaves = 4, kFewGrid = 6 * kGemmGrid;
 template <bool kWide, int kCols, int kUnroll>
 __global__ __launch_bounds__(64 * kFewWaves) void blk_few_kernel(const BlkKArgs p) {
