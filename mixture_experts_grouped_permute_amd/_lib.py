@@ -268,12 +268,17 @@ class _Workspace:
     allocates).  Calls on one stream run in order, so they can share its buffer; calls on
     different streams get different buffers.  A grown buffer replaces the old one, which stays
     valid for the kernels already enqueued: it was allocated on that same stream, so torch's
-    allocator reuses its memory only in that stream's order."""
+    allocator reuses its memory only in that stream's order.
+    A captured call gets a buffer of its own, in its graph's memory, and nobody keeps it: graphs
+    captured on one stream may be replayed on several at once."""
 
     def __init__(self):
         self.buf = {}
 
     def get(self, nbytes: int, device: torch.device) -> torch.Tensor:
+        with _Device(device):
+            if torch.cuda.is_current_stream_capturing():
+                return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
         stream = torch.cuda.current_stream(device)
         key = (device.type, device.index, stream.cuda_stream)
         b = self.buf.get(key)
@@ -281,6 +286,9 @@ class _Workspace:
             b = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
             self.buf[key] = b
         return b
+
+    def holds(self, t: torch.Tensor) -> bool:
+        return any(b is t for b in self.buf.values())
 
 
 _WS = _Workspace()
@@ -828,7 +836,7 @@ def moe_grouped_mlp_fwd(x: torch.Tensor, topk_idx: torch.Tensor, topk_prob: torc
     a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
     _check(lib.moe_grouped_mlp_fwd(ctypes.byref(a), _stream(dev)), "moe_grouped_mlp_fwd")
     ctx = {"perm": perm, "saved": saved, "compute": compute, "E": E, "I": I, "error_flag": flag,
-           "workspace": ws, "_keep": keep, "w_quant_t": wqt}
+           "workspace": ws if workspace is not None or _WS.holds(ws) else None, "_keep": keep, "w_quant_t": wqt}
     if debug is not None:
         ctx["debug"] = debug
     return out, ctx
@@ -855,7 +863,7 @@ def moe_grouped_mlp_fwd_loop(x: torch.Tensor, topk_idx: torch.Tensor, topk_prob:
     a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
     counts = (_i32 * E)(*[int(c) for c in split_sizes_host])
     _check(lib.moe_grouped_mlp_fwd_loop(ctypes.byref(a), counts, _stream(dev)), "moe_grouped_mlp_fwd_loop")
-    return out, {"perm": perm, "error_flag": flag, "workspace": ws, "_keep": keep}
+    return out, {"perm": perm, "error_flag": flag, "workspace": ws if _WS.holds(ws) else None, "_keep": keep}
 
 
 def _bwd_args(dy: torch.Tensor, ctx: dict, w1, w2, dw_dtype=torch.float32, w_quant_t=None):

@@ -216,3 +216,23 @@ def test_products_of_few_rows_end_at_512(lib):
     for R, E, few in ((512, 256, True), (513, 256, False), (2048, 256, False), (512, 64, True), (513, 64, False),
                       (16, 1, True), (17, 1, False), (64, 8, True), (65, 8, False)):
         assert (size(R, 512, 8192, E, 1) == 0) == few, (R, E)
+
+
+def test_captured_calls_share_no_workspace(monkeypatch):
+    """Eager calls of a stream share its buffer; a captured one has its own, which is not kept: two graphs captured
+    on one stream may be replayed at once on two."""
+    from types import SimpleNamespace
+    from mixture_experts_grouped_permute_amd import _lib as L
+    capturing = [False]
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: SimpleNamespace(cuda_stream=7))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    ws, cpu = L._Workspace(), torch.device("cpu")
+    a = ws.get(1000, cpu)
+    assert ws.get(500, cpu) is a
+    capturing[0] = True
+    b, c = ws.get(500, cpu), ws.get(500, cpu)
+    assert len({t.data_ptr() for t in (a, b, c)}) == 3
+    assert ws.holds(a) and not ws.holds(b) and not ws.holds(c)
+    capturing[0] = False
+    assert ws.get(500, cpu) is a

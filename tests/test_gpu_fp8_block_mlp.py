@@ -196,3 +196,39 @@ def test_weight_gradients_split_along_the_tokens(dw):
     log(" ".join(f"{k}={v:.2e}" for k, v in errs.items()))
     assert all(v < MXFP8_TOL for v in errs.values()), errs
     assert torch.equal(dw2, alone)
+
+
+@gpu
+@pytest.mark.parametrize("compute", ["bf16", "mxfp8", "fp8_block"])
+def test_graphs_of_two_layers_replayed_at_once(compute):
+    """Forward and backward of two layers, each captured with the workspaces that the calls take by themselves, on two
+    streams."""
+    m = need_gpu()
+    log(f"two graphs {compute}")
+    steps = []
+    for case in ((300, 256, 384, 4, 2, "bf16", None), (257, 384, 256, 5, 1, "bf16", None)):
+        cfg, inp = _inputs(case)
+        d = inp.to("cuda")
+
+        def step(d=d):
+            out, ctx = m.moe_grouped_mlp_fwd(d.x, d.topk_idx, d.topk_prob, d.w1, d.w2, compute, save_for_backward=True)
+            return (out, *m.moe_grouped_mlp_bwd(d.dy, ctx, d.w1, d.w2))
+        steps.append(step)
+    want = [s() for s in steps]
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for s in steps:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(s())
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in steps]
+    for _ in range(4):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+        steps[0]()
+        torch.cuda.synchronize()
