@@ -451,7 +451,8 @@ moe_status fp8_block_grouped_wgrad(const uint8_t* dyt, const float* dyt_scales, 
  * MOE_FP8_BLOCK, the same fields with w1_scale [E, 2I/128, H/128] and w2_scale
  * [E, H/128, I/128].  Any other mix of the six cached-weight fields is
  * MOE_ERR_INVALID_ARG.  These are pointers: that the scales are of the call's
- * precision and sizes is the caller's to see to.
+ * precision and sizes is the caller's to see to.  MOE_FP8_BLOCK: codes 16-byte
+ * aligned, as in fp8_block_grouped_gemm.
  * error_flag: optional device int32 that receives the permutation's flag for
  * out-of-range expert ids (0 or 1) instead of the first 4 bytes of the
  * workspace, so that it stays readable after later calls reuse the workspace
@@ -558,7 +559,8 @@ const char* moe_fwd_phase_name(int i);   /* NULL when out of range */
  * w1tq, w1ts, w2tq, w2ts: optional (MXFP8, FP8_BLOCK; all four or none, else
  * MOE_ERR_INVALID_ARG): the transposed weights of the dgrad GEMMs quantized
  * once by the caller -- mxfp8_quantize_weights(w1, E, 2I, H, axis 1) and
- * mxfp8_quantize_weights(w2, E, H, I, axis 1).  Without them the backward
+ * mxfp8_quantize_weights(w2, E, H, I, axis 1).  Under FP8_BLOCK these codes and
+ * every dw1[e], dw2[e] are 16-byte aligned.  Without them the backward
  * quantizes them itself on every call (one launch per weight table, experts
  * without tokens skipped).
  * Under MXFP8 the FC2 dgrad epilogue quantizes dgu itself (page "BioNeMo Uses

@@ -31,6 +31,7 @@ struct Carver {
 };
 
 inline bool io_ok(int d) { return d == MOE_F32 || d == MOE_BF16; }
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline size_t io_size(int d) { return d == MOE_F32 ? 4 : 2; }
 
 struct PermWs {
@@ -232,7 +233,9 @@ moe_status validate_fwd(const moe_mlp_fwd_args* a) {
   // activation or one expert's weight matrix, so the limit is on an expert's weights (in bf16),
   // not on the number of tokens
   if (2 * a->I * a->H * 2 >= (int64_t)UINT32_MAX) return MOE_ERR_UNSUPPORTED;
-  if (a->compute == MOE_FP8_BLOCK && !block_sizes_ok(a->T * a->k, a->H, a->I)) return MOE_ERR_UNSUPPORTED;
+  if (a->compute == MOE_FP8_BLOCK &&
+      (!block_sizes_ok(a->T * a->k, a->H, a->I) || !aligned16(a->w1q) || !aligned16(a->w2q)))
+    return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -359,6 +362,9 @@ moe_status validate_bwd(const moe_mlp_bwd_args* a) {
   if (a->compute == MOE_FP8_BLOCK) {
     const int64_t Rp = block_rows_pad(R, a->E);
     if (!block_sizes_ok(Rp, a->H, a->I) || 256 * Rp >= (int64_t)UINT32_MAX) return MOE_ERR_UNSUPPORTED;
+    if (!aligned16(a->w1tq) || !aligned16(a->w2tq)) return MOE_ERR_UNSUPPORTED;
+    for (int e = 0; e < a->E; ++e)
+      if (!aligned16(a->dw1[e]) || !aligned16(a->dw2[e])) return MOE_ERR_UNSUPPORTED;
   }
   return MOE_OK;
 }
@@ -757,7 +763,6 @@ BalanceWs carve_balance(Carver& c, int64_t T, int E) {
   w.arrived = reinterpret_cast<int*>(c.take(sizeof(int)));
   return w;
 }
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool under_4g(int64_t bytes) { return bytes < (int64_t)UINT32_MAX; }
 }  // namespace
 

@@ -236,3 +236,22 @@ def test_captured_calls_share_no_workspace(monkeypatch):
     assert ws.holds(a) and not ws.holds(b) and not ws.holds(c)
     capturing[0] = False
     assert ws.get(500, cpu) is a
+
+
+def test_layer_refuses_codes_and_gradients_off_16_bytes(lib):
+    """What the block-scaled products refuse by themselves."""
+    _, uns, wsp = _codes()
+    from mixture_experts_grouped_permute_amd._lib import BwdArgs, FwdArgs
+    tab = (ctypes.c_void_p * 2)(P, P)
+    f = dict(T=64, H=128, I=128, E=2, k=1, compute=4, io_dtype=1, x=P, topk_idx=P, topk_prob=P, w1=tab, w2=tab, out=P,
+             split_sizes=P, offsets=P, row_id_map=P, src_index=P, prob_perm=P, w1q=P, w2q=P, w1_scale=P, w2_scale=P)
+    for kw, want in (({}, wsp), (dict(w1q=P + 8), uns), (dict(w2q=P + 4), uns)):
+        a = FwdArgs(**{**f, **kw})
+        assert lib.moe_grouped_mlp_fwd(ctypes.byref(a), None) == want, kw
+    b = dict(T=64, H=128, I=128, E=2, k=1, compute=4, io_dtype=1, dw_dtype=0, dy=P, w1=tab, w2=tab, split_sizes=P, offsets=P,
+             row_id_map=P, src_index=P, prob_perm=P, saved_x_perm=P, saved_gu=P, saved_h=P, dx=P, dprob=P, dw1=tab, dw2=tab,
+             w1tq=P, w1ts=P, w2tq=P, w2ts=P)
+    off = (ctypes.c_void_p * 2)(P, P + 8)
+    for kw, want in (({}, wsp), (dict(w1tq=P + 8), uns), (dict(w2tq=P + 4), uns), (dict(dw1=off), uns), (dict(dw2=off), uns)):
+        a = BwdArgs(**{**b, **kw})
+        assert lib.moe_grouped_mlp_bwd(ctypes.byref(a), None) == want, kw
