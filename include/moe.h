@@ -64,9 +64,18 @@ typedef enum {
   MOE_FP8_BLOCK = 4         /* E4M3FN bytes + one fp32 scale per 1 x 128 (weights: 128 x 128) block */
 } moe_dtype;
 
+/* How moe_route_grouped scores an expert. */
+typedef enum {
+  MOE_SCORE_SOFTMAX = 0,
+  MOE_SCORE_SIGMOID = 1
+} moe_score;
+
 /* Largest supported expert count and experts per token. */
 #define MOE_MAX_EXPERTS 256
 #define MOE_MAX_TOPK 16
+/* Most groups of experts (moe_route_grouped) and gradients in one call (moe_grad_sumsq, moe_grad_clip). */
+#define MOE_MAX_GROUPS 16
+#define MOE_MAX_GRADS 65536
 
 /* Version of this ABI (bumped on any incompatible change; entry points and enum values may be added to one). */
 int moe_abi_version(void);
@@ -296,6 +305,136 @@ moe_status moe_route_balance(const void* logits, int logits_dtype, const uint8_t
 moe_status moe_route_balance_bwd(const void* logits, int logits_dtype, const uint8_t* token_mask, int64_t T, int E,
                                  int k, const int32_t* topk_idx, const float* topk_prob, const int32_t* counts,
                                  const float* dprob, const float* dlosses, void* dlogits, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_route_grouped -- routing by sigmoid or softmax scores, with a bias that
+ * counts in the selection alone (it balances the experts' load without a
+ * loss) and a choice of expert groups ahead of that of the experts.
+ *
+ * logits      [T, E] in logits_dtype (MOE_F32 or MOE_BF16), device.
+ * bias        optional [E] fp32, device.
+ * token_mask  optional device bytes [T]: 0 marks a token whose slots are not
+ *             counted (it is routed like any other).  Needs counts.
+ * With s = sigmoid(logits) or softmax(logits) over all E experts (score), and
+ * c = s + bias, -inf where the logit is -inf:
+ *   The groups of E / groups consecutive experts are ordered by the sum of
+ *   their group_best (1 or 2) largest c; the topk_groups best stay (equal sums:
+ *   lower group), the others' experts get c = -inf.
+ *   topk_idx [T, k] int32: the experts of the k largest c in descending order
+ *   (equal: lower id).
+ *   topk_prob [T, k] fp32: s at topk_idx, 0 where c is -inf; with renormalize
+ *   divided by their sum over the k (0 where that is 0); times scale.
+ * Scores, c and the groups' sums are compared as 64-bit values.  A NaN counts as
+ * the largest (so does the sum of a group that holds one among its best); ids
+ * are always in range.
+ * counts      optional [E] int32 out: slots of the counting tokens at e.
+ * 1 <= k <= min(16, topk_groups E / groups), E <= 256, E % groups == 0,
+ * groups <= 16 (else MOE_ERR_UNSUPPORTED), scale finite and above 0.
+ * workspace: with counts, moe_route_grouped_workspace(T, E) bytes (device,
+ * 16-byte aligned, nothing in it is read before it is written); else unused.
+ * ------------------------------------------------------------------------ */
+size_t moe_route_grouped_workspace(int64_t T, int E);
+moe_status moe_route_grouped(const void* logits, int logits_dtype, const float* bias, const uint8_t* token_mask,
+                             int64_t T, int E, int k, int score, int groups, int topk_groups, int group_best,
+                             int renormalize, float scale, int32_t* topk_idx, float* topk_prob, int32_t* counts,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_route_grouped_bwd -- the gradient of moe_route_grouped's topk_prob with
+ * respect to the logits (the selection, and with it bias and groups, has none).
+ *
+ * logits, score, renormalize, scale, topk_idx, topk_prob: the forward's.
+ * dprob       [T, k] fp32 gradient of topk_prob (moe_grouped_mlp_bwd's dprob).
+ * dlogits     [T, E] out in logits_dtype, with w = topk_prob, g = dprob and
+ *             S = 1 - sigmoid(logit) for sigmoid scores, 1 for softmax ones:
+ *               renormalize: S w_j (g_j - sum_m w_m g_m / scale) at topk_idx[., j],
+ *                            0 elsewhere
+ *               else:        S w_j g_j there; for softmax scores also
+ *                            - softmax(logits)_e sum_m w_m g_m at every expert.
+ *             Computed in fp32, rounded once.  An id that repeats gets all its
+ *             parts, one outside [0, E) none.
+ * ------------------------------------------------------------------------ */
+moe_status moe_route_grouped_bwd(const void* logits, int logits_dtype, int64_t T, int E, int k, int score,
+                                 int renormalize, float scale, const int32_t* topk_idx, const float* topk_prob,
+                                 const float* dprob, void* dlogits, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_add_rmsnorm -- the residual stream's addition and the root-mean-square
+ * norm ahead of the router and the experts.
+ *
+ *   s = x + residual, rounded to x_dtype (without residual: x)
+ *   y = s / sqrt(mean over the row of s^2 + eps) * weight
+ *
+ * x, residual [T, H] in x_dtype (MOE_F32 or MOE_BF16); residual may be NULL.
+ * weight      [H] in w_dtype: x_dtype or MOE_F32.
+ * sum         [T, H] in x_dtype: receives s; given if and only if residual is.
+ *             May be x or residual itself; no other two tensors overlap.
+ * y           [T, H] in x_dtype, or NULL.
+ * q, scales   [T, H] E4M3 codes and [H/128, T] fp32 scales of the unrounded
+ *             y, as fp8_block_quantize (axis 0) gives them: the operand of a
+ *             block-scaled product.  Both or neither; y or q or both.
+ * The sum of squares and everything from it on is fp32, rounded once.
+ * H <= 32768, T < 2^31; with q: H % 128 == 0 and every tensor 16-byte aligned
+ * (else MOE_ERR_UNSUPPORTED).
+ * ------------------------------------------------------------------------ */
+moe_status moe_add_rmsnorm(const void* x, const void* residual, int x_dtype, const void* weight, int w_dtype,
+                           int64_t T, int64_t H, float eps, void* sum, void* y, uint8_t* q, float* scales,
+                           void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_add_rmsnorm_bwd -- the gradient of moe_add_rmsnorm.
+ *
+ * dy          [T, H] gradient of y (rounding and quantization pass it on
+ *             unchanged), s [T, H] the forward's sum (without residual: x),
+ *             dsum [T, H] the gradient that reaches s by other ways, or NULL;
+ *             all in dtype.  weight [H] in w_dtype, as the forward's.
+ * dx          [T, H] out in dtype: the gradient of s, and so of x and of
+ *             residual.  May be dsum itself.  With r = 1 / sqrt(mean s^2 + eps):
+ *               r (dy w - s r mean(dy w s r)) + dsum
+ * dweight     [H] fp32 out: sum over the rows of dy s r.
+ * workspace: moe_add_rmsnorm_bwd_workspace(T, H) bytes (device, 16-byte aligned,
+ * nothing in it is read before it is written).  Limits as the forward's.
+ * ------------------------------------------------------------------------ */
+size_t moe_add_rmsnorm_bwd_workspace(int64_t T, int64_t H);
+moe_status moe_add_rmsnorm_bwd(const void* dy, const void* s, const void* dsum, int dtype, const void* weight,
+                               int w_dtype, int64_t T, int64_t H, float eps, void* dx, float* dweight,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_grad_sumsq -- the sum of squares of many gradients, in 64 bits.  Where
+ * ranks hold parts of them, add up their sums ahead of moe_grad_clip.
+ *
+ * grads       HOST array of n device pointers, numel HOST [n] values of each
+ *             (0: skipped, its pointer may be NULL), dtypes HOST int32 [n]
+ *             (MOE_F32 or MOE_BF16).  Aligned to their type.
+ * sumsq       [1] fp64 out, device.
+ * 1 <= n <= 65536, numel <= 2^38.  workspace: moe_grad_sumsq_workspace(numel, n)
+ * bytes (device, 16-byte aligned, nothing in it is read before it is written).
+ * ------------------------------------------------------------------------ */
+size_t moe_grad_sumsq_workspace(const int64_t* numel, int n);
+moe_status moe_grad_sumsq(const void* const* grads, const int64_t* numel, const int32_t* dtypes, int n,
+                          double* sumsq, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_grad_clip -- gradients scaled so that their global norm is at most
+ * max_norm.
+ *
+ *   norm = sqrt(sumsq);  c = min(1, max_norm / (norm + 1e-6));  out = grads * c
+ *
+ * grads, numel, dtypes, n: as moe_grad_sumsq.
+ * out         HOST array of n device pointers that receive the results, in
+ *             out_dtypes; out[i] may be grads[i] (in place, of one type; then
+ *             nothing is written where c is 1).  Other overlaps between out and
+ *             any tensor of the call are refused (MOE_ERR_INVALID_ARG).
+ * sumsq       [1] fp64, device (moe_grad_sumsq's, or the sum of several).
+ * max_norm    at least 0 (infinity: never scaled).
+ * norm        [1] fp32 out, device.
+ * The product is fp32, rounded once.  An infinite sumsq gives c = 0 (and NaN
+ * at infinite gradients), a NaN one NaN everywhere: test norm.
+ * ------------------------------------------------------------------------ */
+moe_status moe_grad_clip(const void* const* grads, const int64_t* numel, const int32_t* dtypes, int n,
+                         void* const* out, const int32_t* out_dtypes, const double* sumsq, float max_norm,
+                         float* norm, void* stream);
 
 /* ------------------------------------------------------------------------
  * fp8_block_quantize -- E4M3 with one fp32 scale per 128 values.

@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(_HERE, "libmoe.so")
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(5)
 MOE_F32, MOE_BF16, MOE_MXFP8_E4M3, MOE_FP8_E4M3, MOE_FP8_BLOCK = 0, 1, 2, 3, 4
 MAX_EXPERTS = 256
+MOE_SCORES = {"softmax": 0, "sigmoid": 1}
 
 # every symbol include/moe.h declares
 EXPORTS = (
@@ -33,6 +34,9 @@ EXPORTS = (
     "moe_route_balance_workspace", "moe_route_balance", "moe_route_balance_bwd", "fp8_block_quantize",
     "fp8_block_quantize_weights", "fp8_block_grouped_gemm_workspace", "fp8_block_grouped_gemm",
     "fp8_block_grouped_wgrad_workspace", "fp8_block_grouped_wgrad",
+    "moe_route_grouped_workspace", "moe_route_grouped", "moe_route_grouped_bwd", "moe_add_rmsnorm",
+    "moe_add_rmsnorm_bwd_workspace", "moe_add_rmsnorm_bwd", "moe_grad_sumsq_workspace", "moe_grad_sumsq",
+    "moe_grad_clip",
 )
 NOALLOC_SCRATCH_BYTES = 4 << 20    # MOE_NOALLOC_SCRATCH_BYTES
 
@@ -173,6 +177,28 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         f.restype = ctypes.c_int
         f.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, _vp, _vp,
                       ctypes.c_size_t, _vp]
+    _f32, _int = ctypes.c_float, ctypes.c_int
+    lib.moe_route_grouped_workspace.restype = ctypes.c_size_t
+    lib.moe_route_grouped_workspace.argtypes = [_i64, _int]
+    lib.moe_route_grouped.restype = _int
+    lib.moe_route_grouped.argtypes = [_vp, _int, _vp, _vp, _i64, _int, _int, _int, _int, _int, _int, _int, _f32, _vp, _vp,
+                                      _vp, _vp, ctypes.c_size_t, _vp]
+    lib.moe_route_grouped_bwd.restype = _int
+    lib.moe_route_grouped_bwd.argtypes = [_vp, _int, _i64, _int, _int, _int, _int, _f32, _vp, _vp, _vp, _vp, _vp]
+    lib.moe_add_rmsnorm.restype = _int
+    lib.moe_add_rmsnorm.argtypes = [_vp, _vp, _int, _vp, _int, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _vp]
+    lib.moe_add_rmsnorm_bwd_workspace.restype = ctypes.c_size_t
+    lib.moe_add_rmsnorm_bwd_workspace.argtypes = [_i64, _i64]
+    lib.moe_add_rmsnorm_bwd.restype = _int
+    lib.moe_add_rmsnorm_bwd.argtypes = [_vp, _vp, _vp, _int, _vp, _int, _i64, _i64, _f32, _vp, _vp, _vp,
+                                        ctypes.c_size_t, _vp]
+    # (host tables as bare addresses: a GradTable converts them once)
+    lib.moe_grad_sumsq_workspace.restype = ctypes.c_size_t
+    lib.moe_grad_sumsq_workspace.argtypes = [_vp, _int]
+    lib.moe_grad_sumsq.restype = _int
+    lib.moe_grad_sumsq.argtypes = [_vp, _vp, _vp, _int, _vp, _vp, ctypes.c_size_t, _vp]
+    lib.moe_grad_clip.restype = _int
+    lib.moe_grad_clip.argtypes = [_vp, _vp, _vp, _int, _vp, _vp, _vp, _f32, _vp, _vp]
     if path is None:
         _lib = lib
     return lib
@@ -570,6 +596,211 @@ def moe_route_balance_bwd(logits: torch.Tensor, topk_idx: torch.Tensor, topk_pro
                                          _ptr(topk_prob), _ptr(counts), _ptr(dprob), _ptr(dlosses), _ptr(dlogits),
                                          _stream(dev)), "moe_route_balance_bwd")
     return dlogits
+
+
+def _score(score: str) -> int:
+    if score not in MOE_SCORES:
+        raise ValueError(f"score must be one of {sorted(MOE_SCORES)}, got {score!r}")
+    return MOE_SCORES[score]
+
+
+def moe_route_grouped(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None, score: str = "sigmoid",
+                      groups: int = 1, topk_groups: Optional[int] = None, group_best: Optional[int] = None,
+                      renormalize: bool = True, scale: float = 1.0, token_mask: Optional[torch.Tensor] = None,
+                      count: bool = False):
+    """Routing of logits [T, E] (bf16 or f32) by "sigmoid" or "softmax" scores s.  Of the `groups` groups of
+    consecutive experts each token keeps the topk_groups (None: all) with the largest sums of their group_best (1 or
+    2; None: 2, or 1 in groups of one) best s + bias, and of their experts the k with the largest s + bias; equal
+    ones: lower id.  bias: optional float32 [E], which counts in the selection alone.  The weights are s of the
+    selected, with renormalize divided by their sum, times scale.
+    count: also return the slots of each expert; token_mask: optional bool or uint8 [T], tokens whose slots are
+    not counted where it is 0.
+    Returns (topk_idx int32 [T, k], topk_prob float32 [T, k], counts int32 [E] or None)."""
+    lib = load()
+    dev = _on(logits, "logits")
+    T, E = logits.shape
+    _shape(bias, (E,), torch.float32, dev, "bias")
+    _mask(token_mask, T, dev)
+    if token_mask is not None and not count:
+        raise ValueError("token_mask goes with count=True")
+    if topk_groups is None:
+        topk_groups = groups
+    if group_best is None:
+        group_best = min(2, E // groups) if groups > 0 else 0
+    with _Device(dev):
+        idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+        prob = torch.empty((T, k), dtype=torch.float32, device=dev)
+        counts = ws = None
+        if count:
+            counts = torch.empty(E, dtype=torch.int32, device=dev)
+            ws = _scratch(lib.moe_route_grouped_workspace(T, E), dev)
+        _check(lib.moe_route_grouped(_ptr(logits), _io(logits), _ptr(bias), _ptr(token_mask), T, E, k, _score(score),
+                                     groups, topk_groups, group_best, bool(renormalize), scale, idx.data_ptr(),
+                                     prob.data_ptr(), _ptr(counts), _ptr(ws), _nbytes(ws), _stream(dev)),
+               "moe_route_grouped")
+    return idx, prob, counts
+
+
+def moe_route_grouped_bwd(logits: torch.Tensor, topk_idx: torch.Tensor, topk_prob: torch.Tensor, dprob: torch.Tensor,
+                          score: str = "sigmoid", renormalize: bool = True, scale: float = 1.0):
+    """Gradient of moe_route_grouped's topk_prob with respect to the logits, in their dtype.  topk_idx, topk_prob,
+    score, renormalize, scale: the forward's; dprob: gradient of topk_prob (float32 [T, k], e.g.
+    moe_grouped_mlp_bwd's dprob)."""
+    lib = load()
+    dev = _on(logits, "logits")
+    T, E = logits.shape
+    if topk_idx.dim() != 2:
+        raise ValueError("topk_idx must be [T, k]")
+    k = topk_idx.shape[1]
+    _shape(topk_idx, (T, k), torch.int32, dev, "topk_idx")
+    _shape(topk_prob, (T, k), torch.float32, dev, "topk_prob")
+    _shape(dprob, (T, k), torch.float32, dev, "dprob")
+    with _Device(dev):
+        dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
+        _check(lib.moe_route_grouped_bwd(_ptr(logits), _io(logits), T, E, k, _score(score), bool(renormalize), scale,
+                                         _ptr(topk_idx), _ptr(topk_prob), _ptr(dprob), dlogits.data_ptr(),
+                                         _stream(dev)), "moe_route_grouped_bwd")
+    return dlogits
+
+
+def _norm_weight(weight: torch.Tensor, H: int, dtype: torch.dtype, device: torch.device) -> int:
+    if weight.dtype is not dtype and weight.dtype is not torch.float32:
+        raise TypeError(f"weight must be {dtype} or float32, got {weight.dtype}")
+    _shape(weight, (H,), weight.dtype, device, "weight")
+    return _io(weight)
+
+
+def moe_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                    y: bool = True, codes: bool = False, sum_out: Optional[torch.Tensor] = None):
+    """The residual addition and root-mean-square norm ahead of the layer: s = x + residual (x [T, H], bf16 or f32;
+    without residual s is x itself), y = s / sqrt(mean(s^2) + eps) * weight (weight [H], in x's dtype or f32).
+    y, codes: which outputs are wanted, y in x's dtype and / or its E4M3 codes with one fp32 scale per 128 columns
+    (fp8_block_quantize's, of the unrounded y: a block-scaled product's operand; H % 128 == 0).
+    sum_out: optional tensor that receives s; may be x or residual itself.
+    Returns (y, s, codes uint8 [T, H], scales float32 [H/128, T]), None for what was not asked for."""
+    lib = load()
+    dev = _on(x, "x")
+    T, H = x.shape
+    io = _io(x)
+    _shape(x, (T, H), x.dtype, dev, "x")
+    _shape(residual, (T, H), x.dtype, dev, "residual")
+    wio = _norm_weight(weight, H, x.dtype, dev)
+    if not (y or codes):
+        raise ValueError("neither y nor codes wanted")
+    if codes and H % 128:
+        raise ValueError(f"codes need whole blocks of 128 columns, got {H}")
+    if sum_out is not None:
+        if residual is None:
+            raise ValueError("sum_out goes with a residual")
+        _shape(sum_out, (T, H), x.dtype, dev, "sum_out")
+    with _Device(dev):
+        out = torch.empty((T, H), dtype=x.dtype, device=dev) if y else None
+        s = None if residual is None else torch.empty((T, H), dtype=x.dtype, device=dev) if sum_out is None else sum_out
+        q = scales = None
+        if codes:
+            q = torch.empty((T, H), dtype=torch.uint8, device=dev)
+            scales = torch.empty((H // 128, T), dtype=torch.float32, device=dev)
+        _check(lib.moe_add_rmsnorm(_ptr(x), _ptr(residual), io, _ptr(weight), wio, T, H, eps, _ptr(s), _ptr(out), _ptr(q),
+                                   _ptr(scales), _stream(dev)), "moe_add_rmsnorm")
+    return out, x if s is None else s, q, scales
+
+
+def moe_add_rmsnorm_bwd(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, ds: Optional[torch.Tensor] = None,
+                        eps: float = 1e-6):
+    """Gradient of moe_add_rmsnorm.  dy: gradient of y [T, H] (also where the codes were used: rounding passes it on);
+    s: the forward's sum; ds: optional gradient that reaches s by other ways (the residual stream's); all of one
+    dtype (bf16 or f32).
+    Returns (dx [T, H], the gradient of x and of residual alike, dweight float32 [H])."""
+    lib = load()
+    dev = _on(dy, "dy")
+    T, H = dy.shape
+    io = _io(dy)
+    _shape(dy, (T, H), dy.dtype, dev, "dy")
+    _shape(s, (T, H), dy.dtype, dev, "s")
+    _shape(ds, (T, H), dy.dtype, dev, "ds")
+    wio = _norm_weight(weight, H, dy.dtype, dev)
+    with _Device(dev):
+        dx = torch.empty((T, H), dtype=dy.dtype, device=dev)
+        dw = torch.empty(H, dtype=torch.float32, device=dev)
+        ws = _scratch(lib.moe_add_rmsnorm_bwd_workspace(T, H), dev)
+        _check(lib.moe_add_rmsnorm_bwd(_ptr(dy), _ptr(s), _ptr(ds), io, _ptr(weight), wio, T, H, eps, _ptr(dx), _ptr(dw),
+                                       _ptr(ws), _nbytes(ws), _stream(dev)), "moe_add_rmsnorm_bwd")
+    return dx, dw
+
+
+class GradTable:
+    """The gradients of a model as moe_grad_sumsq and moe_grad_clip take them: contiguous tensors (bf16 or f32) of one
+    GPU, and optionally as many of the same numbers of values that receive the clipped ones (out; None: in place).
+    Made once, it saves each call the checks and the conversion of a long list.  It holds the tensors and their
+    addresses: make another one after a tensor has been given other memory."""
+
+    def __init__(self, grads: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]] = None):
+        self.grads = list(grads)
+        self.out = self.grads if out is None else list(out)
+        if not self.grads:
+            raise ValueError("no gradients")
+        if len(self.out) != len(self.grads):
+            raise ValueError(f"{len(self.grads)} gradients, {len(self.out)} outputs")
+        self.device = _on(self.grads[0], "gradients")
+        for what, ts in (("gradients", self.grads), ("outputs", self.out)):
+            for t in ts:
+                _io(t)
+                _shape(t, t.shape, t.dtype, self.device, what)
+        for g, o in zip(self.grads, self.out):
+            if g.numel() != o.numel():
+                raise ValueError(f"a gradient has {g.numel()} values, its output {o.numel()}")
+        n = len(self.grads)
+        self._arrays = ((_vp * n)(*[t.data_ptr() for t in self.grads]), (_i64 * n)(*[t.numel() for t in self.grads]),
+                        (_i32 * n)(*[_io(t) for t in self.grads]), (_vp * n)(*[t.data_ptr() for t in self.out]),
+                        (_i32 * n)(*[_io(t) for t in self.out]))
+        self._at = tuple(ctypes.addressof(a) for a in self._arrays)
+        self._workspace = load().moe_grad_sumsq_workspace(self._at[1], n)
+
+    def __len__(self):
+        return len(self.grads)
+
+
+def _sumsq(lib, table: GradTable, stream: int) -> torch.Tensor:
+    g, numel, kinds, _, _ = table._at
+    ws = _scratch(table._workspace, table.device)
+    sumsq = torch.empty(1, dtype=torch.float64, device=table.device)
+    _check(lib.moe_grad_sumsq(g, numel, kinds, len(table.grads), sumsq.data_ptr(), _ptr(ws), _nbytes(ws), stream),
+           "moe_grad_sumsq")
+    return sumsq
+
+
+def moe_grad_sumsq(grads) -> torch.Tensor:
+    """The sum of squares of the gradients (a GradTable, or a list of contiguous bf16 or f32 tensors of one GPU), in 64
+    bits: float64 [1].  Where ranks hold parts of the gradients, the sum of theirs is moe_grad_clip's sumsq."""
+    lib = load()
+    table = grads if isinstance(grads, GradTable) else GradTable(grads)
+    with _Device(table.device):
+        return _sumsq(lib, table, _stream(table.device))
+
+
+def moe_grad_clip(grads, max_norm: float, sumsq: Optional[torch.Tensor] = None, out=None) -> torch.Tensor:
+    """Scales the gradients (a GradTable, or a list of tensors) by min(1, max_norm / (norm + 1e-6)), norm =
+    sqrt(sumsq), in place or into `out` (a list of tensors with as many values, bf16 or f32; a GradTable has its own).
+    sumsq: float64 [1] (None: that of these gradients).  Returns norm, float32 [1], on the GPU; one that is not
+    finite leaves gradients that are not."""
+    lib = load()
+    if isinstance(grads, GradTable):
+        if out is not None:
+            raise ValueError("a GradTable has its outputs already")
+        table = grads
+    else:
+        table = GradTable(grads, out)
+    dev = table.device
+    _shape(sumsq, (1,), torch.float64, dev, "sumsq")
+    with _Device(dev):
+        stream = _stream(dev)
+        norm = torch.empty(1, dtype=torch.float32, device=dev)
+        if sumsq is None:
+            sumsq = _sumsq(lib, table, stream)
+        g, numel, kinds, to, to_kinds = table._at
+        _check(lib.moe_grad_clip(g, numel, kinds, len(table.grads), to, to_kinds, sumsq.data_ptr(), max_norm,
+                                 norm.data_ptr(), stream), "moe_grad_clip")
+    return norm
 
 
 def fp8_block_quantize(x: torch.Tensor, axis: int = 0, group_offsets: Optional[torch.Tensor] = None):

@@ -5,7 +5,9 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <algorithm>
 #include <mutex>
+#include <new>
 
 #include "moe.h"
 #include "common.h"
@@ -764,6 +766,41 @@ BalanceWs carve_balance(Carver& c, int64_t T, int E) {
   return w;
 }
 inline bool under_4g(int64_t bytes) { return bytes < (int64_t)UINT32_MAX; }
+
+// The norm's weight: the activations' type, or fp32.
+inline bool w_fits(int x_dtype, int w_dtype) { return w_dtype == x_dtype || w_dtype == MOE_F32; }
+
+constexpr int64_t kMostGrad = (int64_t)1 << 38;   // (a launch's chunks stay within int32)
+
+// Whether no output of a clipping overlaps another tensor that the call reads or writes (its own gradient, as the same
+// values in the same type, apart): workgroups take them in no order.
+struct Span {
+  uintptr_t lo, hi;
+  bool written;
+};
+moe_status check_apart(const void* const* grads, const int64_t* numel, const int32_t* dtypes, int n, void* const* out,
+                       const int32_t* out_dtypes) {
+  Span* v = new (std::nothrow) Span[2 * (size_t)n];
+  if (!v) return MOE_ERR_WORKSPACE;
+  size_t m = 0;
+  for (int i = 0; i < n; ++i) {
+    if (numel[i] == 0) continue;
+    const uintptr_t o = reinterpret_cast<uintptr_t>(out[i]), g = reinterpret_cast<uintptr_t>(grads[i]);
+    v[m++] = {o, o + (uintptr_t)numel[i] * io_size(out_dtypes[i]), true};
+    if (g != o || dtypes[i] != out_dtypes[i]) v[m++] = {g, g + (uintptr_t)numel[i] * io_size(dtypes[i]), false};
+  }
+  const auto before = [](const Span& a, const Span& b) { return a.lo < b.lo; };
+  if (!std::is_sorted(v, v + m, before)) std::sort(v, v + m, before);
+  uintptr_t any = 0, written = 0;                        // the furthest ends so far
+  bool apart = true;
+  for (size_t i = 0; i < m && apart; ++i) {
+    apart = v[i].lo >= (v[i].written ? any : written);
+    any = std::max(any, v[i].hi);
+    if (v[i].written) written = std::max(written, v[i].hi);
+  }
+  delete[] v;
+  return apart ? MOE_OK : MOE_ERR_INVALID_ARG;
+}
 }  // namespace
 
 size_t moe_route_balance_workspace(int64_t T, int E) {
@@ -797,6 +834,119 @@ moe_status moe_route_balance_bwd(const void* logits, int logits_dtype, const uin
   MOE_CHECK(!dprob || (topk_idx && topk_prob), MOE_ERR_INVALID_ARG);
   HIP_TRY(launch_route_balance_bwd(logits, logits_dtype == MOE_F32, token_mask, T, E, k, topk_idx, topk_prob, counts,
                                    dprob, dlosses, dlogits, reinterpret_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+size_t moe_route_grouped_workspace(int64_t T, int E) {
+  if (T <= 0 || E <= 0 || E > MOE_MAX_EXPERTS) return 0;
+  return align_up((size_t)route_group_blocks(T) * (size_t)E * sizeof(int32_t));
+}
+
+moe_status moe_route_grouped(const void* logits, int logits_dtype, const float* bias, const uint8_t* token_mask, int64_t T,
+                             int E, int k, int score, int groups, int topk_groups, int group_best, int renormalize,
+                             float scale, int32_t* topk_idx, float* topk_prob, int32_t* counts, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  moe_status s = check_common(T, 1, E, k);
+  if (s != MOE_OK) return s;
+  MOE_CHECK(logits && io_ok(logits_dtype) && topk_idx && topk_prob, MOE_ERR_INVALID_ARG);
+  MOE_CHECK(score == MOE_SCORE_SOFTMAX || score == MOE_SCORE_SIGMOID, MOE_ERR_INVALID_ARG);
+  MOE_CHECK(renormalize == 0 || renormalize == 1, MOE_ERR_INVALID_ARG);
+  MOE_CHECK(scale > 0.0f && scale <= 3.402823466e38f, MOE_ERR_INVALID_ARG);
+  MOE_CHECK(groups >= 1 && E % groups == 0 && topk_groups >= 1 && topk_groups <= groups, MOE_ERR_INVALID_ARG);
+  MOE_CHECK(group_best >= 1 && group_best <= 2 && group_best <= E / groups, MOE_ERR_INVALID_ARG);
+  MOE_CHECK(k <= topk_groups * (E / groups), MOE_ERR_INVALID_ARG);
+  MOE_CHECK(groups <= MOE_MAX_GROUPS, MOE_ERR_UNSUPPORTED);
+  MOE_CHECK(!token_mask || counts, MOE_ERR_INVALID_ARG);
+  if (counts) {
+    MOE_CHECK(workspace && workspace_bytes >= moe_route_grouped_workspace(T, E), MOE_ERR_WORKSPACE);
+    MOE_CHECK(aligned16(workspace), MOE_ERR_UNSUPPORTED);
+  }
+  const GroupRoute p{logits, bias, token_mask, T, E, k, topk_groups == groups ? 1 : groups, topk_groups, group_best,
+                     score == MOE_SCORE_SIGMOID, renormalize != 0, scale, topk_idx, topk_prob, counts,
+                     reinterpret_cast<int32_t*>(workspace)};
+  HIP_TRY(launch_route_group(p, logits_dtype == MOE_F32, reinterpret_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_route_grouped_bwd(const void* logits, int logits_dtype, int64_t T, int E, int k, int score, int renormalize,
+                                 float scale, const int32_t* topk_idx, const float* topk_prob, const float* dprob,
+                                 void* dlogits, void* stream) {
+  moe_status s = check_common(T, 1, E, k);
+  if (s != MOE_OK) return s;
+  MOE_CHECK(logits && io_ok(logits_dtype) && topk_idx && topk_prob && dprob && dlogits, MOE_ERR_INVALID_ARG);
+  MOE_CHECK(score == MOE_SCORE_SOFTMAX || score == MOE_SCORE_SIGMOID, MOE_ERR_INVALID_ARG);
+  MOE_CHECK(renormalize == 0 || renormalize == 1, MOE_ERR_INVALID_ARG);
+  MOE_CHECK(scale > 0.0f && scale <= 3.402823466e38f, MOE_ERR_INVALID_ARG);
+  const GroupRouteBwd p{logits, T, E, k, score == MOE_SCORE_SIGMOID, renormalize != 0, scale, topk_idx, topk_prob, dprob, dlogits};
+  HIP_TRY(launch_route_group_bwd(p, logits_dtype == MOE_F32, reinterpret_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_add_rmsnorm(const void* x, const void* residual, int x_dtype, const void* weight, int w_dtype, int64_t T,
+                           int64_t H, float eps, void* sum, void* y, uint8_t* q, float* scales, void* stream) {
+  MOE_CHECK(x && weight && T > 0 && H > 0 && io_ok(x_dtype) && io_ok(w_dtype), MOE_ERR_INVALID_ARG);
+  MOE_CHECK(eps >= 0.0f && eps <= 3.402823466e38f, MOE_ERR_INVALID_ARG);
+  MOE_CHECK((y || q) && !q == !scales && !residual == !sum, MOE_ERR_INVALID_ARG);
+  MOE_CHECK(T <= (int64_t)INT32_MAX && H <= kNormMaxH && w_fits(x_dtype, w_dtype), MOE_ERR_UNSUPPORTED);
+  if (q) MOE_CHECK(H % 128 == 0 && aligned16(x) && aligned16(residual) && aligned16(weight) && aligned16(sum) &&
+                   aligned16(y) && aligned16(q), MOE_ERR_UNSUPPORTED);
+  const NormFwd p{x, residual, weight, T, H, eps, sum, y, q, scales};
+  HIP_TRY(launch_add_rmsnorm(p, x_dtype == MOE_F32, w_dtype == MOE_F32, reinterpret_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+size_t moe_add_rmsnorm_bwd_workspace(int64_t T, int64_t H) {
+  if (T <= 0 || H <= 0 || T > (int64_t)INT32_MAX || H > kNormMaxH) return 0;
+  return align_up(norm_bwd_part_bytes(T, H));
+}
+
+moe_status moe_add_rmsnorm_bwd(const void* dy, const void* s, const void* dsum, int dtype, const void* weight, int w_dtype,
+                               int64_t T, int64_t H, float eps, void* dx, float* dweight, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  MOE_CHECK(dy && s && weight && dx && dweight && T > 0 && H > 0 && io_ok(dtype) && io_ok(w_dtype), MOE_ERR_INVALID_ARG);
+  MOE_CHECK(eps >= 0.0f && eps <= 3.402823466e38f, MOE_ERR_INVALID_ARG);
+  MOE_CHECK(T <= (int64_t)INT32_MAX && H <= kNormMaxH && w_fits(dtype, w_dtype), MOE_ERR_UNSUPPORTED);
+  MOE_CHECK(workspace && workspace_bytes >= moe_add_rmsnorm_bwd_workspace(T, H), MOE_ERR_WORKSPACE);
+  MOE_CHECK(aligned16(workspace), MOE_ERR_UNSUPPORTED);
+  const NormBwd p{dy, s, dsum, weight, T, H, eps, dx, dweight, reinterpret_cast<float*>(workspace)};
+  HIP_TRY(launch_rmsnorm_bwd(p, dtype == MOE_F32, w_dtype == MOE_F32, reinterpret_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+size_t moe_grad_sumsq_workspace(const int64_t* numel, int n) {
+  if (!numel || n < 1 || n > MOE_MAX_GRADS) return 0;
+  return align_up((size_t)grad_parts(numel, n) * sizeof(double));
+}
+
+moe_status moe_grad_sumsq(const void* const* grads, const int64_t* numel, const int32_t* dtypes, int n, double* sumsq,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  MOE_CHECK(grads && numel && dtypes && sumsq && n >= 1, MOE_ERR_INVALID_ARG);
+  MOE_CHECK(n <= MOE_MAX_GRADS, MOE_ERR_UNSUPPORTED);
+  for (int i = 0; i < n; ++i) {
+    MOE_CHECK(numel[i] >= 0 && (grads[i] || numel[i] == 0) && io_ok(dtypes[i]), MOE_ERR_INVALID_ARG);
+    MOE_CHECK(numel[i] <= kMostGrad, MOE_ERR_UNSUPPORTED);
+  }
+  MOE_CHECK(workspace && workspace_bytes >= moe_grad_sumsq_workspace(numel, n), MOE_ERR_WORKSPACE);
+  MOE_CHECK(aligned16(workspace), MOE_ERR_UNSUPPORTED);
+  const GradList l{grads, numel, dtypes, nullptr, nullptr, n};
+  HIP_TRY(launch_grad_sumsq(l, reinterpret_cast<double*>(workspace), sumsq, reinterpret_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_grad_clip(const void* const* grads, const int64_t* numel, const int32_t* dtypes, int n, void* const* out,
+                         const int32_t* out_dtypes, const double* sumsq, float max_norm, float* norm, void* stream) {
+  MOE_CHECK(grads && numel && dtypes && out && out_dtypes && sumsq && norm && n >= 1, MOE_ERR_INVALID_ARG);
+  MOE_CHECK(max_norm >= 0.0f, MOE_ERR_INVALID_ARG);
+  MOE_CHECK(n <= MOE_MAX_GRADS, MOE_ERR_UNSUPPORTED);
+  for (int i = 0; i < n; ++i) {
+    MOE_CHECK(numel[i] >= 0 && ((grads[i] && out[i]) || numel[i] == 0), MOE_ERR_INVALID_ARG);
+    MOE_CHECK(io_ok(dtypes[i]) && io_ok(out_dtypes[i]), MOE_ERR_INVALID_ARG);
+    MOE_CHECK(numel[i] <= kMostGrad, MOE_ERR_UNSUPPORTED);
+  }
+  const moe_status s = check_apart(grads, numel, dtypes, n, out, out_dtypes);
+  if (s != MOE_OK) return s;
+  const GradList l{grads, numel, dtypes, out, out_dtypes, n};
+  HIP_TRY(launch_grad_clip(l, sumsq, max_norm, norm, reinterpret_cast<hipStream_t>(stream)));
   return MOE_OK;
 }
 

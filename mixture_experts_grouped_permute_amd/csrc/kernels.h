@@ -234,4 +234,76 @@ struct BlockGemm {
 size_t block_gemm_part_bytes(bool wgrad, bool out_f32, int64_t rows, int64_t N, int64_t K, int E);
 hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t st);
 
+// ---- routing by scores with a bias and groups (route_group.hip)
+constexpr int kGroupMaxBlocks = 2048;
+struct GroupRoute {
+  const void* logits;
+  const float* bias;         // [E] or null
+  const uint8_t* mask;       // [T] or null: 0 = the token's slots are not counted
+  int64_t T;
+  int E, k, G, kg, best;
+  bool sigmoid, renorm;
+  float scale;
+  int32_t* idx;
+  float* prob;
+  int32_t* counts;           // [E] or null
+  int32_t* part;             // counts: route_group_blocks(T) x E int32
+};
+int route_group_blocks(int64_t T);
+hipError_t launch_route_group(const GroupRoute& p, bool f32, hipStream_t st);
+struct GroupRouteBwd {
+  const void* logits;
+  int64_t T;
+  int E, k;
+  bool sigmoid, renorm;
+  float scale;
+  const int32_t* idx;
+  const float* prob;
+  const float* dprob;
+  void* dlogits;
+};
+hipError_t launch_route_group_bwd(const GroupRouteBwd& p, bool f32, hipStream_t st);
+
+// ---- residual addition and RMS norm (norm.hip)
+constexpr int64_t kNormMaxH = 32768;
+struct NormFwd {
+  const void* x;
+  const void* residual;      // or null
+  const void* weight;
+  int64_t T, H;
+  float eps;
+  void* sum;                 // or null; may be x or residual
+  void* y;                   // or null
+  uint8_t* q;                // or null, with scales [H / 128, T]; H % 128 == 0
+  float* scales;
+};
+hipError_t launch_add_rmsnorm(const NormFwd& p, bool f32, bool w32, hipStream_t st);
+struct NormBwd {
+  const void* dy;
+  const void* s;
+  const void* dsum;          // or null
+  const void* weight;
+  int64_t T, H;
+  float eps;
+  void* dx;
+  float* dw;
+  float* part;               // norm_bwd_part_bytes
+};
+size_t norm_bwd_part_bytes(int64_t T, int64_t H);
+hipError_t launch_rmsnorm_bwd(const NormBwd& p, bool f32, bool w32, hipStream_t st);
+
+// ---- gradient norm and clipping (grad.hip).  Host arrays of n tensors; dtype 0: fp32, 1: bf16.
+constexpr int kGradTable = 128;
+struct GradList {
+  const void* const* g;
+  const int64_t* numel;
+  const int32_t* dtype;
+  void* const* out;          // or null: not written
+  const int32_t* out_dtype;
+  int n;
+};
+int64_t grad_parts(const int64_t* numel, int n);          // doubles of scratch
+hipError_t launch_grad_sumsq(const GradList& l, double* part, double* sumsq, hipStream_t st);
+hipError_t launch_grad_clip(const GradList& l, const double* sumsq, float max_norm, float* norm, hipStream_t st);
+
 }  // namespace moe

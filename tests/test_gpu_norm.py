@@ -1,0 +1,280 @@
+"""GPU parity of the residual RMS norm (moe_add_rmsnorm and its gradient) against the fp64 oracle.
+
+Tolerances, u = 2^-24.  The sum s is one fp32 addition rounded once: equal bit for bit to torch's.  The sum of squares
+adds at most 128 values of a lane in turn and 10 levels of lanes: within 140 u of itself, its root 70 u; with the
+division, the root and three products 80 u of y, and half an output step.  The gradient's mean is such a sum of terms
+of either sign, within 140 u of the sum of their magnitudes, times factors within 80 u: 240 u of all terms' magnitudes.
+dweight adds at most T terms in fp32, each within 80 u: (T + 100) u of the sum of their magnitudes.
+"""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import gpu, log, need_gpu
+from oracle import norm
+
+U = 2.0 ** -24
+F, B = torch.float32, torch.bfloat16
+
+
+def _x(T, H, dtype, seed):
+    g = np.random.default_rng(seed + 3 * T + H)
+    return torch.from_numpy((g.standard_normal((T, H)) * np.exp(0.7 * g.standard_normal(H))).astype(np.float32)).to(dtype)
+
+
+def _w(H, dtype):
+    return torch.from_numpy((1 + 0.1 * np.random.default_rng(H).standard_normal(H)).astype(np.float32)).to(dtype)
+
+
+def _np(t):
+    return t.detach().cpu().double().numpy()
+
+
+def _half(dtype):
+    return float(torch.finfo(dtype).eps) / 2
+
+
+SHAPES = [(1, 1), (1, 7), (2, 64), (3, 128), (1, 4096), (5, 255), (4, 257), (300, 96), (7, 1003), (33, 1024), (130, 2048),
+          (2, 8192), (3, 16384), (1, 32768), (2, 30001), (5, 8194), (1000, 130), (17, 4097), (9, 6016), (700, 640)]
+
+
+@gpu
+@pytest.mark.parametrize("dtype,wdtype", [(B, B), (B, F), (F, F)], ids=["bf16", "bf16-w32", "f32"])
+@pytest.mark.parametrize("T,H", SHAPES)
+def test_norm_and_gradient(T, H, dtype, wdtype):
+    m = need_gpu()
+    log(f"norm {T} x {H} {dtype} {wdtype}")
+    x, r, w = _x(T, H, dtype, 0), _x(T, H, dtype, 1), _w(H, wdtype)
+    xs, rs, ws = x.cuda(), r.cuda(), w.cuda()
+    for res in (None, rs):
+        y, s, q, scales = m.moe_add_rmsnorm(xs, ws, residual=res, eps=1e-6)
+        torch.cuda.synchronize()
+        assert q is None and scales is None and y.dtype == dtype
+        want_s = x if res is None else (x.float() + r.float()).to(dtype)
+        assert (s is xs) if res is None else torch.equal(s.cpu(), want_s)
+        want = norm.forward(want_s, w, 1e-6)
+        err = np.abs(_np(y) - want)
+        assert (err <= (80 * U + _half(dtype)) * np.abs(want) + 1e-38).all(), float((err / np.abs(want)).max())
+    dy, ds = _x(T, H, dtype, 2), _x(T, H, dtype, 3)
+    for d in (None, ds):
+        dx, dw = m.moe_add_rmsnorm_bwd(dy.cuda(), s, ws, ds=None if d is None else d.cuda(), eps=1e-6)
+        torch.cuda.synchronize()
+        assert dx.dtype == dtype and dw.dtype == F
+        rx, rw, mag, wmag = norm.backward(dy, want_s, w, 1e-6, d)
+        err = np.abs(_np(dx) - rx)
+        tol = 240 * U * mag + _half(dtype) * np.abs(rx) + 1e-38
+        assert (err <= tol).all(), float((err / tol).max())
+        err = np.abs(_np(dw) - rw)
+        assert (err <= (T + 100) * U * wmag + 1e-38).all(), float((err / wmag).max() / U)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,wdtype", [(B, B), (B, F), (F, F)], ids=["bf16", "bf16-w32", "f32"])
+@pytest.mark.parametrize("T,H", [(1, 128), (1, 4096), (3, 256), (50, 1408), (300, 2048), (37, 640), (2, 16384), (1, 32768),
+                                 (129, 1152)])
+def test_codes(T, H, dtype, wdtype):
+    m = need_gpu()
+    x, r, w = _x(T, H, dtype, 0), _x(T, H, dtype, 1), _w(H, wdtype)
+    x[T // 2, :128] = 0
+    r[T // 2, :128] = 0                           # a block of zeros
+    xs, rs, ws = x.cuda(), r.cuda(), w.cuda()
+    for res in (None, rs):
+        y, s, q, scales = m.moe_add_rmsnorm(xs, ws, residual=res, codes=True)
+        none, s2, q2, scales2 = m.moe_add_rmsnorm(xs, ws, residual=res, y=False, codes=True)
+        y3, _, _, _ = m.moe_add_rmsnorm(xs, ws, residual=res)
+        torch.cuda.synchronize()
+        assert none is None and torch.equal(q, q2) and torch.equal(scales, scales2) and torch.equal(y, y3)
+        assert torch.equal(s, s2)
+        if dtype == F:                            # y is not rounded then: the quantizer's own result
+            cq, cs = m.fp8_block_quantize(y)
+            assert torch.equal(cq, q) and torch.equal(cs, scales)
+        want = norm.forward(s.cpu(), w, 1e-6)
+        amax = np.abs(want).reshape(T, H // 128, 128).max(axis=2).T
+        d = np.where(amax > 0, amax / 448, 1.0)
+        assert (np.abs(_np(scales) - d) <= 90 * U * d).all()
+        got = _np(q.view(torch.float8_e4m3fn)).reshape(T, H // 128, 128) * _np(scales).T[:, :, None]
+        # half a step: 2^-4 of a normal code, 2^-10 of the scale under 2^-6; the value itself within 90 u
+        tol = np.maximum(np.abs(want).reshape(got.shape) * (2.0 ** -4 + 200 * U), d.T[:, :, None] * 2.0 ** -10 * (1 + 1e-4))
+        assert (np.abs(got - want.reshape(got.shape)) <= tol).all()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [B, F], ids=["bf16", "f32"])
+def test_sum_in_place_and_gradient_in_place(dtype):
+    m = need_gpu()
+    for T, H in ((1, 4096), (70, 1003), (19, 2048), (3, 20000)):
+        x, r, w = _x(T, H, dtype, 0).cuda(), _x(T, H, dtype, 1).cuda(), _w(H, dtype).cuda()
+        want = m.moe_add_rmsnorm(x, w, residual=r, codes=H % 128 == 0)
+        a, b = x.clone(), r.clone()
+        for out, args in ((a, (a, r)), (b, (x, b))):
+            got = m.moe_add_rmsnorm(args[0], w, residual=args[1], codes=H % 128 == 0, sum_out=out)
+            torch.cuda.synchronize()
+            assert got[1] is out
+            for g, h in zip(got, want):
+                assert (g is None and h is None) or torch.equal(g, h)
+
+
+@gpu
+def test_zero_rows_infinities_and_nan():
+    m = need_gpu()
+    for dtype in (B, F):
+        x = _x(6, 256, dtype, 0)
+        x[0] = 0
+        x[1, 5], x[2, 9], x[3, 200] = float("nan"), float("inf"), -float("inf")
+        w = _w(256, dtype)
+        y, s, q, scales = m.moe_add_rmsnorm(x.cuda(), w.cuda(), eps=0.0, codes=True)
+        torch.cuda.synchronize()
+        want = norm.forward(x[4:], w, 0.0)
+        assert (np.abs(_np(y)[4:] - want) <= (80 * U + _half(dtype)) * np.abs(want)).all()
+        assert torch.isnan(y[0]).all() and torch.isnan(y[1]).all()          # 0 / 0, as the formula has it
+        ref = torch.tensor([float("inf")]) * 0
+        assert torch.isnan(ref).all() and torch.isnan(y[2, 9]) and float(y[2, 8]) == 0 and torch.isnan(y[3, 200])
+        y, _, q, scales = m.moe_add_rmsnorm(x.cuda(), w.cuda(), eps=1e-6, codes=True)
+        torch.cuda.synchronize()
+        assert not y[0].any() and not (q[0] & 0x7F).any() and (scales[:, 0] == 1).all()
+        assert torch.isfinite(scales[:, 4:]).all() and torch.isnan(scales[:, 1]).all()
+
+
+@gpu
+def test_rows_at_the_ends_stay_apart():
+    """Tensors inside larger ones, at odd places where only the type's alignment is asked for: nothing else changes."""
+    m = need_gpu()
+    for dtype, T, H in ((B, 5, 1001), (F, 3, 515), (B, 4, 1024)):
+        def inside(t, shift):
+            flat = torch.full((t.numel() + 64,), 7.0, dtype=dtype, device="cuda")
+            v = flat[shift:shift + t.numel()].view(t.shape)
+            v.copy_(t)
+            return flat, v
+        x, r, w = _x(T, H, dtype, 0), _x(T, H, dtype, 1), _w(H, dtype)
+        (fx, xv), (fr, rv), (fw, wv) = inside(x, 1), inside(r, 3), inside(w, 5)
+        fo, ov = inside(torch.zeros_like(x), 9)
+        y, s, _, _ = m.moe_add_rmsnorm(xv, wv, residual=rv, sum_out=ov)
+        y2, s2, _, _ = m.moe_add_rmsnorm(x.cuda(), w.cuda(), residual=r.cuda())
+        dx, dw = m.moe_add_rmsnorm_bwd(xv, rv, wv, ds=ov)
+        dx2, dw2 = m.moe_add_rmsnorm_bwd(x.cuda(), r.cuda(), w.cuda(), ds=s2)
+        torch.cuda.synchronize()
+        want = norm.forward(s.cpu(), w, 1e-6)
+        assert torch.equal(s, s2)
+        for a, b in ((y, y2), (dx, dx2), (dw, dw2)):
+            a, b = _np(a), _np(b)
+            assert (np.abs(a - b) <= 2 * (1000 * U + _half(dtype)) * np.abs(b).max()).all()
+        assert (np.abs(_np(y) - want) <= (80 * U + _half(dtype)) * np.abs(want)).all()
+        assert (fo[:9] == 7).all() and (fo[9 + T * H:] == 7).all()
+
+
+@gpu
+def test_gradient_against_differences():
+    """The kernels' own outputs moved by a step: fp32 in, so differences carry about 1e-3."""
+    m = need_gpu()
+    g = torch.Generator().manual_seed(4)
+    s, w = torch.randn((3, 48), generator=g).cuda(), (1 + 0.1 * torch.randn(48, generator=g)).cuda()
+    dy = torch.randn((3, 48), generator=g).cuda()
+    dx, dw = m.moe_add_rmsnorm_bwd(dy, s, w)
+    h = 1e-2
+    def value(a, b):
+        return float((m.moe_add_rmsnorm(a, b)[0].double() * dy.double()).sum())
+    for t, i in ((0, 0), (1, 17), (2, 47)):
+        a = s.clone(); a[t, i] += h
+        b = s.clone(); b[t, i] -= h
+        # h^2 / 6 of a third derivative of order 1, and 48 x 3 values' rounding 1e-6 over 2 h
+        assert abs((value(a, w) - value(b, w)) / (2 * h) - float(dx[t, i])) <= 1e-3
+        a = w.clone(); a[i] += h
+        b = w.clone(); b[i] -= h
+        assert abs((value(s, a) - value(s, b)) / (2 * h) - float(dw[i])) <= 1e-3
+
+
+@gpu
+def test_many_rows_and_determinism():
+    m = need_gpu()
+    for T, H, dtype in ((20011, 72, F), (9001, 384, B)):
+        x, w, dy = _x(T, H, dtype, 0), _w(H, dtype), _x(T, H, dtype, 1)
+        y, _, _, _ = m.moe_add_rmsnorm(x.cuda(), w.cuda())
+        dx, dw = m.moe_add_rmsnorm_bwd(dy.cuda(), x.cuda(), w.cuda())
+        dx2, dw2 = m.moe_add_rmsnorm_bwd(dy.cuda(), x.cuda(), w.cuda())
+        torch.cuda.synchronize()
+        assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+        want = norm.forward(x[-500:], w, 1e-6)
+        assert (np.abs(_np(y[-500:]) - want) <= (80 * U + _half(dtype)) * np.abs(want)).all()
+        xd, wd, dd = _np(x), _np(w), _np(dy)
+        r = 1 / np.sqrt((xd * xd).mean(1, keepdims=True) + 1e-6)
+        terms = dd * xd * r
+        assert (np.abs(_np(dw) - terms.sum(0)) <= (T + 100) * U * np.abs(terms).sum(0)).all()
+        # far below that bound: rounding of either sign, a few hundred u of the root of the squares' sum
+        assert (np.abs(_np(dw) - terms.sum(0)) <= 300 * U * np.sqrt((terms ** 2).sum(0)) * np.sqrt(T) / 8).all()
+
+
+@gpu
+def test_streams_and_graphs():
+    m = need_gpu()
+    x, r, w = _x(500, 1024, B, 0).cuda(), _x(500, 1024, B, 1).cuda(), _w(1024, B).cuda()
+    x2, w2 = _x(300, 1001, F, 0).cuda(), _w(1001, F).cuda()
+
+    def one():
+        y, s, q, sc = m.moe_add_rmsnorm(x, w, residual=r, codes=True)
+        return (y, s, q, sc) + m.moe_add_rmsnorm_bwd(y, s, w, ds=x)
+
+    def two():
+        y, s, _, _ = m.moe_add_rmsnorm(x2, w2)
+        return (y,) + m.moe_add_rmsnorm_bwd(y, s, w2)
+
+    want, want2 = one(), two()
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s1):
+        a = one()
+    with torch.cuda.stream(s2):
+        b = two()
+    torch.cuda.synchronize()
+    for got, ref in ((a, want), (b, want2)):
+        assert all(torch.equal(p, q) for p, q in zip(got, ref))
+    with torch.cuda.graph(g1):
+        a = one()
+    with torch.cuda.graph(g2):
+        b = two()
+    for _ in range(3):
+        with torch.cuda.stream(s1):
+            g1.replay()
+        with torch.cuda.stream(s2):
+            g2.replay()
+        torch.cuda.synchronize()
+        two()
+        torch.cuda.synchronize()
+        for got, ref in ((a, want), (b, want2)):
+            assert all(torch.equal(p, q) for p, q in zip(got, ref))
+
+
+@gpu
+def test_refusals_on_the_gpu():
+    m = need_gpu()
+    x, w = torch.zeros((4, 256), device="cuda"), torch.ones(256, device="cuda")
+    with pytest.raises(TypeError):
+        m.moe_add_rmsnorm(x.half(), w)
+    with pytest.raises(TypeError):
+        m.moe_add_rmsnorm(x, w.bfloat16())
+    with pytest.raises(TypeError):
+        m.moe_add_rmsnorm(x, w, residual=x.bfloat16())
+    with pytest.raises(ValueError):
+        m.moe_add_rmsnorm(x, w[:255])
+    with pytest.raises(ValueError):
+        m.moe_add_rmsnorm(x, w, residual=x[:3])
+    with pytest.raises(ValueError):
+        m.moe_add_rmsnorm(x.t(), torch.ones(4, device="cuda"))
+    with pytest.raises(ValueError):
+        m.moe_add_rmsnorm(x, w, y=False)
+    with pytest.raises(ValueError):
+        m.moe_add_rmsnorm(x[:, :200].contiguous(), w[:200].contiguous(), codes=True)
+    with pytest.raises(ValueError):
+        m.moe_add_rmsnorm(x, w, sum_out=torch.empty_like(x))
+    with pytest.raises(m.MoeError):
+        m.moe_add_rmsnorm(x, w, eps=-1.0)
+    with pytest.raises(m.MoeError):
+        m.moe_add_rmsnorm(torch.zeros((0, 256), device="cuda"), w)
+    with pytest.raises(m.MoeError):
+        m.moe_add_rmsnorm(torch.zeros((1, 40000), device="cuda"), torch.ones(40000, device="cuda"))
+    with pytest.raises(m.MoeError):                       # codes want 16-byte rows
+        m.moe_add_rmsnorm(torch.zeros(4 * 256 + 1, device="cuda")[1:].view(4, 256), w, codes=True)
+    with pytest.raises(TypeError):
+        m.moe_add_rmsnorm_bwd(x, x.bfloat16(), w)
+    with pytest.raises(ValueError):
+        m.moe_add_rmsnorm_bwd(x, x, w, ds=x[:2])

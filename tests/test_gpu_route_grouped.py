@@ -1,0 +1,293 @@
+"""GPU parity of grouped routing (moe_route_grouped and its gradient) against the fp64 oracle.
+
+Ids and counts are compared exactly: the order is that of 64-bit scores, whose distances in these inputs are far above
+what two 64-bit exponentials differ by.  Tolerances, u = 2^-24: the exponential is the hardware's exp2 of x log2 e,
+off by (|x| + 2) u, with |x| <= 12 here (a difference of logits, or a logit whose score is not next to 1), its sum
+with 1 and the reciprocal 4 u: a score is within 18 u of itself; a sum of scores of one sign within 18 u + 16 u;
+quotient and scale 4 u: a weight within 56 u of itself, 80 u allowed.  A gradient's terms are products of such
+factors with sums of at most 16 terms: within 96 u of the sum of their magnitudes, and half an output step.
+"""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import gpu, log, need_gpu
+from oracle import group_route
+
+U = 2.0 ** -24
+TINY = 2.0 ** -126      # results below the smallest normal number may be flushed
+
+
+def _logits(T, E, kind, dtype, seed=3):
+    g = np.random.default_rng(seed + 7 * T + E)
+    lg = g.standard_normal((T, E)) * 1.5
+    if kind == "ties":
+        lg = np.round(lg)
+    elif kind == "zeros":
+        lg = np.where(g.random((T, E)) < 0.5, 0.0, -0.0)
+    elif kind == "masked-experts":
+        lg[:, :: 3] = -np.inf
+    elif kind == "lowest":
+        lg[:, 1:: 2] = float(torch.finfo(dtype).min)
+    elif kind == "dead-rows":
+        lg[:: 2] = -np.inf
+        lg[1:: 4, 2:] = -np.inf
+    elif kind == "tiny-scores":
+        lg = lg - 95.0
+    elif kind == "saturated":
+        lg = lg + 30.0
+    return torch.from_numpy(lg.astype(np.float32)).to(dtype)
+
+
+F, B = torch.float32, torch.bfloat16
+CASES = [
+    # T, E, k, G, kg, best, score, bias, renorm, scale, kind, dtype, masked
+    (1, 1, 1, 1, 1, 1, "sigmoid", False, True, 1.0, "normal", F, False),
+    (1, 256, 8, 8, 4, 2, "sigmoid", True, True, 2.5, "normal", F, False),
+    (3, 2, 2, 2, 2, 1, "softmax", True, False, 1.0, "normal", F, True),
+    (5, 7, 7, 1, 1, 1, "sigmoid", True, True, 1.0, "ties", B, False),
+    (257, 8, 2, 4, 2, 2, "sigmoid", True, True, 1.0, "normal", B, True),
+    (129, 9, 3, 3, 1, 2, "softmax", False, True, 1.0, "ties", F, False),
+    (513, 16, 1, 16, 3, 1, "sigmoid", True, False, 1.0, "normal", F, True),
+    (400, 32, 16, 16, 8, 2, "softmax", True, True, 16.0, "normal", F, True),
+    (1000, 18, 5, 6, 4, 2, "sigmoid", False, True, 1.0, "masked-experts", F, False),
+    (300, 48, 6, 3, 2, 1, "softmax", True, False, 1.0, "masked-experts", B, True),
+    (700, 30, 16, 5, 3, 2, "sigmoid", False, True, 1.0, "zeros", B, False),
+    (400, 33, 9, 11, 5, 2, "softmax", False, False, 2.5, "zeros", F, True),
+    (900, 64, 8, 4, 2, 2, "sigmoid", True, True, 2.5, "normal", B, True),
+    (640, 64, 8, 8, 3, 1, "sigmoid", False, True, 1.0, "ties", B, True),
+    (500, 100, 7, 10, 3, 2, "sigmoid", True, False, 1.0, "normal", F, True),
+    (300, 129, 12, 3, 2, 2, "softmax", True, True, 1.0, "normal", F, False),
+    (333, 160, 6, 8, 3, 1, "softmax", False, False, 16.0, "normal", B, False),
+    (2000, 256, 8, 8, 4, 2, "sigmoid", True, True, 2.5, "normal", F, True),
+    (333, 256, 16, 16, 2, 2, "sigmoid", False, True, 1.0, "normal", B, False),
+    (333, 256, 16, 1, 1, 1, "sigmoid", False, True, 1.0, "normal", F, False),
+    (250, 251, 5, 1, 1, 1, "softmax", True, True, 1.0, "normal", B, False),
+    (300, 200, 4, 2, 1, 2, "sigmoid", True, True, 1.0, "lowest", F, False),
+    (300, 200, 4, 2, 1, 2, "softmax", False, True, 1.0, "lowest", F, False),
+    (200, 6, 4, 3, 2, 2, "sigmoid", False, True, 1.0, "dead-rows", F, True),
+    (200, 6, 4, 3, 2, 1, "softmax", True, False, 1.0, "dead-rows", B, True),
+    (200, 40, 4, 4, 2, 2, "sigmoid", False, True, 1.0, "tiny-scores", F, False),
+    (200, 40, 4, 4, 2, 2, "sigmoid", True, False, 1.0, "tiny-scores", F, False),
+    (200, 40, 4, 4, 2, 1, "sigmoid", True, True, 1.0, "saturated", F, False),
+    (9001, 24, 4, 6, 3, 2, "sigmoid", True, True, 1.0, "normal", F, True),
+    (20993, 12, 4, 1, 1, 1, "softmax", True, True, 1.0, "normal", B, True),
+]
+IDS = [f"T{c[0]}-E{c[1]}-k{c[2]}-G{c[3]}.{c[4]}.{c[5]}-{c[6]}{'-bias' if c[7] else ''}{'' if c[8] else '-plain'}-{c[10]}-"
+       f"{'f32' if c[11] == F else 'bf16'}{'-mask' if c[12] else ''}" for c in CASES]
+
+
+def _bias(E, kind, seed=5):
+    return torch.from_numpy((np.random.default_rng(seed + E).standard_normal(E) * 0.1).astype(np.float32))
+
+
+def _mask(T, masked):
+    return torch.from_numpy(np.random.default_rng(T).random(T) < 0.8) if masked else None
+
+
+def _gpu(t):
+    return None if t is None else t.cuda()
+
+
+def _close(got, want, tol):
+    assert ((np.abs(got - want) <= tol) | ((got == want) | (np.isnan(got) & np.isnan(want)))).all(), \
+        float(np.nanmax(np.abs(got - want) / np.maximum(tol, 1e-300)))
+
+
+@gpu
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_forward_and_gradient(case):
+    m = need_gpu()
+    T, E, k, G, kg, best, score, bias, renorm, scale, kind, dtype, masked = case
+    lg, mask, b = _logits(T, E, kind, dtype), _mask(T, masked), _bias(E, kind) if bias else None
+    kw = dict(score=score, groups=G, topk_groups=kg, group_best=best, renormalize=renorm, scale=scale)
+    idx, prob, counts = m.moe_route_grouped(lg.cuda(), k, bias=_gpu(b), token_mask=_gpu(mask), count=True, **kw)
+    i2, p2, none = m.moe_route_grouped(lg.cuda(), k, bias=_gpu(b), **kw)
+    torch.cuda.synchronize()
+    assert none is None and torch.equal(idx, i2) and torch.equal(prob, p2)
+    ri, rp, rc = group_route.forward(lg, k, b, mask=None if mask is None else mask.numpy(), **kw)
+    np.testing.assert_array_equal(idx.cpu().numpy(), ri)
+    np.testing.assert_array_equal(counts.cpu().numpy(), rc)
+    got = prob.cpu().double().numpy()
+    log(f"weights off by at most {np.max(np.abs(got - rp) / np.maximum(rp, TINY)) / U:.1f} u")
+    _close(got, rp, 80 * U * rp + TINY * scale)
+    # the gradient, from the kernel's own ids and weights
+    dp = torch.from_numpy(np.random.default_rng(1).standard_normal((T, k)).astype(np.float32))
+    out = m.moe_route_grouped_bwd(lg.cuda(), idx, prob, dp.cuda(), score=score, renormalize=renorm, scale=scale)
+    torch.cuda.synchronize()
+    assert out.dtype == dtype
+    want, mag = group_route.backward(lg, ri, prob.cpu().numpy(), dp.numpy(), score, renorm, scale)
+    _close(out.cpu().double().numpy(), want,
+           96 * U * mag + np.abs(want) * float(torch.finfo(dtype).eps) / 2 + TINY * 16 * scale)
+
+
+@gpu
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,G", [(40, 1), (256, 8), (96, 3)])
+def test_nearly_equal_scores_take_their_64_bit_order(score, E, G):
+    """Biases that make every score + bias equal to within fp32's rounding: 32-bit values would tie or swap."""
+    m = need_gpu()
+    g = np.random.default_rng(E + G)
+    T, k = 37, min(8, E // G)
+    base = (g.standard_normal(E) * 1.5).astype(np.float32)
+    lg = np.repeat(base[None], T, 0)
+    lg[1::3] = (g.standard_normal((len(lg[1::3]), E)) * 1.5).astype(np.float32)       # ordinary rows between
+    s = group_route.scores(base[None].astype(np.float64), score)[0]
+    b = (0.9 - s).astype(np.float32)
+    c = s + b.astype(np.float64)
+    assert 0 < np.diff(np.sort(c)).min() and np.ptp(c) < 1.3e-7
+    kw = dict(score=score, groups=G, topk_groups=max(1, G // 2), group_best=2 if G > 1 else 1)
+    idx, prob, _ = m.moe_route_grouped(torch.from_numpy(lg).cuda(), k, bias=torch.from_numpy(b).cuda(), **kw)
+    torch.cuda.synchronize()
+    ri, rp, _ = group_route.forward(lg, k, b, **kw)
+    np.testing.assert_array_equal(idx.cpu().numpy(), ri)
+    _close(prob.cpu().double().numpy(), rp, 80 * U * rp)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [F, B], ids=["f32", "bf16"])
+@pytest.mark.parametrize("E,k,G,kg,best", [(7, 2, 1, 1, 1), (32, 4, 8, 3, 2), (256, 8, 8, 4, 2), (60, 16, 4, 2, 1)])
+def test_nan_infinity_and_large_biases(dtype, E, k, G, kg, best):
+    m = need_gpu()
+    lg = _logits(40, E, "normal", dtype)
+    nan, inf = float("nan"), float("inf")
+    lg[1, E - 1], lg[2, 3], lg[3, E // 2], lg[4, 0], lg[5, 1] = nan, inf, -inf, -nan, inf
+    lg[5, E - 2] = nan
+    lg[6] = nan
+    for score in ("sigmoid", "softmax"):
+        for b in (None, torch.zeros(E), torch.linspace(-300, 300, E)):
+            if b is not None and E > 30:
+                b[5], b[9], b[11] = inf, -inf, nan
+            kw = dict(score=score, groups=G, topk_groups=kg, group_best=best)
+            idx, prob, _ = m.moe_route_grouped(lg.cuda(), k, bias=_gpu(b), **kw)
+            torch.cuda.synchronize()
+            ri, rp, _ = group_route.forward(lg, k, b, **kw)
+            np.testing.assert_array_equal(idx.cpu().numpy(), ri)
+            _close(prob.cpu().double().numpy(), rp, 80 * U * rp + TINY)
+
+
+@gpu
+def test_softmax_without_groups_is_the_plain_router():
+    m = need_gpu()
+    for T, E, k, dtype in ((5000, 8, 2, F), (3001, 64, 8, B), (777, 256, 16, F)):
+        lg = _logits(T, E, "ties", dtype).cuda()
+        idx, prob, counts = m.moe_route_grouped(lg, k, score="softmax", count=True)
+        i2, p2, c2, _ = m.moe_route_balance(lg, k)
+        torch.cuda.synchronize()
+        assert torch.equal(idx, i2) and torch.equal(counts, c2)
+        assert float((prob - p2).abs().max()) <= 120 * U
+
+
+@gpu
+def test_repeated_and_foreign_ids_in_the_gradient():
+    m = need_gpu()
+    for score in ("sigmoid", "softmax"):
+        for renorm in (True, False):
+            for dtype in (F, B):
+                lg = _logits(23, 9, "normal", dtype)
+                g = np.random.default_rng(2)
+                idx = torch.from_numpy(g.integers(0, 9, (23, 5)).astype(np.int32))
+                idx[2::3, 0], idx[2::3, 3], idx[::4, 1] = -1, 9, 2 ** 31 - 1
+                idx[7] = 4
+                prob = torch.from_numpy(g.random((23, 5)).astype(np.float32))
+                dp = torch.from_numpy(g.standard_normal((23, 5)).astype(np.float32))
+                out = m.moe_route_grouped_bwd(lg.cuda(), idx.cuda(), prob.cuda(), dp.cuda(), score=score, renormalize=renorm,
+                                              scale=1.5)
+                again = m.moe_route_grouped_bwd(lg.cuda(), idx.cuda(), prob.cuda(), dp.cuda(), score=score,
+                                                renormalize=renorm, scale=1.5)
+                torch.cuda.synchronize()
+                assert torch.equal(out, again)
+                want, mag = group_route.backward(lg, idx.numpy(), prob.numpy(), dp.numpy(), score, renorm, 1.5)
+                _close(out.cpu().double().numpy(), want, 96 * U * mag + np.abs(want) * float(torch.finfo(dtype).eps) / 2 + TINY)
+
+
+@gpu
+def test_many_tokens_and_unaligned_logits():
+    """More tokens than the kernels hold at once, and logits that begin anywhere."""
+    m = need_gpu()
+    for T, E, dtype, shift in ((70001, 20, F, 1), (40003, 33, B, 3), (3, 256, B, 1)):
+        flat = torch.empty(T * E + 8, dtype=dtype, device="cuda")
+        lg = _logits(T, E, "normal", dtype)
+        view = flat[shift:shift + T * E].view(T, E)
+        view.copy_(lg)
+        b = _bias(E, "normal")
+        kw = dict(score="sigmoid", groups=1 if E == 33 else 4, topk_groups=1 if E == 33 else 2)
+        idx, prob, counts = m.moe_route_grouped(view, 4, bias=b.cuda(), count=True, **kw)
+        i2, p2, c2 = m.moe_route_grouped(lg.cuda(), 4, bias=b.cuda(), count=True, **kw)
+        out = m.moe_route_grouped_bwd(view, idx, prob, prob)
+        o2 = m.moe_route_grouped_bwd(lg.cuda(), idx, prob, prob)
+        torch.cuda.synchronize()
+        assert torch.equal(idx, i2) and torch.equal(prob, p2) and torch.equal(counts, c2) and torch.equal(out, o2)
+        ri, rp, rc = group_route.forward(lg[-2000:], 4, b, group_best=2, **kw)
+        np.testing.assert_array_equal(idx[-2000:].cpu().numpy(), ri)
+        assert int(counts.sum()) == 4 * T
+
+
+@gpu
+def test_deterministic_on_two_streams_and_in_two_graphs():
+    m = need_gpu()
+    lg, lg2 = _logits(9000, 64, "normal", F).cuda(), _logits(5000, 32, "ties", B).cuda()
+    b, b2 = _bias(64, "normal").cuda(), _bias(32, "normal").cuda()
+
+    def step(x, bias, k):
+        idx, prob, counts = m.moe_route_grouped(x, k, bias=bias, groups=4, topk_groups=2, count=True)
+        return idx, prob, counts, m.moe_route_grouped_bwd(x, idx, prob, prob)
+
+    want, want2 = step(lg, b, 8), step(lg2, b2, 4)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(s1):
+        a = step(lg, b, 8)
+    with torch.cuda.stream(s2):
+        c = step(lg2, b2, 4)
+    torch.cuda.synchronize()
+    for got, ref in ((a, want), (c, want2)):
+        assert all(torch.equal(x, y) for x, y in zip(got, ref))
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g1):
+        a = step(lg, b, 8)
+    with torch.cuda.graph(g2):
+        c = step(lg2, b2, 4)
+    for _ in range(3):
+        with torch.cuda.stream(s1):
+            g1.replay()
+        with torch.cuda.stream(s2):
+            g2.replay()
+        torch.cuda.synchronize()
+        step(lg2, b2, 8)
+        torch.cuda.synchronize()
+        for got, ref in ((a, want), (c, want2)):
+            assert all(torch.equal(x, y) for x, y in zip(got, ref))
+
+
+@gpu
+def test_refusals_on_the_gpu():
+    m = need_gpu()
+    lg = torch.zeros((6, 8), device="cuda")
+    idx, prob, _ = m.moe_route_grouped(lg, 2)
+    for kw in (dict(k=9), dict(k=0), dict(groups=3), dict(groups=0), dict(groups=4, topk_groups=1, k=3),
+               dict(groups=8, group_best=2), dict(scale=0.0), dict(topk_groups=2)):
+        with pytest.raises(m.MoeError):
+            m.moe_route_grouped(lg, **{"k": 2, **kw})
+    with pytest.raises(ValueError):
+        m.moe_route_grouped(lg, 2, score="tanh")
+    with pytest.raises(ValueError):
+        m.moe_route_grouped(lg, 2, token_mask=torch.ones(6, dtype=torch.bool, device="cuda"))
+    with pytest.raises(ValueError):
+        m.moe_route_grouped(lg, 2, bias=torch.zeros(7, device="cuda"))
+    with pytest.raises(TypeError):
+        m.moe_route_grouped(lg, 2, bias=torch.zeros(8, device="cuda", dtype=torch.bfloat16))
+    with pytest.raises(TypeError):
+        m.moe_route_grouped(lg, 2, bias=torch.zeros(8))
+    with pytest.raises(TypeError):
+        m.moe_route_grouped(lg.half(), 2)
+    with pytest.raises(ValueError):
+        m.moe_route_grouped(lg.t(), 2)
+    with pytest.raises(ValueError):
+        m.moe_route_grouped_bwd(lg, idx, prob[:5], prob)
+    with pytest.raises(TypeError):
+        m.moe_route_grouped_bwd(lg, idx.long(), prob, prob)
+    with pytest.raises(m.MoeError):
+        m.moe_route_grouped_bwd(lg, idx, prob, prob, scale=-1.0)
+    with pytest.raises(m.MoeError):
+        m.moe_route_grouped(torch.zeros((0, 8), device="cuda"), 2)
