@@ -8,7 +8,7 @@
 // rstd is formed again from s, which the backward reads anyway: both of its sums come from the same read.
 //
 // Memory bounds both.  A row stays in the registers of kL lanes between the sums and the results, kN pieces of 8
-// columns each, so that everything is read and written once; the next row's loads are in flight behind the sums.
+// columns each, so that everything is read and written once.
 #include "common.h"
 #include "kernels.h"
 #include "block_scale.h"
@@ -36,6 +36,16 @@ struct Eight {
       if constexpr (kF32) w[1] = reinterpret_cast<const u32x4_any*>(b)[1];
     }
   }
+  // the same past the caches, for values that are read once
+  __device__ __forceinline__ void load_once(const void* p, int64_t at) {
+    const char* b = reinterpret_cast<const char*>(p) + at * (kF32 ? 4 : 2);
+    if constexpr (kAligned) {
+      w[0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b));
+      if constexpr (kF32) w[1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b) + 1);
+    } else {
+      load(p, at);
+    }
+  }
   __device__ __forceinline__ void zero() {
     w[0] = u32x4{0u, 0u, 0u, 0u};
     if constexpr (kF32) w[1] = u32x4{0u, 0u, 0u, 0u};
@@ -54,11 +64,18 @@ struct Eight {
       for (int i = 0; i < 4; ++i) w[0][i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
     }
   }
+  // kOnce: past the caches
+  template <bool kOnce = false>
   __device__ __forceinline__ void store(void* p, int64_t at) const {
     char* b = reinterpret_cast<char*>(p) + at * (kF32 ? 4 : 2);
     if constexpr (kAligned) {
-      reinterpret_cast<u32x4*>(b)[0] = w[0];
-      if constexpr (kF32) reinterpret_cast<u32x4*>(b)[1] = w[1];
+      if constexpr (kOnce) {
+        __builtin_nontemporal_store(w[0], reinterpret_cast<u32x4*>(b));
+        if constexpr (kF32) __builtin_nontemporal_store(w[1], reinterpret_cast<u32x4*>(b) + 1);
+      } else {
+        reinterpret_cast<u32x4*>(b)[0] = w[0];
+        if constexpr (kF32) reinterpret_cast<u32x4*>(b)[1] = w[1];
+      }
     } else {
       reinterpret_cast<u32x4_any*>(b)[0] = w[0];
       if constexpr (kF32) reinterpret_cast<u32x4_any*>(b)[1] = w[1];
@@ -132,145 +149,133 @@ __device__ __forceinline__ Piece piece(int c, int sub, int H) {
   return q;
 }
 
-// ---- forward.  A workgroup takes `unit` consecutive rows, kRows at a time.
-template <bool kF32, bool kW32, int kL, int kN, bool kAligned>
-__global__ __launch_bounds__(threads_of(kL)) void add_rmsnorm_kernel(const NormFwd p, int unit) {
+// ---- forward.  A workgroup takes the kRows rows that its lanes hold and ends: others begin in its place, and their
+// loads overlap (several rows one after the other, with the next one's loads behind the sums and the scales gathered
+// in LDS into runs: 126 us at 16384 x 4096 bf16 with 16 rows, 117 with 4, 109 so).
+// kOnce: the sum and y are stored past the caches.
+template <bool kF32, bool kW32, int kL, int kN, bool kAligned, bool kOnce>
+__global__ __launch_bounds__(threads_of(kL)) void add_rmsnorm_kernel(const NormFwd p) {
   using Sum = RowSum<kL, 1>;
-  constexpr int kRows = Sum::kRows;
   __shared__ float red[Sum::kWords];
-  extern __shared__ float sc[];                         // [H / 128][unit] scales, which leave as runs of rows
-  const int tid = threadIdx.x, sub = tid % kL, slot = tid / kL, H = (int)p.H;
-  const int64_t r0 = (int64_t)blockIdx.x * unit;
+  const int tid = threadIdx.x, sub = tid % kL, H = (int)p.H;
+  const int64_t t = (int64_t)blockIdx.x * Sum::kRows + tid / kL;
   Piece q[kN];
+  bool in[kN];
+  Eight<kF32, kAligned> x[kN], r[kN];
   Eight<kW32, kAligned> w[kN];
 #pragma unroll
   for (int c = 0; c < kN; ++c) {
     q[c] = piece<kL, kAligned>(c, sub, H);
-    if (q[c].in) w[c].load(p.weight, q[c].col);
-    else w[c].zero();
+    in[c] = q[c].in && t < p.T;
+    x[c].zero();
+    r[c].zero();
+    w[c].zero();
+    if (in[c]) x[c].load_once(p.x, t * H + q[c].col);
   }
-  Eight<kF32, kAligned> x[kN], r[kN];
-  const auto fetch = [&](int64_t t) {
+  if (p.residual) {
 #pragma unroll
-    for (int c = 0; c < kN; ++c) {
-      if (q[c].in && t < p.T) x[c].load(p.x, t * H + q[c].col);
-      else x[c].zero();
-    }
+    for (int c = 0; c < kN; ++c)
+      if (in[c]) r[c].load_once(p.residual, t * H + q[c].col);
+  }
+#pragma unroll
+  for (int c = 0; c < kN; ++c)
+    if (in[c]) w[c].load(p.weight, q[c].col);
+  float s[kN][8], sq[1] = {0.f};
+#pragma unroll
+  for (int c = 0; c < kN; ++c) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[c][j] = x[c].at(j);
     if (p.residual) {
 #pragma unroll
-      for (int c = 0; c < kN; ++c) {
-        if (q[c].in && t < p.T) r[c].load(p.residual, t * H + q[c].col);
-        else r[c].zero();
-      }
+      for (int j = 0; j < 8; ++j) s[c][j] += r[c].at(j);
+      x[c].set(s[c]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[c][j] = x[c].at(j);   // as it is stored
     }
-  };
-  fetch(r0 + slot);
-  for (int i = 0; i < unit && r0 + i < p.T; i += kRows) {
-    const int64_t t = r0 + i + slot;
-    const bool live = t < p.T;
-    float s[kN][8], sq[1] = {0.f};
 #pragma unroll
-    for (int c = 0; c < kN; ++c) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[c][j] = x[c].at(j);
-      if (p.residual) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[c][j] += r[c].at(j);
-        Eight<kF32, kAligned> o;
-        o.set(s[c]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[c][j] = o.at(j);   // as it is stored
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sq[0] += kAligned || j >= q[c].skip ? s[c][j] * s[c][j] : 0.f;
-    }
-    if (i + kRows < unit) fetch(t + kRows);
-    Sum::sum(sq, red, i / kRows);
-    // (the sums are stored behind the row's last read, which may be of the same memory)
-    const float rstd = 1.0f / sqrtf(sq[0] / (float)H + p.eps);
-#pragma unroll
-    for (int c = 0; c < kN; ++c) {
-      const bool out = q[c].in && live;
-      const int64_t at = t * H + q[c].col;
-      Eight<kF32, kAligned> o;
-      if (p.sum && out) {
-        o.set(s[c]);
-        o.store(p.sum, at);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[c][j] = s[c][j] * rstd * w[c].at(j);
-      if (p.y && out) {
-        o.set(s[c]);
-        o.store(p.y, at);
-      }
-      if constexpr (kAligned) {
-        if (p.q) {
-          uint32_t m = 0;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) m = umax(m, __builtin_bit_cast(uint32_t, s[c][j]) & 0x7FFFFFFFu);
-          const BlockScale b = block_scale(max16(m));
-          if (out) {
-            u32x2 o8;
-            o8[0] = codes4(s[c][0], s[c][1], s[c][2], s[c][3], b.factor);
-            o8[1] = codes4(s[c][4], s[c][5], s[c][6], s[c][7], b.factor);
-            *reinterpret_cast<u32x2*>(p.q + at) = o8;
-            if ((tid & 15) == 0) {
-              const int blk = q[c].col >> 7;
-              if (unit == 1) p.scales[(int64_t)blk * p.T + t] = b.d;
-              else sc[blk * unit + i + slot] = b.d;
-            }
-          }
-        }
-      }
-    }
+    for (int j = 0; j < 8; ++j) sq[0] += kAligned || j >= q[c].skip ? s[c][j] * s[c][j] : 0.f;
   }
-  if constexpr (kAligned) {
-    if (p.q && unit > 1) {
-      __syncthreads();
-      for (int i = tid; i < H / 128 * unit; i += threads_of(kL)) {
-        const int blk = i / unit, u = i % unit;
-        if (r0 + u < p.T) p.scales[(int64_t)blk * p.T + r0 + u] = sc[i];
+  Sum::sum(sq, red, 0);
+  const float rstd = 1.0f / sqrtf(sq[0] / (float)H + p.eps);
+#pragma unroll
+  for (int c = 0; c < kN; ++c) {
+    const int64_t at = t * H + q[c].col;
+    // (stored behind the row's last read, which may be of the same memory)
+    if (p.sum && in[c]) x[c].template store<kOnce>(p.sum, at);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[c][j] = s[c][j] * rstd * w[c].at(j);
+    if (p.y && in[c]) {
+      x[c].set(s[c]);
+      x[c].template store<kOnce>(p.y, at);
+    }
+    if constexpr (kAligned) {
+      if (p.q) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = umax(m, __builtin_bit_cast(uint32_t, s[c][j]) & 0x7FFFFFFFu);
+        const BlockScale b = block_scale(max16(m));      // 16 lanes hold 128 columns
+        if (in[c]) {
+          u32x2 o;
+          o[0] = codes4(s[c][0], s[c][1], s[c][2], s[c][3], b.factor);
+          o[1] = codes4(s[c][4], s[c][5], s[c][6], s[c][7], b.factor);
+          *reinterpret_cast<u32x2*>(p.q + at) = o;
+          if ((tid & 15) == 0) p.scales[(int64_t)(q[c].col >> 7) * p.T + t] = b.d;
+        }
       }
     }
   }
 }
 
-// ---- backward.  Workgroup b takes rows b kRows, (b + grid) kRows, ..: dx, and sums of dy xh over them for each
-// of its slots, in registers till its end.
+// ---- backward.  Workgroup b takes rows b kRows, (b + grid) kRows, ..: dx, and sums of dy xh over them in registers
+// till its end; the next rows' loads are in flight behind the sums of a row.  (kLate: where 1024 lanes hold 16 columns
+// each or more, or 512 hold 32 in fp32, that would take more registers than there are -- 460 us at 2000 x 32768 bf16 --
+// so the weight and ds are read when they are needed, and the next row when this one is done.)
 template <bool kF32, bool kW32, int kL, int kN, bool kAligned>
 __global__ __launch_bounds__(threads_of(kL)) void rmsnorm_bwd_kernel(const NormBwd p) {
   using Sum = RowSum<kL, 2>;
   constexpr int kRows = Sum::kRows;
+  constexpr bool kLate = (kL == 1024 && kN >= 2) || (kF32 && kL == 512 && kN == 4);
+  constexpr int kK = kLate ? 1 : kN;                    // pieces of the weight and ds in registers
   __shared__ float red[Sum::kWords];
   const int tid = threadIdx.x, sub = tid % kL, slot = tid / kL, H = (int)p.H;
   Piece q[kN];
-  Eight<kW32, kAligned> w[kN];
+  Eight<kW32, kAligned> w[kK];
   float acc[kN][8];
 #pragma unroll
   for (int c = 0; c < kN; ++c) {
     q[c] = piece<kL, kAligned>(c, sub, H);
-    if (q[c].in) w[c].load(p.weight, q[c].col);
-    else w[c].zero();
+    if constexpr (!kLate) {
+      w[c].zero();
+      if (q[c].in) w[c].load(p.weight, q[c].col);
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[c][j] = 0.f;
   }
-  Eight<kF32, kAligned> rs[kN], rd[kN], ra[kN];
+  Eight<kF32, kAligned> rs[kN], rd[kN], ra[kK];
   const auto fetch = [&](int64_t t) {
 #pragma unroll
     for (int c = 0; c < kN; ++c) {
-      const bool in = q[c].in && t < p.T;
-      if (in) {
-        rs[c].load(p.s, t * H + q[c].col);
-        rd[c].load(p.dy, t * H + q[c].col);
-      } else {
-        rs[c].zero();
-        rd[c].zero();
+      rs[c].zero();
+      rd[c].zero();
+      if (q[c].in && t < p.T) {
+        rs[c].load_once(p.s, t * H + q[c].col);
+        rd[c].load_once(p.dy, t * H + q[c].col);
       }
     }
-    if (p.dsum) {
+    if constexpr (!kLate)
+      if (p.dsum) {
 #pragma unroll
-      for (int c = 0; c < kN; ++c)
-        if (q[c].in && t < p.T) ra[c].load(p.dsum, t * H + q[c].col);
+        for (int c = 0; c < kN; ++c)
+          if (q[c].in && t < p.T) ra[c].load_once(p.dsum, t * H + q[c].col);
+      }
+  };
+  const auto weight = [&](int c) -> const Eight<kW32, kAligned>& {
+    if constexpr (kLate) {
+      w[0].zero();
+      if (q[c].in) w[0].load(p.weight, q[c].col);
+      return w[0];
+    } else {
+      return w[c];
     }
   };
   const int64_t step = (int64_t)gridDim.x * kRows;
@@ -278,44 +283,82 @@ __global__ __launch_bounds__(threads_of(kL)) void rmsnorm_bwd_kernel(const NormB
   int turn = 0;
   for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < p.T; t0 += step, ++turn) {
     const int64_t t = t0 + slot;
-    float s[kN][8], d[kN][8], a[kN][8], v[2] = {0.f, 0.f};
+    float s[kN][8], d[kN][8], a[kK][8], v[2] = {0.f, 0.f};
 #pragma unroll
-    for (int c = 0; c < kN; ++c)
+    for (int c = 0; c < kN; ++c) {
+      const Eight<kW32, kAligned>& wc = weight(c);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         s[c][j] = rs[c].at(j);
         d[c][j] = rd[c].at(j);
-        a[c][j] = p.dsum ? ra[c].at(j) : 0.f;
+        if constexpr (!kLate) a[c][j] = p.dsum ? ra[c].at(j) : 0.f;
         const bool mine = kAligned || j >= q[c].skip;
         v[0] += mine ? s[c][j] * s[c][j] : 0.f;
-        v[1] += mine ? s[c][j] * d[c][j] * w[c].at(j) : 0.f;
+        v[1] += mine ? s[c][j] * d[c][j] * wc.at(j) : 0.f;
       }
-    fetch(t + step);
+    }
+    if constexpr (!kLate) {
+      fetch(t + step);
+    } else {
+      // (the values are unpacked again from the words: unpacked ones across the sums would not fit)
+#pragma unroll
+      for (int c = 0; c < kN; ++c)
+#pragma unroll
+        for (int i = 0; i < (kF32 ? 2 : 1); ++i) asm volatile("" : "+v"(rs[c].w[i]), "+v"(rd[c].w[i]));
+    }
     Sum::sum(v, red, turn);
     const float rstd = 1.0f / sqrtf(v[0] / (float)H + p.eps);
     const float mean = v[1] * rstd / (float)H;          // of g xh
 #pragma unroll
     for (int c = 0; c < kN; ++c) {
+      const bool in = q[c].in && t < p.T;
+      const Eight<kW32, kAligned>& wc = weight(c);
+      if constexpr (kLate) {
+        ra[0].zero();
+        if (p.dsum && in) ra[0].load_once(p.dsum, t * H + q[c].col);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[0][j] = ra[0].at(j);
+      }
+      if constexpr (kLate) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          s[c][j] = rs[c].at(j);
+          d[c][j] = rd[c].at(j);
+        }
+      }
       float o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float xh = s[c][j] * rstd;
-        o[j] = rstd * (d[c][j] * w[c].at(j) - xh * mean) + a[c][j];
+        o[j] = rstd * (d[c][j] * wc.at(j) - xh * mean) + a[kLate ? 0 : c][j];
         acc[c][j] += d[c][j] * xh;
       }
-      if (q[c].in && t < p.T) {
+      if (in) {
         Eight<kF32, kAligned> e;
         e.set(o);
         e.store(p.dx, t * H + q[c].col);
       }
     }
+    if constexpr (kLate) fetch(t + step);
   }
-  float* to = p.part + ((int64_t)blockIdx.x * kRows + slot) * H;
+  // the slots' sums in turn, so that a workgroup leaves one part
+  __shared__ float all[kRows > 1 ? kRows * kL * kN * 8 : 1];
+  float* part = p.part + (int64_t)blockIdx.x * H;
+  float* to = kRows > 1 ? all + slot * H : part;
 #pragma unroll
   for (int c = 0; c < kN; ++c)
     if (q[c].in)
 #pragma unroll
       for (int j = 0; j < 8; ++j) to[q[c].col + j] = acc[c][j];
+  if constexpr (kRows > 1) {
+    __syncthreads();
+    for (int h = tid; h < H; h += threads_of(kL)) {
+      float v = all[h];
+#pragma unroll
+      for (int i = 1; i < kRows; ++i) v += all[i * H + h];
+      part[h] = v;
+    }
+  }
 }
 
 // dw[h] = sum of the parts, in 64 bits: 16 columns by a workgroup, 64 slices of the parts.
@@ -451,6 +494,7 @@ Shape shape_few(int64_t H) {
   return {1024, 4};
 }
 constexpr int64_t kFewRows = 512;
+constexpr int64_t kOnceBytes = (int64_t)384 << 20;
 
 template <class F>
 hipError_t with_shape(Shape s, F&& f) {
@@ -475,32 +519,36 @@ hipError_t launch_fwd(const NormFwd& p, hipStream_t st) {
   const Shape s = few ? shape_few(p.H) : shape_of(p.H);
   const bool aligned = p.H % 8 == 0 && at16(p.x) && at16(p.residual) && at16(p.weight) && at16(p.sum) && at16(p.y);
   const int rows = threads_of(s.L) / s.L;
-  const int unit = few ? rows : rows > 16 ? rows : 16;
-  const unsigned grid = (unsigned)((p.T + unit - 1) / unit);
-  const size_t lds = p.q && unit > 1 ? (size_t)(p.H / 128) * unit * sizeof(float) : 0;
+  const unsigned grid = (unsigned)((p.T + rows - 1) / rows);
+  // Past the caches where the call moves more than the last of them (256 MB) holds: 16384 x 4096 bf16 with residual,
+  // y and codes 96 us instead of 109, and with two products that read y and the codes behind it 186 instead of 199;
+  // 8192 x 4096, which the cache still holds, 112 with them against 115.
+  const int64_t moved = p.T * p.H * (kF32 ? 4 : 2) * (1 + (p.y != nullptr) + 2 * (p.residual != nullptr));
+  const bool once = moved > kOnceBytes;
   return with_shape(s, [&](auto l, auto n) {
     constexpr int kL = decltype(l)::value, kN = decltype(n)::value;
-    if (aligned) add_rmsnorm_kernel<kF32, kW32, kL, kN, true><<<grid, threads_of(kL), lds, st>>>(p, unit);
-    else add_rmsnorm_kernel<kF32, kW32, kL, kN, false><<<grid, threads_of(kL), 0, st>>>(p, unit);
+    if (aligned && once) add_rmsnorm_kernel<kF32, kW32, kL, kN, true, true><<<grid, threads_of(kL), 0, st>>>(p);
+    else if (aligned) add_rmsnorm_kernel<kF32, kW32, kL, kN, true, false><<<grid, threads_of(kL), 0, st>>>(p);
+    else add_rmsnorm_kernel<kF32, kW32, kL, kN, false, false><<<grid, threads_of(kL), 0, st>>>(p);
     return hipGetLastError();
   });
 }
 
-// Workgroups of the backward: kBwdBlocks at most, so that the sums' parts stay few.
-constexpr int kBwdBlocks = 1024;
-int bwd_blocks(int64_t T, int rows) {
+// Workgroups of the backward: few, since each leaves a part of dw (16384 x 4096 bf16: 88 us with 512, 96 with 1024;
+// 65536 x 512: 47 with 512, 60 with 256), and one a CU where a row takes most of its registers (8192 x 8192 bf16: 94 us
+// with 512, 89 with 256; 4096 x 16384: 109 and 98).
+int bwd_blocks(int64_t T, int rows, int most) {
   const int64_t need = (T + rows - 1) / rows;
-  return (int)(need < kBwdBlocks ? need : kBwdBlocks);
+  return (int)(need < most ? need : most);
 }
 struct BwdPlan {
   Shape s;
-  int rows, blocks;       // rows: slots a workgroup, and so parts
+  int blocks;
 };
 BwdPlan plan_bwd(int64_t T, int64_t H) {
-  if (H < 8) return {{0, 0}, 1, bwd_blocks(T, 256)};
+  if (H < 8) return {{0, 0}, bwd_blocks(T, 256, 512)};
   const Shape s = T <= kFewRows ? shape_few(H) : shape_of(H);
-  const int rows = threads_of(s.L) / s.L;
-  return {s, rows, bwd_blocks(T, rows)};
+  return {s, bwd_blocks(T, threads_of(s.L) / s.L, s.N >= 4 ? 256 : 512)};
 }
 
 template <bool kF32, bool kW32>
@@ -520,7 +568,7 @@ hipError_t launch_bwd(const NormBwd& p, hipStream_t st) {
     });
   }
   if (e != hipSuccess) return e;
-  rmsnorm_dw_kernel<<<(unsigned)((p.H + 15) / 16), kSumThreads, 0, st>>>(p.part, b.blocks * b.rows, (int)p.H, p.dw);
+  rmsnorm_dw_kernel<<<(unsigned)((p.H + 15) / 16), kSumThreads, 0, st>>>(p.part, b.blocks, (int)p.H, p.dw);
   return hipGetLastError();
 }
 
@@ -528,7 +576,7 @@ hipError_t launch_bwd(const NormBwd& p, hipStream_t st) {
 
 size_t norm_bwd_part_bytes(int64_t T, int64_t H) {
   const BwdPlan b = plan_bwd(T, H);
-  return (size_t)b.blocks * (size_t)b.rows * (size_t)H * sizeof(float);
+  return (size_t)b.blocks * (size_t)H * sizeof(float);
 }
 
 hipError_t launch_add_rmsnorm(const NormFwd& p, bool f32, bool w32, hipStream_t st) {
