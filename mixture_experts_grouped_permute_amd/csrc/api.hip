@@ -770,7 +770,7 @@ inline bool under_4g(int64_t bytes) { return bytes < (int64_t)UINT32_MAX; }
 // The norm's weight: the activations' type, or fp32.
 inline bool w_fits(int x_dtype, int w_dtype) { return w_dtype == x_dtype || w_dtype == MOE_F32; }
 
-constexpr int64_t kMostGrad = (int64_t)1 << 38;   // (a launch's chunks stay within int32)
+constexpr int64_t kMostGrad = (int64_t)1 << 35;   // (a launch's chunks stay within int32)
 
 // Whether no output of a clipping overlaps another tensor that the call reads or writes (its own gradient, as the same
 // values in the same type, apart): workgroups take them in no order.

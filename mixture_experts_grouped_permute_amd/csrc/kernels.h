@@ -293,7 +293,6 @@ size_t norm_bwd_part_bytes(int64_t T, int64_t H);
 hipError_t launch_rmsnorm_bwd(const NormBwd& p, bool f32, bool w32, hipStream_t st);
 
 // ---- gradient norm and clipping (grad.hip).  Host arrays of n tensors; dtype 0: fp32, 1: bf16.
-constexpr int kGradTable = 128;
 struct GradList {
   const void* const* g;
   const int64_t* numel;

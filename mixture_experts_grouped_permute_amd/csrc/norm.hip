@@ -12,76 +12,12 @@
 #include "common.h"
 #include "kernels.h"
 #include "block_scale.h"
+#include "eight.h"
 
 #include <type_traits>
 
 namespace moe {
 namespace {
-
-// 8 consecutive values.  kAligned: at 16 bytes; else at the type's alignment, which global memory's wide
-// accesses take as well.
-typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
-typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
-
-template <bool kF32, bool kAligned>
-struct Eight {
-  u32x4 w[kF32 ? 2 : 1];
-  __device__ __forceinline__ void load(const void* p, int64_t at) {
-    const char* b = reinterpret_cast<const char*>(p) + at * (kF32 ? 4 : 2);
-    if constexpr (kAligned) {
-      w[0] = reinterpret_cast<const u32x4*>(b)[0];
-      if constexpr (kF32) w[1] = reinterpret_cast<const u32x4*>(b)[1];
-    } else {
-      w[0] = reinterpret_cast<const u32x4_any*>(b)[0];
-      if constexpr (kF32) w[1] = reinterpret_cast<const u32x4_any*>(b)[1];
-    }
-  }
-  // the same past the caches, for values that are read once
-  __device__ __forceinline__ void load_once(const void* p, int64_t at) {
-    const char* b = reinterpret_cast<const char*>(p) + at * (kF32 ? 4 : 2);
-    if constexpr (kAligned) {
-      w[0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b));
-      if constexpr (kF32) w[1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(b) + 1);
-    } else {
-      load(p, at);
-    }
-  }
-  __device__ __forceinline__ void zero() {
-    w[0] = u32x4{0u, 0u, 0u, 0u};
-    if constexpr (kF32) w[1] = u32x4{0u, 0u, 0u, 0u};
-  }
-  __device__ __forceinline__ float at(int i) const {
-    // (the word is copied first: a bit cast of the vector's element itself reads element 0)
-    const uint32_t u = kF32 ? w[kF32 ? i >> 2 : 0][i & 3] : (i & 1) ? w[0][i >> 1] & 0xFFFF0000u : w[0][i >> 1] << 16;
-    return __builtin_bit_cast(float, u);
-  }
-  __device__ __forceinline__ void set(const float* v) {
-    if constexpr (kF32) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i >> 2][i & 3] = __builtin_bit_cast(uint32_t, v[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[0][i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-    }
-  }
-  // kOnce: past the caches
-  template <bool kOnce = false>
-  __device__ __forceinline__ void store(void* p, int64_t at) const {
-    char* b = reinterpret_cast<char*>(p) + at * (kF32 ? 4 : 2);
-    if constexpr (kAligned) {
-      if constexpr (kOnce) {
-        __builtin_nontemporal_store(w[0], reinterpret_cast<u32x4*>(b));
-        if constexpr (kF32) __builtin_nontemporal_store(w[1], reinterpret_cast<u32x4*>(b) + 1);
-      } else {
-        reinterpret_cast<u32x4*>(b)[0] = w[0];
-        if constexpr (kF32) reinterpret_cast<u32x4*>(b)[1] = w[1];
-      }
-    } else {
-      reinterpret_cast<u32x4_any*>(b)[0] = w[0];
-      if constexpr (kF32) reinterpret_cast<u32x4_any*>(b)[1] = w[1];
-    }
-  }
-};
 
 template <int ctrl, int rows>
 __device__ __forceinline__ float dpp_add(float v) {
