@@ -324,8 +324,10 @@ moe_status moe_route_balance_bwd(const void* logits, int logits_dtype, const uin
  *   (equal: lower id).
  *   topk_prob [T, k] fp32: s at topk_idx, 0 where c is -inf; with renormalize
  *   divided by their sum over the k (0 where that is 0); times scale.
- * Scores, c and the groups' sums are compared as 64-bit values.  A NaN counts as
- * the largest (so does the sum of a group that holds one among its best); ids
+ * Without a bias experts are ordered by their logits (as their scores are, also
+ * where these round to the same value), and groups of one best by their best
+ * one's; else c and the sums are compared as 64-bit values.  A NaN goes ahead of
+ * +inf (so does a group that holds one among its best); several: lower id.  Ids
  * are always in range.
  * counts      optional [E] int32 out: slots of the counting tokens at e.
  * 1 <= k <= min(16, topk_groups E / groups), E <= 256, E % groups == 0,

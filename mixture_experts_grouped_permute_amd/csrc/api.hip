@@ -863,7 +863,7 @@ moe_status moe_route_grouped(const void* logits, int logits_dtype, const float* 
   }
   const GroupRoute p{logits, bias, token_mask, T, E, k, topk_groups == groups ? 1 : groups, topk_groups, group_best,
                      score == MOE_SCORE_SIGMOID, renormalize != 0, scale, topk_idx, topk_prob, counts,
-                     reinterpret_cast<int32_t*>(workspace)};
+                     reinterpret_cast<int32_t*>(workspace), false, 0};
   HIP_TRY(launch_route_group(p, logits_dtype == MOE_F32, reinterpret_cast<hipStream_t>(stream)));
   return MOE_OK;
 }

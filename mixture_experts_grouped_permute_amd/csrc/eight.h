@@ -7,6 +7,7 @@ namespace moe {
 // 8 consecutive values.  kAligned: at 16 bytes; else at the type's alignment, which global memory's wide
 // accesses take as well.
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
 
 // (global memory said outright: addresses out of a table would be generic ones)
 template <class T>

@@ -235,7 +235,7 @@ size_t block_gemm_part_bytes(bool wgrad, bool out_f32, int64_t rows, int64_t N, 
 hipError_t launch_block_gemm(const BlockGemm& g, hipStream_t st);
 
 // ---- routing by scores with a bias and groups (route_group.hip)
-constexpr int kGroupMaxBlocks = 2048;
+constexpr int kGroupMaxBlocks = 1024;
 struct GroupRoute {
   const void* logits;
   const float* bias;         // [E] or null
@@ -248,9 +248,11 @@ struct GroupRoute {
   float* prob;
   int32_t* counts;           // [E] or null
   int32_t* part;             // counts: route_group_blocks(T) x E int32
+  bool f32;                  // (the launcher's)
+  int lanes;
 };
 int route_group_blocks(int64_t T);
-hipError_t launch_route_group(const GroupRoute& p, bool f32, hipStream_t st);
+hipError_t launch_route_group(GroupRoute p, bool f32, hipStream_t st);
 struct GroupRouteBwd {
   const void* logits;
   int64_t T;

@@ -5,18 +5,27 @@
 //   kg best stay (equal sums: lower group), experts of the others have c = -inf;
 //   idx = the k largest c (equal: lower id);  w_j = s[idx_j], 0 where c is -inf, divided by their sum if
 //   renormalised (0 if that is 0), times scale.
-// The order is that of 64-bit values, so that it does not hang on how an exponential rounds.
+// Without a bias experts are ordered by their logits, as their scores are, and groups of one best by their best's; else
+// c and the sums are compared as 64-bit values, so that the order does not hang on how an exponential rounds.
 //
 // Gradient, g = dprob and w = prob: with S_j = (1 - s_j) for sigmoid and 1 for softmax scores,
 //   renormalised:  dl[idx_j] = S_j w_j (g_j - sum_m w_m g_m / scale), else 0
 //   not:           dl[idx_j] = S_j w_j g_j, and for softmax scores also -p_e sum_m w_m g_m at every expert.
+//
+// Forward: 16 lanes share a token; a group's experts lie with 16 / (power of two >= G) of them.  Scores are fp32
+// first: their error is known (2^-21 and a rounding of c), and where two numbers whose order counts are nearer than
+// that -- neighbours in the list, the last one in and the first one out, the last group in and the first one out -- the
+// wave does that token again in 64 bits (one of some thousand with fp32 logits).
 #include "common.h"
 #include "kernels.h"
+#include "eight.h"
+#include "route_select.h"
 
 namespace moe {
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 4, kTokens = 4 * kWaves;         // tokens of a workgroup at a time
+constexpr float kNone = -__builtin_huge_valf();
 
 // A number in the order of the doubles: -inf lowest, both zeros equal, every NaN on top.
 __device__ __forceinline__ uint64_t order_of(double v) {
@@ -24,7 +33,6 @@ __device__ __forceinline__ uint64_t order_of(double v) {
   if (v != v) return ~0ull;
   return (u >> 63) ? ~u : u | 1ull << 63;
 }
-__device__ __forceinline__ double shfl_f64(double v, int src) { return __shfl(v, src, 64); }
 __device__ __forceinline__ uint64_t shfl_u64(uint64_t v, int src) {
   return (uint64_t)__shfl((unsigned long long)v, src, 64);
 }
@@ -32,6 +40,10 @@ __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
   return v;
+}
+__device__ __forceinline__ void wave_lds() {            // LDS writes of the wave's lanes ahead of its later reads
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 template <bool kF32>
@@ -47,7 +59,7 @@ struct Slot {
   float w;
 };
 template <bool kF32>
-__device__ __noinline__ Slot route_token(const GroupRoute& p, int64_t t, int lane, double* cs) {
+__device__ __forceinline__ Slot route_token(const GroupRoute& p, int64_t t, int lane, double* cs) {
   constexpr int kC = kMaxExperts / 64;
   const double none = -__builtin_huge_val();
   double s[kC];
@@ -58,6 +70,8 @@ __device__ __noinline__ Slot route_token(const GroupRoute& p, int64_t t, int lan
     const int e = lane + 64 * c;
     s[c] = e < p.E ? (double)logit<kF32>(p.logits, t * p.E + e) : none;
     out[c] = s[c] == none;
+    key[c] = order_of(s[c]);
+    if (p.G > 1 && p.best == 1 && !p.bias && e < p.E) cs[e] = s[c];
   }
   if (p.sigmoid) {
 #pragma unroll
@@ -79,19 +93,22 @@ __device__ __noinline__ Slot route_token(const GroupRoute& p, int64_t t, int lan
 #pragma unroll
     for (int c = 0; c < kC; ++c) s[c] = total == 0.0 ? 0.0 : s[c] / total;
   }
+  if (p.bias || (p.G > 1 && p.best == 2)) {
 #pragma unroll
-  for (int c = 0; c < kC; ++c) {
-    const int e = lane + 64 * c;
-    double v = s[c] + (p.bias && e < p.E ? (double)p.bias[e] : 0.0);
-    if (out[c]) v = none;
-    out[c] = v == none;
-    key[c] = order_of(v);
-    if (p.G > 1 && e < p.E) cs[e] = v;
+    for (int c = 0; c < kC; ++c) {
+      const int e = lane + 64 * c;
+      double v = s[c] + (p.bias && e < p.E ? (double)p.bias[e] : 0.0);
+      if (out[c]) v = none;
+      if (p.bias) {
+        key[c] = order_of(v);
+        out[c] = v == none;
+      }
+      if (p.G > 1 && e < p.E) cs[e] = v;
+    }
   }
   if (p.G > 1) {
     const int n = p.E / p.G;
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    wave_lds();
     uint64_t mine = 0;
     if (lane < p.G) {
       double a = none, b = none;                        // the two largest
@@ -108,6 +125,7 @@ __device__ __noinline__ Slot route_token(const GroupRoute& p, int64_t t, int lan
       }
       mine = order_of(p.best == 2 ? a + b : a);
     }
+    wave_lds();
     int rank = 0;
     for (int h = 0; h < p.G; ++h) {
       const uint64_t o = shfl_u64(mine, h);
@@ -152,7 +170,7 @@ __device__ __noinline__ Slot route_token(const GroupRoute& p, int64_t t, int lan
         te = oe;
       }
     }
-    const double sel = shfl_f64(bs, te & 63);           // (the owner's best is the wave's)
+    const double sel = __shfl(bs, te & 63, 64);         // (the owner's best is the wave's)
     if ((te & 63) == lane) gone |= 1u << (te >> 6);
     if (lane == j) {
       r.e = te;
@@ -167,42 +185,297 @@ __device__ __noinline__ Slot route_token(const GroupRoute& p, int64_t t, int lan
   return r;
 }
 
+// ---- the logits of a wave's 4 tokens, which lie one after the other, in LDS: loads of 16 bytes a lane whatever E is,
+// and the lanes take their experts from there.  2 words of room after each 32 keep the lanes of groups of 16 or 32
+// experts on banks of their own.
+constexpr int kStage = 4 * kMaxExperts / 32 * 34;
+__device__ __forceinline__ int staged(int i) { return i + (i >> 5) * 2; }
+
 template <bool kF32>
+__device__ __forceinline__ void stage_logits(const void* lg, int64_t at, int n, int lane, float* to) {
+#pragma unroll
+  for (int u = 0; u < kMaxExperts / 64; ++u) {
+    const int i = (u * 64 + lane) * 4;
+    if (u * 256 >= n) break;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    const char* b = reinterpret_cast<const char*>(lg) + (at + i) * (kF32 ? 4 : 2);
+    if (i + 4 <= n) {
+      if constexpr (kF32) {
+        const u32x4_any w = *global<u32x4_any>(b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) { const uint32_t x = w[j]; v[j] = __builtin_bit_cast(float, x); }
+      } else {
+        const u32x2_any w = *global<u32x2_any>(b);
+        const uint32_t x = w[0], y = w[1];
+        v[0] = __builtin_bit_cast(float, x << 16);
+        v[1] = __builtin_bit_cast(float, x & 0xFFFF0000u);
+        v[2] = __builtin_bit_cast(float, y << 16);
+        v[3] = __builtin_bit_cast(float, y & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j < n) v[j] = logit<kF32>(lg, at + i + j);
+    }
+    if (i < n) {
+      float* d = to + staged(i);
+      *reinterpret_cast<f32x2_t*>(d) = f32x2_t{v[0], v[1]};
+      *reinterpret_cast<f32x2_t*>(d + 2) = f32x2_t{v[2], v[3]};
+    }
+  }
+}
+
+// Exchange among 16 lanes: rotation by r, and lane j - 1's value for lane j.  (All lanes take part: one that is switched
+// off by a condition gives zeros.)
+template <int r>
+__device__ __forceinline__ int ror16(int v) { return __builtin_amdgcn_mov_dpp(v, 0x120 + r, 0xF, 0xF, true); }
+template <int r>
+__device__ __forceinline__ float ror16(float v) { return __builtin_bit_cast(float, ror16<r>(__builtin_bit_cast(int, v))); }
+__device__ __forceinline__ float before(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x111, 0xF, 0xF, true));
+}
+// Groups ahead of the lane's own: those r, r + 1, .. lanes away, `lanes` to a group.
+template <int r>
+__device__ __forceinline__ void rank_groups(float score, int g, int lanes, int& rank) {
+  if constexpr (r < 16) {
+    if ((r & (lanes - 1)) == 0) {
+      const float o = ror16<r>(score);
+      const int og = ror16<r>(g);
+      rank += o > score || (o == score && og < g);
+    }
+    rank_groups<r + 1>(score, g, lanes, rank);
+  }
+}
+// The two largest of two lanes' two.
+template <int st>
+__device__ __forceinline__ void merge_best(float& a, float& b) {
+  const float oa = pair<st>(a), ob = pair<st>(b);
+  b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+  a = fmaxf(a, oa);
+}
+
+// kN experts a lane, lists of kK >= k.
+template <int kN, int kK>
 __global__ __launch_bounds__(64 * kWaves) void route_group_kernel(const GroupRoute p) {
-  __shared__ double cs[kWaves][kMaxExperts];
+  using K = Key<true>;
+  __shared__ __attribute__((aligned(16))) float stage[kWaves][kStage];
   __shared__ int cnt[kMaxExperts];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, sub = lane & 15, grp = lane >> 4;
+  const int E = p.E, k = p.k, n = E / p.G, lanes = p.lanes, g = sub / lanes, q = sub % lanes;
+  float* const sl = stage[wave];
   if (tid < kMaxExperts) cnt[tid] = 0;
   __syncthreads();
-  for (int64_t t = (int64_t)blockIdx.x * kWaves + wave; t < p.T; t += (int64_t)gridDim.x * kWaves) {
-    const Slot s = route_token<kF32>(p, t, lane, cs[wave]);
-    if (lane < p.k) {
-      p.idx[t * p.k + lane] = s.e;
-      p.prob[t * p.k + lane] = s.w;
-      if (p.counts && (!p.mask || p.mask[t] != 0)) atomicAdd(&cnt[s.e], 1);
+  // what the order goes by: scores where a bias or sums of two count, else the logits themselves
+  const bool sums = p.G > 1 && p.best == 2, scored = p.bias || sums;
+  const bool stats = !p.sigmoid && (scored || !p.renorm);
+  const int own = g < p.G ? n : 0;                      // experts of the lane's group
+  float b[kN];
+#pragma unroll
+  for (int c = 0; c < kN; ++c) b[c] = p.bias && q + lanes * c < own ? p.bias[g * n + q + lanes * c] : 0.f;
+  // errors of two scores and their rounding, twice over (see above; a softmax's sum has more of them)
+  const float t0_err = p.sigmoid ? 0x1p-20f : 0x1p-17f;
+  for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 < p.T; t0 += (int64_t)gridDim.x * kTokens) {
+    const int64_t tw = t0 + 4 * wave, t = tw + grp;
+    const int64_t left = p.T - tw;
+    const bool in = t < p.T;
+    const int have = left >= 4 ? 4 * E : left > 0 ? (int)left * E : 0;
+    wave_lds();
+    if (p.f32) stage_logits<true>(p.logits, tw * E, have, lane, sl);
+    else stage_logits<false>(p.logits, tw * E, have, lane, sl);
+    wave_lds();
+    float l[kN], v[kN];
+    bool live[kN];
+#pragma unroll
+    for (int c = 0; c < kN; ++c) {
+      const int i = q + lanes * c;
+      live[c] = i < own;
+      l[c] = live[c] ? sl[staged(grp * E + g * n + i)] : kNone;
+      v[c] = l[c];
+    }
+    float m = 0.f, total = 0.f;                         // of the whole row's exponentials
+    if (stats) {
+      m = l[0];
+#pragma unroll
+      for (int c = 1; c < kN; ++c) m = fmaxf(m, l[c]);
+      m = group_max<16>(m);
+      m = m == kNone ? 0.f : m;
+#pragma unroll
+      for (int c = 0; c < kN; ++c) {
+        v[c] = __expf(l[c] - m);
+        total += v[c];
+      }
+      total = group_sum<16>(total);
+    }
+    bool bad = false;
+    if (scored) {
+      const float inv = p.sigmoid ? 0.f : 1.0f / total;
+#pragma unroll
+      for (int c = 0; c < kN; ++c) {
+        const float s = p.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-l[c])) : v[c] * inv;
+        v[c] = l[c] == kNone ? kNone : s + b[c];
+      }
+    } else if (stats) {
+#pragma unroll
+      for (int c = 0; c < kN; ++c) v[c] = l[c];
+    }
+    if (p.G > 1) {
+      float x = kNone, y = kNone;                       // the two largest
+      bool nan = false;
+#pragma unroll
+      for (int c = 0; c < kN; ++c) {
+        y = fmaxf(y, fminf(x, v[c]));
+        x = fmaxf(x, v[c]);
+        nan |= v[c] != v[c];
+      }
+      if (lanes > 1) merge_best<0>(x, y);
+      if (lanes > 2) merge_best<1>(x, y);
+      if (lanes > 4) merge_best<2>(x, y);
+      const float score = sums ? x + y : x;
+      int rank = 0;
+      rank_groups<1>(score, g, lanes, rank);
+      const bool kept = own && rank < p.kg;
+      bad = nan;
+      if (scored) {
+        const float lo = -group_max<16>(kept ? -score : kNone), hi = group_max<16>(kept ? kNone : score);
+        const float most = group_max<16>(score > kNone ? fabsf(x) + (sums ? fabsf(y) : 0.f) : 0.f);
+        bad |= !(lo - hi > 2.f * t0_err + 0x1p-21f * most);
+      }
+#pragma unroll
+      for (int c = 0; c < kN; ++c) live[c] = live[c] && kept;
+      if (!p.bias) {
+#pragma unroll
+        for (int c = 0; c < kN; ++c) v[c] = l[c];
+      }
+    }
+    constexpr int kA = kN > kK ? kN : kK;
+    typename K::type a[kA];
+#pragma unroll
+    for (int c = 0; c < kN; ++c) {
+      const typename K::type key = K::make(v[c], g * n + q + lanes * c);
+      a[c] = live[c] ? key : K::none();
+    }
+    sort_top<K, kN, kK>(a);
+    constexpr int kM = kN < kK ? kN : kK;
+    merge_lanes<K, 16, kM, kK, 0>(a);
+    // the lane's slot, and the last one
+    typename K::type mine = a[0], end = a[0];
+#pragma unroll
+    for (int j = 1; j < kK; ++j) {
+      mine = sub == j ? a[j] : mine;
+      end = k - 1 == j ? a[j] : end;
+    }
+    const float least = K::value(end), value = K::value(mine);
+    bad |= !(least > kNone) && least == least;          // fewer experts than k: the others go by their ids
+    const bool slot = sub < k;
+    const int e = slot ? K::expert(mine) : 0;
+    const float le = slot ? sl[staged(grp * E + (e < E ? e : 0))] : kNone;
+    if (p.bias) {
+      const float near = t0_err + 0x1p-22f * fabsf(value), above = before(value);
+      bool odd = slot && sub > 0 && !(above - value > near);
+      odd |= slot && !(fabsf(value) < __builtin_huge_valf());
+      // every expert that reaches the last one's neighbourhood is in the list
+      const float floor = least - (t0_err + 0x1p-22f * fabsf(least));
+      int reach = 0;
+#pragma unroll
+      for (int c = 0; c < kN; ++c) reach += live[c] && v[c] >= floor;
+      reach += dpp_pair<0>(reach);
+      reach += dpp_pair<1>(reach);
+      reach += dpp_pair<2>(reach);
+      reach += dpp_pair<3>(reach);
+      odd |= reach != k;
+      if (__any(odd)) {
+        // equal logits with equal biases are equal in any arithmetic, and in the right order already: they pass
+        const float be = slot ? p.bias[e < E ? e : 0] : 0.f;
+        odd = slot && !(fabsf(value) < __builtin_huge_valf());
+        const float lp = before(le), bp = before(be);
+        odd |= slot && sub > 0 && !(above - value > near) && !(le == lp && be == bp);
+        const int last = (lane & 48) + k - 1;
+        const float ll = __shfl(le, last, 64), bl = __shfl(be, last, 64);
+        int others = slot && !(le == ll && be == bl) ? -1 : 0;
+#pragma unroll
+        for (int c = 0; c < kN; ++c) others += live[c] && v[c] >= floor && !(l[c] == ll && b[c] == bl);
+        others += dpp_pair<0>(others);
+        others += dpp_pair<1>(others);
+        others += dpp_pair<2>(others);
+        others += dpp_pair<3>(others);
+        odd |= others != 0;
+      }
+      bad |= odd;
+    }
+    // weights: of sigmoids as multiples of e^m, which the quotient drops, so that tiny ones keep their ratios
+    float w = 0.f;
+    if (p.sigmoid) {
+      const float top = p.renorm ? fminf(group_max<16>(le), 0.f) : 0.f;
+      w = le >= 0.f ? 1.0f / (1.0f + expf(-le)) : expf(le - top) / (1.0f + expf(le));
+    } else {
+      w = p.renorm ? expf(le - group_max<16>(le)) : expf(le - m) / total;
+    }
+    w = slot ? w : 0.f;
+    if (p.renorm) w /= group_sum<16>(w);
+    const uint64_t again = __ballot(bad && in);
+    const bool done = (again >> (lane & 48) & 0xFFFFu) == 0;
+    if (in && done && slot) {
+      p.idx[t * k + sub] = e;
+      p.prob[t * k + sub] = w * p.scale;
+      if (p.counts && (!p.mask || p.mask[t] != 0)) atomicAdd(&cnt[e], 1);
+    }
+    if (again) {
+      wave_lds();                                       // the stage is free: it holds the 64-bit scores now
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        if ((again >> (16 * i) & 0xFFFFu) == 0) continue;
+        const int64_t ti = tw + i;
+        double* cs = reinterpret_cast<double*>(sl);
+        const Slot s = p.f32 ? route_token<true>(p, ti, lane, cs) : route_token<false>(p, ti, lane, cs);
+        if (lane < k) {
+          p.idx[ti * k + lane] = s.e;
+          p.prob[ti * k + lane] = s.w;
+          if (p.counts && (!p.mask || p.mask[ti] != 0)) atomicAdd(&cnt[s.e], 1);
+        }
+      }
     }
   }
   if (p.counts) {
     __syncthreads();
-    int32_t* to = gridDim.x == 1 ? p.counts : p.part + (int64_t)blockIdx.x * p.E;
-    if (tid < p.E) to[tid] = cnt[tid];
+    int32_t* to = gridDim.x == 1 ? p.counts : p.part + (int64_t)blockIdx.x * E;
+    if (tid < E) to[tid] = cnt[tid];
   }
 }
 
-// counts[e] = sum over the nb blocks; a workgroup takes 16 experts.
-__global__ __launch_bounds__(256) void route_counts_kernel(const int32_t* __restrict__ part, int nb, int E,
-                                                           int32_t* __restrict__ counts) {
-  __shared__ int red[16][16];
+template <int kN>
+void launch_k(const GroupRoute& p, int nb, hipStream_t st) {
+  if (p.k <= 2) route_group_kernel<kN, 2><<<nb, 64 * kWaves, 0, st>>>(p);
+  else if (p.k <= 4) route_group_kernel<kN, 4><<<nb, 64 * kWaves, 0, st>>>(p);
+  else if (p.k <= 8) route_group_kernel<kN, 8><<<nb, 64 * kWaves, 0, st>>>(p);
+  else route_group_kernel<kN, 16><<<nb, 64 * kWaves, 0, st>>>(p);
+}
+
+// counts[e] = sum over the nb blocks; a workgroup takes 16 experts, 64 slices of the blocks.
+constexpr int kCountThreads = 1024;
+__global__ __launch_bounds__(kCountThreads) void route_counts_kernel(const int32_t* __restrict__ part, int nb, int E,
+                                                                     int32_t* __restrict__ counts) {
+  constexpr int kS = kCountThreads / 16;
+  __shared__ int red[kS][16];
   const int le = threadIdx.x & 15, s = threadIdx.x >> 4, e = blockIdx.x * 16 + le;
   int c = 0;
-  if (e < E)
-    for (int b = s; b < nb; b += 16) c += part[(int64_t)b * E + e];
+  if (e < E) {
+    int i = s;
+    for (; i + 7 * kS < nb; i += 8 * kS) {
+      int v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = part[(int64_t)(i + u * kS) * E + e];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) c += v[u];
+    }
+    for (; i < nb; i += kS) c += part[(int64_t)i * E + e];
+  }
   red[s][le] = c;
   __syncthreads();
-  if (s == 0 && e < E) {
-    for (int i = 1; i < 16; ++i) c += red[i][le];
-    counts[e] = c;
+  for (int h = kS / 2; h >= 1; h /= 2) {
+    if (s < h) red[s][le] += red[s + h][le];
+    __syncthreads();
   }
+  if (s == 0 && e < E) counts[e] = red[0][le];
 }
 
 // ---- backward: a wave takes a token.
@@ -263,15 +536,24 @@ __global__ __launch_bounds__(64 * kWaves) void route_group_bwd_kernel(const Grou
 }  // namespace
 
 int route_group_blocks(int64_t T) {
-  const int64_t nb = (T + kWaves - 1) / kWaves;
+  const int64_t nb = (T + kTokens - 1) / kTokens;
   return (int)(nb < kGroupMaxBlocks ? nb : kGroupMaxBlocks);
 }
 
-hipError_t launch_route_group(const GroupRoute& p, bool f32, hipStream_t st) {
+hipError_t launch_route_group(GroupRoute p, bool f32, hipStream_t st) {
   const int nb = route_group_blocks(p.T);
-  if (f32) route_group_kernel<true><<<nb, 64 * kWaves, 0, st>>>(p);
-  else route_group_kernel<false><<<nb, 64 * kWaves, 0, st>>>(p);
-  if (p.counts && nb > 1) route_counts_kernel<<<(p.E + 15) / 16, 256, 0, st>>>(p.part, nb, p.E, p.counts);
+  int wide = 1;
+  while (wide < p.G) wide *= 2;
+  p.f32 = f32;
+  p.lanes = 16 / wide;
+  const int per = (p.E / p.G + p.lanes - 1) / p.lanes;  // experts a lane
+  if (per <= 1) launch_k<1>(p, nb, st);
+  else if (per <= 2) launch_k<2>(p, nb, st);
+  else if (per <= 4) launch_k<4>(p, nb, st);
+  else if (per <= 8) launch_k<8>(p, nb, st);
+  else if (per <= 16) launch_k<16>(p, nb, st);
+  else launch_k<32>(p, nb, st);
+  if (p.counts && nb > 1) route_counts_kernel<<<(p.E + 15) / 16, kCountThreads, 0, st>>>(p.part, nb, p.E, p.counts);
   return hipGetLastError();
 }
 

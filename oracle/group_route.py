@@ -1,7 +1,8 @@
 """Routing by scores with a bias and groups, and its gradient, in fp64 -- TEST INFRASTRUCTURE ONLY.
 
 Loops over tokens and sorts of Python tuples, apart from the kernels' networks: an order is (value
-descending with NaN first, id ascending).
+descending with NaN first, id ascending).  Without a bias experts (and groups of one best) go by their logits, whose order
+is that of the scores as real numbers; else scores are compared as fp64 values.
 """
 from __future__ import annotations
 
@@ -44,11 +45,11 @@ def forward(logits, k, bias=None, score="sigmoid", groups=1, topk_groups=None, g
     c = np.where(lg == -np.inf, -np.inf, c)
     idx, prob = np.zeros((T, k), dtype=np.int32), np.zeros((T, k))
     for t in range(T):
-        v = c[t].copy()
+        v = (lg if bias is None else c)[t].copy()
         if groups > 1:
             sums = []
             for g in range(groups):
-                part = v[g * n:(g + 1) * n]
+                part = (v if group_best == 1 else c[t])[g * n:(g + 1) * n]
                 best = [part[i] for i in _order(part)[:group_best]]
                 sums.append(best[0] + best[1] if group_best == 2 else best[0])
             for g in _order(sums)[topk_groups:]:
