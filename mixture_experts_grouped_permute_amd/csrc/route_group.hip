@@ -188,7 +188,7 @@ __device__ __forceinline__ Slot route_token(const GroupRoute& p, int64_t t, int 
 // ---- the logits of a wave's 4 tokens, which lie one after the other, in LDS: loads of 16 bytes a lane whatever E is,
 // and the lanes take their experts from there.  2 words of room after each 32 keep the lanes of groups of 16 or 32
 // experts on banks of their own.
-constexpr int kStage = 4 * kMaxExperts / 32 * 34;
+constexpr int kStage = 34 * 34;                         // 4 x 256 values, and what a group's last lanes read past them
 __device__ __forceinline__ int staged(int i) { return i + (i >> 5) * 2; }
 
 template <bool kF32>
@@ -283,13 +283,15 @@ __global__ __launch_bounds__(64 * kWaves) void route_group_kernel(const GroupRou
     if (p.f32) stage_logits<true>(p.logits, tw * E, have, lane, sl);
     else stage_logits<false>(p.logits, tw * E, have, lane, sl);
     wave_lds();
-    float l[kN], v[kN];
-    bool live[kN];
+    // (not known to be the same in every turn: places and ids would all be kept in registers)
+    int q1 = q, e0 = (own ? g * n : 0) + q;
+    asm volatile("" : "+v"(q1), "+v"(e0));
+    float l[kN], v[kN];                                 // (-inf: no expert, which like one of -inf is never selected here)
+#pragma unroll
+    for (int c = 0; c < kN; ++c) l[c] = sl[staged(grp * E + e0 + lanes * c)];
 #pragma unroll
     for (int c = 0; c < kN; ++c) {
-      const int i = q + lanes * c;
-      live[c] = i < own;
-      l[c] = live[c] ? sl[staged(grp * E + g * n + i)] : kNone;
+      l[c] = q1 + lanes * c < own ? l[c] : kNone;
       v[c] = l[c];
     }
     float m = 0.f, total = 0.f;                         // of the whole row's exponentials
@@ -341,19 +343,12 @@ __global__ __launch_bounds__(64 * kWaves) void route_group_kernel(const GroupRou
         bad |= !(lo - hi > 2.f * t0_err + 0x1p-21f * most);
       }
 #pragma unroll
-      for (int c = 0; c < kN; ++c) live[c] = live[c] && kept;
-      if (!p.bias) {
-#pragma unroll
-        for (int c = 0; c < kN; ++c) v[c] = l[c];
-      }
+      for (int c = 0; c < kN; ++c) v[c] = kept ? p.bias ? v[c] : l[c] : kNone;
     }
     constexpr int kA = kN > kK ? kN : kK;
     typename K::type a[kA];
 #pragma unroll
-    for (int c = 0; c < kN; ++c) {
-      const typename K::type key = K::make(v[c], g * n + q + lanes * c);
-      a[c] = live[c] ? key : K::none();
-    }
+    for (int c = 0; c < kN; ++c) a[c] = K::make(v[c], e0 + lanes * c);
     sort_top<K, kN, kK>(a);
     constexpr int kM = kN < kK ? kN : kK;
     merge_lanes<K, 16, kM, kK, 0>(a);
@@ -377,7 +372,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_group_kernel(const GroupRou
       const float floor = least - (t0_err + 0x1p-22f * fabsf(least));
       int reach = 0;
 #pragma unroll
-      for (int c = 0; c < kN; ++c) reach += live[c] && v[c] >= floor;
+      for (int c = 0; c < kN; ++c) reach += v[c] >= floor;
       reach += dpp_pair<0>(reach);
       reach += dpp_pair<1>(reach);
       reach += dpp_pair<2>(reach);
@@ -393,7 +388,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_group_kernel(const GroupRou
         const float ll = __shfl(le, last, 64), bl = __shfl(be, last, 64);
         int others = slot && !(le == ll && be == bl) ? -1 : 0;
 #pragma unroll
-        for (int c = 0; c < kN; ++c) others += live[c] && v[c] >= floor && !(l[c] == ll && b[c] == bl);
+        for (int c = 0; c < kN; ++c) others += v[c] >= floor && !(sl[staged(grp * E + e0 + lanes * c)] == ll && b[c] == bl);
         others += dpp_pair<0>(others);
         others += dpp_pair<1>(others);
         others += dpp_pair<2>(others);
