@@ -428,7 +428,9 @@ moe_status moe_grad_sumsq(const void* const* grads, const int64_t* numel, const 
  *             out_dtypes; out[i] may be grads[i] (in place, of one type; then
  *             nothing is written where c is 1).  Other overlaps between out and
  *             any tensor of the call are refused (MOE_ERR_INVALID_ARG).
- * sumsq       [1] fp64, device (moe_grad_sumsq's, or the sum of several).
+ * sumsq       [1] fp64, device (moe_grad_sumsq's, or the sum of several), or
+ *             NULL: that of grads, computed here in moe_grad_sumsq_workspace
+ *             bytes of workspace (else unused).
  * max_norm    at least 0 (infinity: never scaled).
  * norm        [1] fp32 out, device.
  * The product is fp32, rounded once.  An infinite sumsq gives c = 0 (and NaN
@@ -436,7 +438,7 @@ moe_status moe_grad_sumsq(const void* const* grads, const int64_t* numel, const 
  * ------------------------------------------------------------------------ */
 moe_status moe_grad_clip(const void* const* grads, const int64_t* numel, const int32_t* dtypes, int n,
                          void* const* out, const int32_t* out_dtypes, const double* sumsq, float max_norm,
-                         float* norm, void* stream);
+                         float* norm, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * fp8_block_quantize -- E4M3 with one fp32 scale per 128 values.

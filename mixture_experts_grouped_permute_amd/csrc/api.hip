@@ -934,8 +934,9 @@ moe_status moe_grad_sumsq(const void* const* grads, const int64_t* numel, const 
 }
 
 moe_status moe_grad_clip(const void* const* grads, const int64_t* numel, const int32_t* dtypes, int n, void* const* out,
-                         const int32_t* out_dtypes, const double* sumsq, float max_norm, float* norm, void* stream) {
-  MOE_CHECK(grads && numel && dtypes && out && out_dtypes && sumsq && norm && n >= 1, MOE_ERR_INVALID_ARG);
+                         const int32_t* out_dtypes, const double* sumsq, float max_norm, float* norm, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  MOE_CHECK(grads && numel && dtypes && out && out_dtypes && norm && n >= 1, MOE_ERR_INVALID_ARG);
   MOE_CHECK(max_norm >= 0.0f, MOE_ERR_INVALID_ARG);
   MOE_CHECK(n <= MOE_MAX_GRADS, MOE_ERR_UNSUPPORTED);
   for (int i = 0; i < n; ++i) {
@@ -945,8 +946,12 @@ moe_status moe_grad_clip(const void* const* grads, const int64_t* numel, const i
   }
   const moe_status s = check_apart(grads, numel, dtypes, n, out, out_dtypes);
   if (s != MOE_OK) return s;
+  if (!sumsq) {
+    MOE_CHECK(workspace && workspace_bytes >= moe_grad_sumsq_workspace(numel, n), MOE_ERR_WORKSPACE);
+    MOE_CHECK(aligned16(workspace), MOE_ERR_UNSUPPORTED);
+  }
   const GradList l{grads, numel, dtypes, out, out_dtypes, n};
-  HIP_TRY(launch_grad_clip(l, sumsq, max_norm, norm, reinterpret_cast<hipStream_t>(stream)));
+  HIP_TRY(launch_grad_clip(l, sumsq, reinterpret_cast<double*>(workspace), max_norm, norm, reinterpret_cast<hipStream_t>(stream)));
   return MOE_OK;
 }
 

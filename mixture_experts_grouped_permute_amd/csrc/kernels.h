@@ -303,8 +303,9 @@ struct GradList {
   const int32_t* out_dtype;
   int n;
 };
-int64_t grad_parts(const int64_t* numel, int n);          // doubles of scratch
+int64_t grad_parts(const int64_t* numel, int n);          // doubles of scratch (one more than the parts)
 hipError_t launch_grad_sumsq(const GradList& l, double* part, double* sumsq, hipStream_t st);
-hipError_t launch_grad_clip(const GradList& l, const double* sumsq, float max_norm, float* norm, hipStream_t st);
+// sumsq null: of l itself, through part
+hipError_t launch_grad_clip(const GradList& l, const double* sumsq, double* part, float max_norm, float* norm, hipStream_t st);
 
 }  // namespace moe

@@ -488,8 +488,9 @@ BwdPlan plan_bwd(int64_t T, int64_t H) {
 }
 
 template <bool kF32, bool kW32>
-hipError_t launch_bwd(const NormBwd& p, hipStream_t st) {
+hipError_t launch_bwd(NormBwd p, hipStream_t st) {
   const BwdPlan b = plan_bwd(p.T, p.H);
+  if (b.blocks == 1) p.part = p.dw;                     // the only part
   hipError_t e;
   if (p.H < 8) {
     narrow_rmsnorm_bwd_kernel<kF32, kW32><<<b.blocks, 256, 0, st>>>(p);
@@ -503,7 +504,7 @@ hipError_t launch_bwd(const NormBwd& p, hipStream_t st) {
       return hipGetLastError();
     });
   }
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || b.blocks == 1) return e;
   rmsnorm_dw_kernel<<<(unsigned)((p.H + 15) / 16), kSumThreads, 0, st>>>(p.part, b.blocks, (int)p.H, p.dw);
   return hipGetLastError();
 }

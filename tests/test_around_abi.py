@@ -120,17 +120,20 @@ def test_grad_sumsq_validation(lib):
     assert lib.moe_grad_sumsq(g, numel, kinds, 3, P, P + 8, need, None) == uns
 
 
-def _clip(lib, ptrs, numel, kinds, outs, okinds, *, sumsq=P, max_norm=1.0, norm=None):
+def _clip(lib, ptrs, numel, kinds, outs, okinds, *, sumsq=P, max_norm=1.0, norm=None, ws=None, wbytes=0):
     """(with norm None every call is refused: the others of the checks come first)"""
     g, n, k = _arrays(ptrs, numel, kinds)
     o, _, ok = _arrays(outs, numel, okinds)
-    return lib.moe_grad_clip(g, n, k, len(ptrs), o, ok, sumsq, max_norm, norm, None)
+    return lib.moe_grad_clip(g, n, k, len(ptrs), o, ok, sumsq, max_norm, norm, ws, wbytes, None)
 
 
 def test_grad_clip_validation(lib):
-    inv, uns, _ = _codes()
+    inv, uns, wsp = _codes()
     assert _clip(lib, [P], [4], [0], [P], [0]) == inv                             # no norm
-    assert _clip(lib, [P], [4], [0], [P], [0], sumsq=None, norm=P) == inv
+    need = lib.moe_grad_sumsq_workspace((ctypes.c_int64 * 1)(4), 1)               # its own sum takes a workspace
+    assert _clip(lib, [P], [4], [0], [P], [0], sumsq=None, norm=P) == wsp
+    assert _clip(lib, [P], [4], [0], [P], [0], sumsq=None, norm=P, ws=P, wbytes=need - 1) == wsp
+    assert _clip(lib, [P], [4], [0], [P], [0], sumsq=None, norm=P, ws=P + 8, wbytes=need) == uns
     assert _clip(lib, [P], [4], [0], [P], [0], max_norm=-1.0, norm=P) == inv
     assert _clip(lib, [P], [4], [0], [P], [0], max_norm=float("nan"), norm=P) == inv
     assert _clip(lib, [P], [4], [0], [None], [0], norm=P) == inv
