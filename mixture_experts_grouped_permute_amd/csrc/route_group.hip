@@ -191,7 +191,7 @@ __device__ __forceinline__ Slot route_token(const GroupRoute& p, int64_t t, int 
 constexpr int kStage = 34 * 34;                         // 4 x 256 values, and what a group's last lanes read past them
 __device__ __forceinline__ int staged(int i) { return i + (i >> 5) * 2; }
 
-template <bool kF32>
+template <bool kF32, bool kRoom = true>
 __device__ __forceinline__ void stage_logits(const void* lg, int64_t at, int n, int lane, float* to) {
 #pragma unroll
   for (int u = 0; u < kMaxExperts / 64; ++u) {
@@ -218,7 +218,7 @@ __device__ __forceinline__ void stage_logits(const void* lg, int64_t at, int n, 
         if (i + j < n) v[j] = logit<kF32>(lg, at + i + j);
     }
     if (i < n) {
-      float* d = to + staged(i);
+      float* d = to + (kRoom ? staged(i) : i);
       *reinterpret_cast<f32x2_t*>(d) = f32x2_t{v[0], v[1]};
       *reinterpret_cast<f32x2_t*>(d + 2) = f32x2_t{v[2], v[3]};
     }
@@ -473,59 +473,136 @@ __global__ __launch_bounds__(kCountThreads) void route_counts_kernel(const int32
   if (s == 0 && e < E) counts[e] = red[0][le];
 }
 
-// ---- backward: a wave takes a token.
+// ---- backward.  A wave takes 4 tokens, whose rows of dlogits lie one after the other: they are put together in LDS and
+// leave as 16 bytes a lane, whatever E is.  kN: experts a lane where every logit has a gradient (softmax weights as they
+// are), 0 where only the selected ones have.
 template <bool kF32>
-__global__ __launch_bounds__(64 * kWaves) void route_group_bwd_kernel(const GroupRouteBwd p) {
-  __shared__ float row[kWaves][kMaxExperts];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int64_t t = (int64_t)blockIdx.x * kWaves + wave; t < p.T; t += (int64_t)gridDim.x * kWaves) {
-    int e = -1;
-    float w = 0.f, g = 0.f;
-    if (lane < p.k) {
-      e = p.idx[t * p.k + lane];
-      w = p.prob[t * p.k + lane];
-      g = p.dprob[t * p.k + lane];
-    }
-    float sum = w * g;
+__device__ __forceinline__ void store_rows(void* to, int64_t at, int n, int lane, const float* from) {
+  constexpr int kV = kF32 ? 4 : 8;
+  for (int i = lane * kV; i < n; i += 64 * kV) {
+    float v[8];
+    *reinterpret_cast<f32x4*>(v) = *reinterpret_cast<const f32x4*>(from + i);
+    if constexpr (!kF32) *reinterpret_cast<f32x4*>(v + 4) = *reinterpret_cast<const f32x4*>(from + i + 4);
+    char* b = reinterpret_cast<char*>(to) + (at + i) * (kF32 ? 4 : 2);
+    if (i + kV <= n) {
+      u32x4 w;
 #pragma unroll
-    for (int d = 8; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);   // (k <= 16; in the first 16 lanes)
-    sum = __shfl(sum, 0, 64);
-    float d = w * (p.renorm ? g - sum / p.scale : g);
-    const bool has = e >= 0 && e < p.E;
-    if (p.sigmoid && has) d *= 1.0f / (1.0f + expf(logit<kF32>(p.logits, t * p.E + e)));
-    float p_scale = 0.f, m = 0.f;
-    if (!p.sigmoid && !p.renorm) {
-      m = -__builtin_huge_valf();
-      for (int i = lane; i < p.E; i += 64) m = fmaxf(m, logit<kF32>(p.logits, t * p.E + i));
+      for (int j = 0; j < 4; ++j) w[j] = kF32 ? __builtin_bit_cast(uint32_t, v[j]) : pack_bf16x2(v[2 * j], v[2 * j + 1]);
+      // (bf16 past the caches: 131072 x 256 of softmax weights as they are, 70 us through them, 46 past; fp32: 34, 39)
+      if constexpr (kF32) *global<u32x4_any>(b) = w;
+      else __builtin_nontemporal_store(w, global<u32x4_any>(b));
+    } else {
 #pragma unroll
-      for (int x = 32; x >= 1; x >>= 1) m = fmaxf(m, __shfl_xor(m, x, 64));
-      if (m == -__builtin_huge_valf()) m = 0.f;
-      float s = 0.f;
-      for (int i = lane; i < p.E; i += 64) s += expf(logit<kF32>(p.logits, t * p.E + i) - m);
-#pragma unroll
-      for (int x = 32; x >= 1; x >>= 1) s += __shfl_xor(s, x, 64);
-      p_scale = s == 0.f ? 0.f : -sum / s;
+      for (int j = 0; j < kV; ++j)
+        if (i + j < n) {
+          if constexpr (kF32) reinterpret_cast<float*>(b)[j] = v[j];
+          else reinterpret_cast<uint16_t*>(b)[j] = f32_to_bf16(v[j]);
+        }
     }
-    for (int i = lane; i < p.E; i += 64) {
-      float v = 0.f;
-      if (!p.sigmoid && !p.renorm) v = p_scale * expf(logit<kF32>(p.logits, t * p.E + i) - m);
-      row[wave][i] = v;
-    }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    for (int j = 0; j < p.k; ++j) {                     // in the slots' order, also where an id repeats
-      if (lane == j && has) row[wave][e] += d;
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-    }
-    for (int i = lane; i < p.E; i += 64) {
-      const float v = row[wave][i];
-      if constexpr (kF32) reinterpret_cast<float*>(p.dlogits)[t * p.E + i] = v;
-      else reinterpret_cast<uint16_t*>(p.dlogits)[t * p.E + i] = f32_to_bf16(v);
-    }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
   }
+}
+
+// d summed over the slots of the same expert, in a fixed order; whether the lane's is the first of them.
+template <int r>
+__device__ __forceinline__ void add_same(int e, float d, int sub, float& sum, bool& first) {
+  if constexpr (r < 16) {
+    const int oe = ror16<r>(e), os = ror16<r>(sub);
+    const float od = ror16<r>(d);
+    sum += oe == e ? od : 0.f;
+    first = first && !(oe == e && os < sub);
+    add_same<r + 1>(e, d, sub, sum, first);
+  }
+}
+
+template <bool kF32, int kN>
+__global__ __launch_bounds__(64 * kWaves) void route_group_bwd_kernel(const GroupRouteBwd p) {
+  __shared__ __attribute__((aligned(16))) float rows[kWaves][4 * kMaxExperts + 8];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, sub = lane & 15, grp = lane >> 4, E = p.E, k = p.k;
+  float* const row = rows[wave];
+  for (int i = lane; i < 4 * kMaxExperts + 8; i += 64) row[i] = 0.f;
+  for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 < p.T; t0 += (int64_t)gridDim.x * kTokens) {
+    const int64_t tw = t0 + 4 * wave, t = tw + grp, left = p.T - tw;
+    if (left <= 0) break;                               // (the wave's last turn: nothing below waits for the others)
+    const int have = left >= 4 ? 4 * E : (int)left * E;
+    int e = -1 - sub;                                   // (no slot: an id of its own)
+    float w = 0.f, g = 0.f;
+    if (t < p.T && sub < k) {
+      const int64_t at = t * k + sub;
+      e = p.idx[at];
+      w = p.prob[at];
+      g = p.dprob[at];
+    }
+    const bool has = e >= 0 && e < E;
+    const float sum = group_sum<16>(w * g);
+    float d = w * (p.renorm ? g - sum / p.scale : g);
+    if (p.sigmoid && has) d *= 1.0f / (1.0f + expf(logit<kF32>(p.logits, t * E + e)));
+    float* const mine = row + grp * E;
+    if constexpr (kN > 0) {
+      float v[kN > 0 ? kN : 1], m = kNone, s = 0.f;
+      // (bf16 through LDS: 131072 x 256 71 us with 2-byte loads of 16 lanes, 42 so; fp32 46, 52)
+      if constexpr (kF32) {
+#pragma unroll
+        for (int c = 0; c < kN; ++c) {
+          v[c] = kNone;
+          if (t < p.T && sub + 16 * c < E) v[c] = logit<kF32>(p.logits, t * E + sub + 16 * c);
+        }
+      } else {
+        stage_logits<kF32, false>(p.logits, tw * E, have, lane, row);
+        wave_lds();
+#pragma unroll
+        for (int c = 0; c < kN; ++c) v[c] = mine[sub + 16 * c < E ? sub + 16 * c : 0];
+      }
+#pragma unroll
+      for (int c = 0; c < kN; ++c) {
+        v[c] = sub + 16 * c < E ? v[c] : kNone;
+        m = fmaxf(m, v[c]);
+      }
+      m = group_max<16>(m);
+      m = m == kNone ? 0.f : m;
+#pragma unroll
+      for (int c = 0; c < kN; ++c) {
+        v[c] = __expf(v[c] - m);
+        s += v[c];
+      }
+      s = group_sum<16>(s);
+      const float by = s == 0.f ? 0.f : -sum / s;
+      wave_lds();
+#pragma unroll
+      for (int c = 0; c < kN; ++c)
+        if (sub + 16 * c < E) mine[sub + 16 * c] = v[c] * by;
+    }
+    wave_lds();
+    // the selected ones' own part; a slot that finds another's number at its expert shares it
+    const float before_it = has ? mine[e] : 0.f;
+    wave_lds();
+    if (has) mine[e] = __builtin_bit_cast(float, sub);
+    wave_lds();
+    const bool shared = has && __builtin_bit_cast(int, mine[e]) != sub;
+    bool first = has;
+    if (__any(shared)) {
+      float all = d;
+      add_same<1>(e, d, sub, all, first);
+      d = all;
+    }
+    wave_lds();
+    if (first) mine[e] = before_it + d;
+    wave_lds();
+    store_rows<kF32>(p.dlogits, tw * E, have, lane, row);
+    wave_lds();
+    if (kN == 0 && has) mine[e] = 0.f;
+    wave_lds();
+  }
+}
+
+template <bool kF32>
+void launch_bwd(const GroupRouteBwd& p, hipStream_t st) {
+  const int64_t nb = (p.T + kTokens - 1) / kTokens;
+  const int grid = (int)(nb < 2048 ? nb : 2048);
+  if (p.sigmoid || p.renorm) route_group_bwd_kernel<kF32, 0><<<grid, 64 * kWaves, 0, st>>>(p);
+  else if (p.E <= 32) route_group_bwd_kernel<kF32, 2><<<grid, 64 * kWaves, 0, st>>>(p);
+  else if (p.E <= 64) route_group_bwd_kernel<kF32, 4><<<grid, 64 * kWaves, 0, st>>>(p);
+  else if (p.E <= 128) route_group_bwd_kernel<kF32, 8><<<grid, 64 * kWaves, 0, st>>>(p);
+  else route_group_bwd_kernel<kF32, 16><<<grid, 64 * kWaves, 0, st>>>(p);
 }
 
 }  // namespace
@@ -553,10 +630,8 @@ hipError_t launch_route_group(GroupRoute p, bool f32, hipStream_t st) {
 }
 
 hipError_t launch_route_group_bwd(const GroupRouteBwd& p, bool f32, hipStream_t st) {
-  const int64_t nb = (p.T + kWaves - 1) / kWaves;
-  const int grid = (int)(nb < 2048 ? nb : 2048);
-  if (f32) route_group_bwd_kernel<true><<<grid, 64 * kWaves, 0, st>>>(p);
-  else route_group_bwd_kernel<false><<<grid, 64 * kWaves, 0, st>>>(p);
+  if (f32) launch_bwd<true>(p, st);
+  else launch_bwd<false>(p, st);
   return hipGetLastError();
 }
 
