@@ -839,7 +839,7 @@ moe_status moe_route_balance_bwd(const void* logits, int logits_dtype, const uin
 
 size_t moe_route_grouped_workspace(int64_t T, int E) {
   if (T <= 0 || E <= 0 || E > MOE_MAX_EXPERTS) return 0;
-  return align_up((size_t)route_group_blocks(T) * (size_t)E * sizeof(int32_t));
+  return align_up((size_t)route_group_parts(T) * (size_t)E * sizeof(int32_t));
 }
 
 moe_status moe_route_grouped(const void* logits, int logits_dtype, const float* bias, const uint8_t* token_mask, int64_t T,

@@ -247,11 +247,11 @@ struct GroupRoute {
   int32_t* idx;
   float* prob;
   int32_t* counts;           // [E] or null
-  int32_t* part;             // counts: route_group_blocks(T) x E int32
+  int32_t* part;             // counts: route_group_parts(T) x E int32
   bool f32;                  // (the launcher's)
   int lanes;
 };
-int route_group_blocks(int64_t T);
+int route_group_parts(int64_t T);
 hipError_t launch_route_group(GroupRoute p, bool f32, hipStream_t st);
 struct GroupRouteBwd {
   const void* logits;

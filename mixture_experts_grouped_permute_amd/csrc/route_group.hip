@@ -109,22 +109,34 @@ __device__ __forceinline__ Slot route_token(const GroupRoute& p, int64_t t, int 
   if (p.G > 1) {
     const int n = p.E / p.G;
     wave_lds();
-    uint64_t mine = 0;
-    if (lane < p.G) {
-      double a = none, b = none;                        // the two largest
-      uint64_t ka = 0, kb = 0;
-      for (int i = 0; i < n; ++i) {
-        const double v = cs[lane * n + i];
+    // 4 p.lanes lanes to a group, which then compare what they have found
+    const int per = 4 * p.lanes, gi = lane / per;
+    double a = none, b = none;                          // the two largest
+    uint64_t ka = 0, kb = 0;                            // (0: none yet)
+    if (gi < p.G)
+      for (int i = lane % per; i < n; i += per) {
+        const double v = cs[gi * n + i];
         const uint64_t kv = order_of(v);
-        if (i == 0 || kv > ka) {
+        if (kv > ka) {
           b = a; kb = ka;
           a = v; ka = kv;
         } else if (kv > kb) {
           b = v; kb = kv;
         }
       }
-      mine = order_of(p.best == 2 ? a + b : a);
+    for (int d = 1; d < per; d *= 2) {
+      const double oa = __shfl_xor(a, d, 64), ob = __shfl_xor(b, d, 64);
+      const uint64_t ka2 = order_of(oa) & (uint64_t)-(int64_t)(__shfl_xor((int)(ka != 0), d, 64)),
+                     kb2 = order_of(ob) & (uint64_t)-(int64_t)(__shfl_xor((int)(kb != 0), d, 64));
+      if (ka2 > ka) {
+        if (ka >= kb2) { b = a; kb = ka; } else { b = ob; kb = kb2; }
+        a = oa; ka = ka2;
+      } else if (ka2 > kb) {
+        b = oa; kb = ka2;
+      }
     }
+    const uint64_t sum = order_of(p.best == 2 ? a + b : a);
+    const uint64_t mine = shfl_u64(sum, (lane < p.G ? lane : 0) * per);
     wave_lds();
     int rank = 0;
     for (int h = 0; h < p.G; ++h) {
@@ -185,42 +197,57 @@ __device__ __forceinline__ Slot route_token(const GroupRoute& p, int64_t t, int 
   return r;
 }
 
+__device__ __forceinline__ void token_again(const GroupRoute& p, int64_t t, int lane, double* cs, int* cnt) {
+  const Slot s = p.f32 ? route_token<true>(p, t, lane, cs) : route_token<false>(p, t, lane, cs);
+  if (lane < p.k) {
+    p.idx[t * p.k + lane] = s.e;
+    p.prob[t * p.k + lane] = s.w;
+    if (p.counts && (!p.mask || p.mask[t] != 0)) atomicAdd(&cnt[s.e], 1);
+  }
+}
+
 // ---- the logits of a wave's 4 tokens, which lie one after the other, in LDS: loads of 16 bytes a lane whatever E is,
 // and the lanes take their experts from there.  2 words of room after each 32 keep the lanes of groups of 16 or 32
-// experts on banks of their own.
-constexpr int kStage = 34 * 34;                         // 4 x 256 values, and what a group's last lanes read past them
-__device__ __forceinline__ int staged(int i) { return i + (i >> 5) * 2; }
+// experts on banks of their own.  Places are counted through the workgroup's stage, kSpan for each wave (4 x 256 values,
+// and what a group's last lanes read past them), in bytes: a place is then two instructions.
+constexpr uint32_t kSpan = 1088;
+__device__ __forceinline__ constexpr uint32_t room(uint32_t i) { return i * 4 + (i * 4 >> 7) * 8; }
+template <class T = float>
+__device__ __forceinline__ T& at_room(char* stage, uint32_t i) { return *reinterpret_cast<T*>(stage + room(i)); }
 
-template <bool kF32, bool kRoom = true>
-__device__ __forceinline__ void stage_logits(const void* lg, int64_t at, int n, int lane, float* to) {
+// n values of lg from `at` on to places `to` .. (kRoom) or words `to` .. of `stage`.  kU: 256-value pieces that n has at
+// most.  Lanes past the end repeat the last piece, so that no branch parts the loads.
+template <bool kF32, int kU, bool kRoom = true>
+__device__ __forceinline__ void stage_logits(const void* lg, int64_t at, int n, int lane, char* stage, uint32_t to) {
+  const auto put = [&](uint32_t i, f32x2_t v) {
+    *reinterpret_cast<f32x2_t*>(stage + (kRoom ? room(to + i) : (to + i) * 4)) = v;
+  };
+  if (n & 3) {                                          // the last tokens
+    for (int i = lane; i < n; i += 64)
+      *reinterpret_cast<float*>(stage + (kRoom ? room(to + i) : (to + i) * 4)) = logit<kF32>(lg, at + i);
+  } else if (n) {
+    f32x2_t v[kU][2];
 #pragma unroll
-  for (int u = 0; u < kMaxExperts / 64; ++u) {
-    const int i = (u * 64 + lane) * 4;
-    if (u * 256 >= n) break;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    const char* b = reinterpret_cast<const char*>(lg) + (at + i) * (kF32 ? 4 : 2);
-    if (i + 4 <= n) {
+    for (int u = 0; u < kU; ++u) {
+      const int i = min((u * 64 + lane) * 4, n - 4);
+      const char* b = reinterpret_cast<const char*>(lg) + (at + i) * (kF32 ? 4 : 2);
       if constexpr (kF32) {
         const u32x4_any w = *global<u32x4_any>(b);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) { const uint32_t x = w[j]; v[j] = __builtin_bit_cast(float, x); }
+        const uint32_t x[4] = {w[0], w[1], w[2], w[3]};
+        v[u][0] = f32x2_t{__builtin_bit_cast(float, x[0]), __builtin_bit_cast(float, x[1])};
+        v[u][1] = f32x2_t{__builtin_bit_cast(float, x[2]), __builtin_bit_cast(float, x[3])};
       } else {
         const u32x2_any w = *global<u32x2_any>(b);
         const uint32_t x = w[0], y = w[1];
-        v[0] = __builtin_bit_cast(float, x << 16);
-        v[1] = __builtin_bit_cast(float, x & 0xFFFF0000u);
-        v[2] = __builtin_bit_cast(float, y << 16);
-        v[3] = __builtin_bit_cast(float, y & 0xFFFF0000u);
+        v[u][0] = f32x2_t{__builtin_bit_cast(float, x << 16), __builtin_bit_cast(float, x & 0xFFFF0000u)};
+        v[u][1] = f32x2_t{__builtin_bit_cast(float, y << 16), __builtin_bit_cast(float, y & 0xFFFF0000u)};
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (i + j < n) v[j] = logit<kF32>(lg, at + i + j);
     }
-    if (i < n) {
-      float* d = to + (kRoom ? staged(i) : i);
-      *reinterpret_cast<f32x2_t*>(d) = f32x2_t{v[0], v[1]};
-      *reinterpret_cast<f32x2_t*>(d + 2) = f32x2_t{v[2], v[3]};
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const uint32_t i = (uint32_t)min((u * 64 + lane) * 4, n - 4);
+      put(i, v[u][0]);                                  // (4 values of a multiple of 4 lie between two rooms)
+      put(i + 2, v[u][1]);
     }
   }
 }
@@ -234,16 +261,15 @@ __device__ __forceinline__ float ror16(float v) { return __builtin_bit_cast(floa
 __device__ __forceinline__ float before(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x111, 0xF, 0xF, true));
 }
-// Groups ahead of the lane's own: those r, r + 1, .. lanes away, `lanes` to a group.
-template <int r>
-__device__ __forceinline__ void rank_groups(float score, int g, int lanes, int& rank) {
+// How many groups are ahead of the lane's own, kL lanes to a group: those kL, 2 kL, .. lanes away.
+template <int kL, int r = kL>
+__device__ __forceinline__ int rank_groups(float score, int g) {
   if constexpr (r < 16) {
-    if ((r & (lanes - 1)) == 0) {
-      const float o = ror16<r>(score);
-      const int og = ror16<r>(g);
-      rank += o > score || (o == score && og < g);
-    }
-    rank_groups<r + 1>(score, g, lanes, rank);
+    const float o = ror16<r>(score);
+    const int og = ror16<r>(g);
+    return (int)(o > score || (o == score && og < g)) + rank_groups<kL, r + kL>(score, g);
+  } else {
+    return 0;
   }
 }
 // The two largest of two lanes' two.
@@ -254,150 +280,251 @@ __device__ __forceinline__ void merge_best(float& a, float& b) {
   a = fmaxf(a, oa);
 }
 
-// kN experts a lane, lists of kK >= k.
-template <int kN, int kK>
-__global__ __launch_bounds__(64 * kWaves) void route_group_kernel(const GroupRoute p) {
-  using K = Key<true>;
-  __shared__ __attribute__((aligned(16))) float stage[kWaves][kStage];
+// key = the upper 24 bits of x, the lower 8 of id.
+__device__ __forceinline__ uint32_t with_id(uint32_t x, int id) { return (x & ~255u) | ((uint32_t)id & 255u); }
+
+// x as an unsigned number, cut off: 0 for what is below it and for a NaN, the largest for what is above (the instruction's
+// way; the language leaves these open).
+__device__ __forceinline__ uint32_t whole(float x) {
+  uint32_t r;
+  asm("v_cvt_u32_f32 %0, %1" : "=v"(r) : "v"(x));
+  return r;
+}
+
+// kN experts a lane, lists of kK >= k.  Keys are 24 bits of a number in the order of what counts, above 255 - id (so that
+// of equal ones the lower id is the larger key), and a selection is max and min of 32-bit numbers, of which those between
+// lanes read their neighbour as they go:
+//   bf16 logits, no bias   the logit itself
+//   fp32 logits, no bias   the logit's distance from the row's largest in steps of 2^-19, 32 of it
+//   bias                   the score with its bias over the lowest bias, from 0 to the largest it can be
+// The first is exact.  The others' roundings keep the order, so that one step apart is right without a bias, and as far
+// apart as twice the scores' errors with one; what is nearer and not of equal logits and biases is done again.
+// (Keys of the fp32 number in a double's mantissa, the id below it, need no second look at logits but 64-bit max and min
+// and moves of 2 words between lanes: 98 us at 131072 x 256 with a bias and 8 groups, where these take 75.)
+// kInline: the wave does such tokens itself; else it marks them with id -1 for route_again_kernel, whose 64-bit code would
+// take half of this one's waves for its registers (140 us in one kernel, 98 and 19 in two).
+// Measured: 131072 x 256 f32, bias, 4 of 8 groups, k = 8, with counts: 90 us -- 75 here, VALU issue 76 % busy with 980
+// instructions for 4 tokens, 264 of them the networks, 180 the scores; 15 for the 285 tokens done again, 5 for the counts'
+// total -- of 28 that its bytes take.  Without groups and bias 55.
+template <int kN, int kK, bool kInline>
+__global__ __launch_bounds__(64 * kWaves, kInline ? 1 : kN <= 16 ? 4 : 2) void route_group_kernel(const GroupRoute p) {
+  using K = Key<false>;
+  __shared__ __attribute__((aligned(16))) char stage[room(kWaves * kSpan)];
   __shared__ int cnt[kMaxExperts];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, sub = lane & 15, grp = lane >> 4;
   const int E = p.E, k = p.k, n = E / p.G, lanes = p.lanes, g = sub / lanes, q = sub % lanes;
-  float* const sl = stage[wave];
+  const uint32_t place = wave * kSpan + grp * E;        // of the token's first logit
   if (tid < kMaxExperts) cnt[tid] = 0;
   __syncthreads();
   // what the order goes by: scores where a bias or sums of two count, else the logits themselves
-  const bool sums = p.G > 1 && p.best == 2, scored = p.bias || sums;
+  const bool sums = p.G > 1 && p.best == 2, scored = p.bias || sums, exact = !p.bias && !p.f32;
   const bool stats = !p.sigmoid && (scored || !p.renorm);
   const int own = g < p.G ? n : 0;                      // experts of the lane's group
+  const bool full = lanes * kN == n && lanes * p.G == 16;
+  const bool steps = n <= 32 && 32 % n == 0 && E % 32 == 0;   // a group lies between two rooms
+  const int mine_n = (own - q + lanes - 1) / lanes;     // experts of the lane
+  // biases over the lowest one (-inf aside), and how far the largest sum is from 0
+  float lo = 0.f, range = 0.f;
+  if (p.bias) {
+    lo = -kNone;
+    float hi = kNone;
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < kMaxExperts / 64; ++i) {
+      const float x = lane + 64 * i < E ? p.bias[lane + 64 * i] : kNone;
+      lo = x > kNone ? fminf(lo, x) : lo;
+      hi = fmaxf(hi, x);
+      odd |= x != x;
+    }
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) {
+      lo = fminf(lo, __shfl_xor(lo, d, 64));
+      hi = fmaxf(hi, __shfl_xor(hi, d, 64));
+    }
+    range = __any(odd) ? -kNone : hi - lo + 1.f;        // (infinite or NaN: every token is done in 64 bits)
+  }
+  const float t0_err = p.sigmoid ? 0x1p-20f : 0x1p-17f;  // twice the errors of two scores (a softmax's sum has more)
+  const float near = t0_err + 0x1p-22f * range;          // and of two of them with their biases
+  const bool hopeless = p.bias && !(range < 0x1p60f);
   float b[kN];
 #pragma unroll
-  for (int c = 0; c < kN; ++c) b[c] = p.bias && q + lanes * c < own ? p.bias[g * n + q + lanes * c] : 0.f;
-  // errors of two scores and their rounding, twice over (see above; a softmax's sum has more of them)
-  const float t0_err = p.sigmoid ? 0x1p-20f : 0x1p-17f;
+  for (int c = 0; c < kN; ++c) b[c] = p.bias && q + lanes * c < own ? p.bias[g * n + q + lanes * c] - lo : 0.f;
+  constexpr float kTop = 0x1p32f - 0x1p16f;
+  float by = 0x1p27f, plus = 0.f;                        // key = by x + plus
+  uint32_t apart = 0;
+  if (p.bias) {
+    by = kTop / range;
+    plus = 4096.f;
+    apart = whole(near * by * 0x1p-8f) + 2u;
+  }
   for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 < p.T; t0 += (int64_t)gridDim.x * kTokens) {
     const int64_t tw = t0 + 4 * wave, t = tw + grp;
     const int64_t left = p.T - tw;
     const bool in = t < p.T;
     const int have = left >= 4 ? 4 * E : left > 0 ? (int)left * E : 0;
     wave_lds();
-    if (p.f32) stage_logits<true>(p.logits, tw * E, have, lane, sl);
-    else stage_logits<false>(p.logits, tw * E, have, lane, sl);
+    // (E <= 16 kN and 256)
+    constexpr int kU = kN < 4 ? 1 : kN < 16 ? kN / 4 : 4;
+    if (p.f32) stage_logits<true, kU>(p.logits, tw * E, have, lane, stage, wave * kSpan);
+    else stage_logits<false, kU>(p.logits, tw * E, have, lane, stage, wave * kSpan);
     wave_lds();
     // (not known to be the same in every turn: places and ids would all be kept in registers)
-    int q1 = q, e0 = (own ? g * n : 0) + q;
-    asm volatile("" : "+v"(q1), "+v"(e0));
-    float l[kN], v[kN];                                 // (-inf: no expert, which like one of -inf is never selected here)
+    int e0 = (own ? g * n : 0) + q;
+    asm volatile("" : "+v"(e0));
+    float v[kN];                                         // (-inf: no expert, which like one of -inf is never selected here)
+    const uint32_t from = place + e0;
+    if (lanes == 16 && E % 32 == 0) {                    // (places without arithmetic where no group crosses a room)
 #pragma unroll
-    for (int c = 0; c < kN; ++c) l[c] = sl[staged(grp * E + e0 + lanes * c)];
+      for (int c = 0; c < kN; ++c) v[c] = *reinterpret_cast<const float*>(stage + room(from) + c * 64 + c / 2 * 8);
+    } else if (steps) {
+      uint32_t at = room(from);
 #pragma unroll
-    for (int c = 0; c < kN; ++c) {
-      l[c] = q1 + lanes * c < own ? l[c] : kNone;
-      v[c] = l[c];
+      for (int c = 0; c < kN; ++c, at += 4 * lanes) v[c] = *reinterpret_cast<const float*>(stage + at);
+    } else {
+#pragma unroll
+      for (int c = 0; c < kN; ++c) v[c] = at_room(stage, from + lanes * c);
     }
-    float m = 0.f, total = 0.f;                         // of the whole row's exponentials
-    if (stats) {
-      m = l[0];
+    if (!full) {
+      int end = mine_n;
+      asm volatile("" : "+v"(end));                      // (a branch, and 16 comparisons in it, not their results kept)
 #pragma unroll
-      for (int c = 1; c < kN; ++c) m = fmaxf(m, l[c]);
+      for (int c = 0; c < kN; ++c) v[c] = c < end ? v[c] : kNone;
+    }
+    float m = 0.f, total = 0.f;                          // largest logit, and of the row's exponentials
+    if (stats || !(exact || p.bias)) {
+      m = v[0];
+#pragma unroll
+      for (int c = 1; c < kN; ++c) m = fmaxf(m, v[c]);
       m = group_max<16>(m);
+      if (!p.bias) plus = kTop - m * 0x1p27f;
       m = m == kNone ? 0.f : m;
-#pragma unroll
-      for (int c = 0; c < kN; ++c) {
-        v[c] = __expf(l[c] - m);
-        total += v[c];
-      }
-      total = group_sum<16>(total);
     }
-    bool bad = false;
-    if (scored) {
-      const float inv = p.sigmoid ? 0.f : 1.0f / total;
-#pragma unroll
-      for (int c = 0; c < kN; ++c) {
-        const float s = p.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-l[c])) : v[c] * inv;
-        v[c] = l[c] == kNone ? kNone : s + b[c];
-      }
-    } else if (stats) {
-#pragma unroll
-      for (int c = 0; c < kN; ++c) v[c] = l[c];
-    }
-    if (p.G > 1) {
-      float x = kNone, y = kNone;                       // the two largest
+    bool bad = hopeless;
+    if (!p.bias && !exact) bad |= !(fabsf(m) < 4096.f);  // (plus would round by more than its room)
+    if (!exact || p.G > 1) {
       bool nan = false;
 #pragma unroll
+      for (int c = 0; c < kN; ++c) nan |= v[c] != v[c];
+      bad |= nan;
+    }
+    if (stats) {
+#pragma unroll
+      for (int c = 0; c < kN; ++c) total += __expf(v[c] - m);
+      total = group_sum<16>(total);
+    }
+    // scores with their biases (0 without), -inf where the logit is
+    const auto score_all = [&]() {
+      if (p.sigmoid) {
+#pragma unroll
+        for (int c = 0; c < kN; ++c) {
+          const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-v[c])) + b[c];
+          v[c] = v[c] == kNone ? kNone : s;
+        }
+      } else {
+        const float inv = 1.0f / total;
+#pragma unroll
+        for (int c = 0; c < kN; ++c) {
+          const float s = __builtin_fmaf(__expf(v[c] - m), inv, b[c]);
+          v[c] = v[c] == kNone ? kNone : s;
+        }
+      }
+    };
+    uint32_t key[kN];
+    int id = 255 - e0;
+    if (p.bias) {
+      score_all();
+    } else if (exact) {
+#pragma unroll
+      for (int c = 0; c < kN; ++c, id -= lanes) key[c] = with_id(rank_of<0x10000u>(v[c]), id);
+    } else {
+#pragma unroll
+      for (int c = 0; c < kN; ++c, id -= lanes) key[c] = with_id(whole(__builtin_fmaf(v[c], by, plus)), id);
+    }
+    if (p.G > 1) {
+      if (sums && !p.bias) score_all();
+      float x = kNone, y = kNone;                        // the two largest
+#pragma unroll
       for (int c = 0; c < kN; ++c) {
-        y = fmaxf(y, fminf(x, v[c]));
+        y = __builtin_amdgcn_fmed3f(x, y, v[c]);
         x = fmaxf(x, v[c]);
-        nan |= v[c] != v[c];
       }
       if (lanes > 1) merge_best<0>(x, y);
       if (lanes > 2) merge_best<1>(x, y);
       if (lanes > 4) merge_best<2>(x, y);
       const float score = sums ? x + y : x;
-      int rank = 0;
-      rank_groups<1>(score, g, lanes, rank);
+      int rank;
+      if (lanes == 8) rank = rank_groups<8>(score, g);
+      else if (lanes == 4) rank = rank_groups<4>(score, g);
+      else if (lanes == 2) rank = rank_groups<2>(score, g);
+      else rank = rank_groups<1>(score, g);
       const bool kept = own && rank < p.kg;
-      bad = nan;
       if (scored) {
-        const float lo = -group_max<16>(kept ? -score : kNone), hi = group_max<16>(kept ? kNone : score);
-        const float most = group_max<16>(score > kNone ? fabsf(x) + (sums ? fabsf(y) : 0.f) : 0.f);
-        bad |= !(lo - hi > 2.f * t0_err + 0x1p-21f * most);
+        const float least = -group_max<16>(kept ? -score : kNone), most = group_max<16>(kept ? kNone : score);
+        bad |= !(least - most > 2.f * t0_err + 0x1p-21f * (range + 2.f));
       }
+      if (p.bias) {
 #pragma unroll
-      for (int c = 0; c < kN; ++c) v[c] = kept ? p.bias ? v[c] : l[c] : kNone;
+        for (int c = 0; c < kN; ++c) v[c] = kept ? v[c] : kNone;
+      } else {
+#pragma unroll
+        for (int c = 0; c < kN; ++c) key[c] = kept ? key[c] : 0u;
+      }
+    }
+    if (p.bias) {
+#pragma unroll
+      for (int c = 0; c < kN; ++c, id -= lanes) key[c] = with_id(whole(__builtin_fmaf(v[c], by, plus)), id);
     }
     constexpr int kA = kN > kK ? kN : kK;
-    typename K::type a[kA];
+    uint32_t a[kA];
 #pragma unroll
-    for (int c = 0; c < kN; ++c) a[c] = K::make(v[c], e0 + lanes * c);
+    for (int c = 0; c < kN; ++c) a[c] = key[c];
     sort_top<K, kN, kK>(a);
     constexpr int kM = kN < kK ? kN : kK;
     merge_lanes<K, 16, kM, kK, 0>(a);
     // the lane's slot, and the last one
-    typename K::type mine = a[0], end = a[0];
 #pragma unroll
-    for (int j = 1; j < kK; ++j) {
-      mine = sub == j ? a[j] : mine;
-      end = k - 1 == j ? a[j] : end;
+    for (int h = 1; h < kK; h *= 2) {
+      const uint32_t upper = sub & h ? ~0u : 0u;         // (masks: a choice of an array's elements becomes a search in it)
+#pragma unroll
+      for (int j = 0; j < kK; j += 2 * h) a[j] = (a[j] & ~upper) | (a[j + h] & upper);
     }
-    const float least = K::value(end), value = K::value(mine);
-    bad |= !(least > kNone) && least == least;          // fewer experts than k: the others go by their ids
+    const uint32_t mine = a[0], end = (uint32_t)__shfl((int)mine, (lane & 48) + k - 1, 64);
+    bad |= end < 256u;                                   // fewer experts than k, or below the keys' range: by their ids
     const bool slot = sub < k;
-    const int e = slot ? K::expert(mine) : 0;
-    const float le = slot ? sl[staged(grp * E + (e < E ? e : 0))] : kNone;
-    if (p.bias) {
-      const float near = t0_err + 0x1p-22f * fabsf(value), above = before(value);
-      bool odd = slot && sub > 0 && !(above - value > near);
-      odd |= slot && !(fabsf(value) < __builtin_huge_valf());
+    const int e = slot ? 255 - (int)(mine & 255u) : 0;
+    const float le = slot ? at_room(stage, place + (e < E ? e : 0)) : kNone;
+    if (!exact) {
+      const uint32_t above = (uint32_t)__builtin_amdgcn_mov_dpp((int)mine, 0x111, 0xF, 0xF, true) >> 8;
+      const uint32_t at = mine >> 8, last = end >> 8;
+      const bool close = slot && sub > 0 && !(above - at > apart);
       // every expert that reaches the last one's neighbourhood is in the list
-      const float floor = least - (t0_err + 0x1p-22f * fabsf(least));
+      const uint32_t floor = (last > apart ? last - apart : 0u) << 8;
       int reach = 0;
 #pragma unroll
-      for (int c = 0; c < kN; ++c) reach += v[c] >= floor;
+      for (int c = 0; c < kN; ++c) reach += key[c] >= floor;
       reach += dpp_pair<0>(reach);
       reach += dpp_pair<1>(reach);
       reach += dpp_pair<2>(reach);
       reach += dpp_pair<3>(reach);
-      odd |= reach != k;
-      if (__any(odd)) {
+      if (__any(close || reach != k)) {
         // equal logits with equal biases are equal in any arithmetic, and in the right order already: they pass
-        const float be = slot ? p.bias[e < E ? e : 0] : 0.f;
-        odd = slot && !(fabsf(value) < __builtin_huge_valf());
+        const float be = slot && p.bias ? p.bias[e < E ? e : 0] - lo : 0.f;
         const float lp = before(le), bp = before(be);
-        odd |= slot && sub > 0 && !(above - value > near) && !(le == lp && be == bp);
-        const int last = (lane & 48) + k - 1;
-        const float ll = __shfl(le, last, 64), bl = __shfl(be, last, 64);
+        bool odd = close && !(le == lp && be == bp);
+        const int end_lane = (lane & 48) + k - 1;
+        const float ll = __shfl(le, end_lane, 64), bl = __shfl(be, end_lane, 64);
         int others = slot && !(le == ll && be == bl) ? -1 : 0;
 #pragma unroll
-        for (int c = 0; c < kN; ++c) others += v[c] >= floor && !(sl[staged(grp * E + e0 + lanes * c)] == ll && b[c] == bl);
+        for (int c = 0; c < kN; ++c)
+          others += key[c] >= floor && !(at_room(stage, place + e0 + lanes * c) == ll && b[c] == bl);
         others += dpp_pair<0>(others);
         others += dpp_pair<1>(others);
         others += dpp_pair<2>(others);
         others += dpp_pair<3>(others);
-        odd |= others != 0;
+        bad |= odd || others != 0;
       }
-      bad |= odd;
     }
-    // weights: of sigmoids as multiples of e^m, which the quotient drops, so that tiny ones keep their ratios
+    // weights: of sigmoids as multiples of e^top, which the quotient drops, so that tiny ones keep their ratios
     float w = 0.f;
     if (p.sigmoid) {
       const float top = p.renorm ? fminf(group_max<16>(le), 0.f) : 0.f;
@@ -414,35 +541,57 @@ __global__ __launch_bounds__(64 * kWaves) void route_group_kernel(const GroupRou
       p.prob[t * k + sub] = w * p.scale;
       if (p.counts && (!p.mask || p.mask[t] != 0)) atomicAdd(&cnt[e], 1);
     }
-    if (again) {
-      wave_lds();                                       // the stage is free: it holds the 64-bit scores now
+    if constexpr (!kInline) {
+      if (in && !done && sub == 0) p.idx[t * k] = -1;
+    } else if (again) {
+      wave_lds();                                        // the stage is free: it holds the 64-bit scores now
 #pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        if ((again >> (16 * i) & 0xFFFFu) == 0) continue;
-        const int64_t ti = tw + i;
-        double* cs = reinterpret_cast<double*>(sl);
-        const Slot s = p.f32 ? route_token<true>(p, ti, lane, cs) : route_token<false>(p, ti, lane, cs);
-        if (lane < k) {
-          p.idx[ti * k + lane] = s.e;
-          p.prob[ti * k + lane] = s.w;
-          if (p.counts && (!p.mask || p.mask[ti] != 0)) atomicAdd(&cnt[s.e], 1);
-        }
-      }
+      for (int i = 0; i < 4; ++i)
+        if (again >> (16 * i) & 0xFFFFu) token_again(p, tw + i, lane, reinterpret_cast<double*>(stage + room(wave * kSpan)), cnt);
     }
   }
   if (p.counts) {
     __syncthreads();
-    int32_t* to = gridDim.x == 1 ? p.counts : p.part + (int64_t)blockIdx.x * E;
+    int32_t* to = kInline && gridDim.x == 1 ? p.counts : p.part + (int64_t)blockIdx.x * E;
     if (tid < E) to[tid] = cnt[tid];
   }
 }
 
-template <int kN>
+// The tokens that route_group_kernel has marked, in 64 bits: a workgroup looks through 256 and deals the marked ones to
+// its waves.  Its counts follow the first kernel's.
+__global__ __launch_bounds__(64 * kWaves) void route_again_kernel(const GroupRoute p, int32_t* part) {
+  __shared__ double cs[kWaves][kMaxExperts];
+  __shared__ int cnt[kMaxExperts], list[64 * kWaves], marked;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (tid < kMaxExperts) cnt[tid] = 0;
+  for (int64_t t0 = (int64_t)blockIdx.x * 64 * kWaves; t0 < p.T; t0 += (int64_t)gridDim.x * 64 * kWaves) {
+    if (tid == 0) marked = 0;
+    __syncthreads();
+    const int64_t t = t0 + tid;
+    if (t < p.T && p.idx[t * p.k] < 0) list[atomicAdd(&marked, 1)] = tid;
+    __syncthreads();
+    for (int i = wave; i < marked; i += kWaves) token_again(p, t0 + list[i], lane, cs[wave], cnt);
+    __syncthreads();
+  }
+  if (p.counts && tid < p.E) part[(int64_t)blockIdx.x * p.E + tid] = cnt[tid];
+}
+
+template <int kN, bool kInline>
 void launch_k(const GroupRoute& p, int nb, hipStream_t st) {
-  if (p.k <= 2) route_group_kernel<kN, 2><<<nb, 64 * kWaves, 0, st>>>(p);
-  else if (p.k <= 4) route_group_kernel<kN, 4><<<nb, 64 * kWaves, 0, st>>>(p);
-  else if (p.k <= 8) route_group_kernel<kN, 8><<<nb, 64 * kWaves, 0, st>>>(p);
-  else route_group_kernel<kN, 16><<<nb, 64 * kWaves, 0, st>>>(p);
+  if (p.k <= 2) route_group_kernel<kN, 2, kInline><<<nb, 64 * kWaves, 0, st>>>(p);
+  else if (p.k <= 4) route_group_kernel<kN, 4, kInline><<<nb, 64 * kWaves, 0, st>>>(p);
+  else if (p.k <= 8) route_group_kernel<kN, 8, kInline><<<nb, 64 * kWaves, 0, st>>>(p);
+  else route_group_kernel<kN, 16, kInline><<<nb, 64 * kWaves, 0, st>>>(p);
+}
+template <bool kInline>
+void launch_n(const GroupRoute& p, int nb, hipStream_t st) {
+  const int per = (p.E / p.G + p.lanes - 1) / p.lanes;   // experts a lane
+  if (per <= 1) launch_k<1, kInline>(p, nb, st);
+  else if (per <= 2) launch_k<2, kInline>(p, nb, st);
+  else if (per <= 4) launch_k<4, kInline>(p, nb, st);
+  else if (per <= 8) launch_k<8, kInline>(p, nb, st);
+  else if (per <= 16) launch_k<16, kInline>(p, nb, st);
+  else launch_k<32, kInline>(p, nb, st);
 }
 
 // counts[e] = sum over the nb blocks; a workgroup takes 16 experts, 64 slices of the blocks.
@@ -547,7 +696,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_group_bwd_kernel(const Grou
           if (t < p.T && sub + 16 * c < E) v[c] = logit<kF32>(p.logits, t * E + sub + 16 * c);
         }
       } else {
-        stage_logits<kF32, false>(p.logits, tw * E, have, lane, row);
+        stage_logits<kF32, kN / 4 < 1 ? 1 : kN / 4, false>(p.logits, tw * E, have, lane, reinterpret_cast<char*>(row), 0u);
         wave_lds();
 #pragma unroll
         for (int c = 0; c < kN; ++c) v[c] = mine[sub + 16 * c < E ? sub + 16 * c : 0];
@@ -607,25 +756,30 @@ void launch_bwd(const GroupRouteBwd& p, hipStream_t st) {
 
 }  // namespace
 
-int route_group_blocks(int64_t T) {
-  const int64_t nb = (T + kTokens - 1) / kTokens;
-  return (int)(nb < kGroupMaxBlocks ? nb : kGroupMaxBlocks);
-}
+namespace {
+// Tokens up to which a workgroup a CU takes them, marked ones and all, in one launch.
+constexpr int64_t kInlineTokens = 256 * kTokens;
+int most(int64_t n, int m) { return (int)(n < m ? n : m); }
+int group_blocks(int64_t T) { return most((T + kTokens - 1) / kTokens, kGroupMaxBlocks); }
+int again_blocks(int64_t T) { return T <= kInlineTokens ? 0 : most((T + 64 * kWaves - 1) / (64 * kWaves), kGroupMaxBlocks); }
+}  // namespace
+
+int route_group_parts(int64_t T) { return group_blocks(T) + again_blocks(T); }
 
 hipError_t launch_route_group(GroupRoute p, bool f32, hipStream_t st) {
-  const int nb = route_group_blocks(p.T);
+  const int nb = group_blocks(p.T), more = again_blocks(p.T);
   int wide = 1;
   while (wide < p.G) wide *= 2;
   p.f32 = f32;
   p.lanes = 16 / wide;
-  const int per = (p.E / p.G + p.lanes - 1) / p.lanes;  // experts a lane
-  if (per <= 1) launch_k<1>(p, nb, st);
-  else if (per <= 2) launch_k<2>(p, nb, st);
-  else if (per <= 4) launch_k<4>(p, nb, st);
-  else if (per <= 8) launch_k<8>(p, nb, st);
-  else if (per <= 16) launch_k<16>(p, nb, st);
-  else launch_k<32>(p, nb, st);
-  if (p.counts && nb > 1) route_counts_kernel<<<(p.E + 15) / 16, kCountThreads, 0, st>>>(p.part, nb, p.E, p.counts);
+  if (more) {
+    launch_n<false>(p, nb, st);
+    route_again_kernel<<<more, 64 * kWaves, 0, st>>>(p, p.part + (int64_t)nb * p.E);
+  } else {
+    launch_n<true>(p, nb, st);
+  }
+  if (p.counts && nb + more > 1)
+    route_counts_kernel<<<(p.E + 15) / 16, kCountThreads, 0, st>>>(p.part, nb + more, p.E, p.counts);
   return hipGetLastError();
 }
 
