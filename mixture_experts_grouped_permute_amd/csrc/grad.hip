@@ -129,19 +129,19 @@ __global__ __launch_bounds__(kThreads) void grad_sumsq_finish_kernel(const doubl
   if (threadIdx.x == 0) *sumsq = acc;
 }
 
-template <bool kOnce>
-__global__ __launch_bounds__(kThreads) void grad_clip_kernel(const Table<kClipTable, true> tab,
-                                                             const double* __restrict__ sumsq, int parts, float max_norm,
-                                                             float* __restrict__ norm) {
+// kTensors, kOut: the table's; without outputs of their own the gradients are scaled in place.
+template <bool kOnce, int kTensors, bool kOut>
+__global__ __launch_bounds__(kThreads) void grad_clip_kernel(const Table<kTensors, kOut> tab, const double* __restrict__ sumsq,
+                                                             int parts, float max_norm, float* __restrict__ norm) {
   const double total = sqrt(parts == 1 ? *sumsq : sum_parts(sumsq, parts));
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)total;
   const double ratio = (double)max_norm / (total + 1e-6);
   const float by = ratio >= 1.0 || max_norm == __builtin_huge_valf() ? 1.0f : (float)ratio;   // (a NaN stays)
-  const Finder<kClipTable, true> finder(tab);
+  const Finder<kTensors, kOut> finder(tab);
   const int chunks = tab.first[tab.tensors];
   for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
     const Chunk k = finder.find(tab, c);
-    const uint64_t g = tab.g[k.e], o = tab.out[k.e];
+    const uint64_t g = tab.g[k.e], o = kOut ? tab.out[kOut ? k.e : 0] : g;
     if (by == 1.0f && g == o) continue;                 // in place, and nothing to change
     const void* base = reinterpret_cast<const void*>(g & ~kF32Bit);
     void* to = reinterpret_cast<void*>(o & ~kF32Bit);
@@ -229,6 +229,23 @@ int64_t launch_parts(const GradList& l, double* part, hipStream_t st) {
   }
   return parts;
 }
+
+template <int kTensors, bool kOut>
+void launch_scaled(const GradList& l, const double* sumsq, int parts, float max_norm, float* norm, hipStream_t st) {
+  Table<kTensors, kOut> tab;
+  const bool once = past_caches(l);
+  int at = 0;
+  bool first = true;
+  while (true) {
+    const int chunks = next_table(l, &at, &tab);
+    if (!chunks && !first) break;                       // (with nothing but empty tensors: the norm alone)
+    const int nb = chunks < kClipBlocks ? chunks : kClipBlocks, grid = nb > 0 ? nb : 1;
+    float* to = first ? norm : nullptr;
+    if (once) grad_clip_kernel<true, kTensors, kOut><<<grid, kThreads, 0, st>>>(tab, sumsq, parts, max_norm, to);
+    else grad_clip_kernel<false, kTensors, kOut><<<grid, kThreads, 0, st>>>(tab, sumsq, parts, max_norm, to);
+    first = false;
+  }
+}
 }  // namespace
 
 hipError_t launch_grad_sumsq(const GradList& l, double* part, double* sumsq, hipStream_t st) {
@@ -251,19 +268,11 @@ hipError_t launch_grad_clip(const GradList& l, const double* sumsq, double* part
       parts = 1;
     }
   }
-  Table<kClipTable, true> tab;
-  const bool once = past_caches(l);
-  int at = 0;
-  bool first = true;
-  while (true) {
-    const int chunks = next_table(l, &at, &tab);
-    if (!chunks && !first) break;                       // (with nothing but empty tensors: the norm alone)
-    const int nb = chunks < kClipBlocks ? chunks : kClipBlocks, grid = nb > 0 ? nb : 1;
-    float* to = first ? norm : nullptr;
-    if (once) grad_clip_kernel<true><<<grid, kThreads, 0, st>>>(tab, sumsq, (int)parts, max_norm, to);
-    else grad_clip_kernel<false><<<grid, kThreads, 0, st>>>(tab, sumsq, (int)parts, max_norm, to);
-    first = false;
-  }
+  bool in_place = true;
+  for (int i = 0; i < l.n; ++i) in_place &= l.numel[i] == 0 || (l.g[i] == l.out[i] && l.dtype[i] == l.out_dtype[i]);
+  // (256 tensors a launch in place, 176 with outputs of their own)
+  if (in_place) launch_scaled<kSumTable, false>(l, sumsq, (int)parts, max_norm, norm, st);
+  else launch_scaled<kClipTable, true>(l, sumsq, (int)parts, max_norm, norm, st);
   return hipGetLastError();
 }
 

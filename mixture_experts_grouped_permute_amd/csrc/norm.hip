@@ -90,11 +90,11 @@ __device__ __forceinline__ Piece piece(int c, int sub, int H) {
 // in LDS into runs: 126 us at 16384 x 4096 bf16 with 16 rows, 117 with 4, 109 so).
 // kOnce: the sum and y are stored past the caches.
 template <bool kF32, bool kW32, int kL, int kN, bool kAligned, bool kOnce>
-__global__ __launch_bounds__(threads_of(kL)) void add_rmsnorm_kernel(const NormFwd p) {
+__global__ __launch_bounds__(threads_of(kL)) void add_rmsnorm_kernel(const NormFwd p, int64_t t0) {
   using Sum = RowSum<kL, 1>;
   __shared__ float red[Sum::kWords];
   const int tid = threadIdx.x, sub = tid % kL, H = (int)p.H;
-  const int64_t t = (int64_t)blockIdx.x * Sum::kRows + tid / kL;
+  const int64_t t = t0 + (int64_t)blockIdx.x * Sum::kRows + tid / kL;
   Piece q[kN];
   bool in[kN];
   Eight<kF32, kAligned> x[kN], r[kN];
@@ -166,7 +166,8 @@ __global__ __launch_bounds__(threads_of(kL)) void add_rmsnorm_kernel(const NormF
 // till its end; the next rows' loads are in flight behind the sums of a row.  (kLate: where 1024 lanes hold 16 columns
 // each or more, or 512 hold 32 in fp32, that would take more registers than there are -- 460 us at 2000 x 32768 bf16 --
 // so the weight and ds are read when they are needed, and the next row when this one is done.)
-template <bool kF32, bool kW32, int kL, int kN, bool kAligned>
+// kOnce: dx is stored past the caches.
+template <bool kF32, bool kW32, int kL, int kN, bool kAligned, bool kOnce>
 __global__ __launch_bounds__(threads_of(kL)) void rmsnorm_bwd_kernel(const NormBwd p) {
   using Sum = RowSum<kL, 2>;
   constexpr int kRows = Sum::kRows;
@@ -272,7 +273,7 @@ __global__ __launch_bounds__(threads_of(kL)) void rmsnorm_bwd_kernel(const NormB
       if (in) {
         Eight<kF32, kAligned> e;
         e.set(o);
-        e.store(p.dx, t * H + q[c].col);
+        e.template store<kOnce>(p.dx, t * H + q[c].col);
       }
     }
     if constexpr (kLate) fetch(t + step);
@@ -430,7 +431,7 @@ Shape shape_few(int64_t H) {
   return {1024, 4};
 }
 constexpr int64_t kFewRows = 512;
-constexpr int64_t kOnceBytes = (int64_t)384 << 20;
+constexpr int64_t kOnceBytes = (int64_t)384 << 20, kOnceBytesBwd = (int64_t)576 << 20;
 
 template <class F>
 hipError_t with_shape(Shape s, F&& f) {
@@ -455,17 +456,23 @@ hipError_t launch_fwd(const NormFwd& p, hipStream_t st) {
   const Shape s = few ? shape_few(p.H) : shape_of(p.H);
   const bool aligned = p.H % 8 == 0 && at16(p.x) && at16(p.residual) && at16(p.weight) && at16(p.sum) && at16(p.y);
   const int rows = threads_of(s.L) / s.L;
-  const unsigned grid = (unsigned)((p.T + rows - 1) / rows);
   // Past the caches where the call moves more than the last of them (256 MB) holds: 16384 x 4096 bf16 with residual,
   // y and codes 96 us instead of 109, and with two products that read y and the codes behind it 186 instead of 199;
-  // 8192 x 4096, which the cache still holds, 112 with them against 115.
+  // 8192 x 4096, which the cache still holds, 112 with them against 115; 16384 x 4095 107 instead of 117, 8192 x 4095 55
+  // against 51.
   const int64_t moved = p.T * p.H * (kF32 ? 4 : 2) * (1 + (p.y != nullptr) + 2 * (p.residual != nullptr));
   const bool once = moved > kOnceBytes;
   return with_shape(s, [&](auto l, auto n) {
-    constexpr int kL = decltype(l)::value, kN = decltype(n)::value;
-    if (aligned && once) add_rmsnorm_kernel<kF32, kW32, kL, kN, true, true><<<grid, threads_of(kL), 0, st>>>(p);
-    else if (aligned) add_rmsnorm_kernel<kF32, kW32, kL, kN, true, false><<<grid, threads_of(kL), 0, st>>>(p);
-    else add_rmsnorm_kernel<kF32, kW32, kL, kN, false, false><<<grid, threads_of(kL), 0, st>>>(p);
+    constexpr int kL = decltype(l)::value, kN = decltype(n)::value, kT = threads_of(kL);
+    constexpr int64_t kMost = ((int64_t)1 << 31) / kT;   // workgroups of a launch (which takes fewer than 2^32 threads)
+    for (int64_t t0 = 0; t0 < p.T; t0 += kMost * rows) {
+      const int64_t need = (p.T - t0 + rows - 1) / rows;
+      const unsigned grid = (unsigned)(need < kMost ? need : kMost);
+      if (aligned && once) add_rmsnorm_kernel<kF32, kW32, kL, kN, true, true><<<grid, kT, 0, st>>>(p, t0);
+      else if (aligned) add_rmsnorm_kernel<kF32, kW32, kL, kN, true, false><<<grid, kT, 0, st>>>(p, t0);
+      else if (once) add_rmsnorm_kernel<kF32, kW32, kL, kN, false, true><<<grid, kT, 0, st>>>(p, t0);
+      else add_rmsnorm_kernel<kF32, kW32, kL, kN, false, false><<<grid, kT, 0, st>>>(p, t0);
+    }
     return hipGetLastError();
   });
 }
@@ -496,11 +503,16 @@ hipError_t launch_bwd(NormBwd p, hipStream_t st) {
     narrow_rmsnorm_bwd_kernel<kF32, kW32><<<b.blocks, 256, 0, st>>>(p);
     e = hipGetLastError();
   } else {
+    // past the caches from more on than forward, whose outputs are most of what it moves: 32768 x 4096 bf16 173 us instead
+    // of 185, 100000 x 1003 149 instead of 163, 16384 x 4096 alike, 20011 x 1407 f32 (338 MB) 77 instead of 75
+    const bool once = p.T * p.H * (kF32 ? 4 : 2) * (p.dsum ? 4 : 3) > kOnceBytesBwd;
     const bool aligned = p.H % 8 == 0 && at16(p.dy) && at16(p.s) && at16(p.dsum) && at16(p.weight) && at16(p.dx);
     e = with_shape(b.s, [&](auto l, auto n) {
       constexpr int kL = decltype(l)::value, kN = decltype(n)::value;
-      if (aligned) rmsnorm_bwd_kernel<kF32, kW32, kL, kN, true><<<b.blocks, threads_of(kL), 0, st>>>(p);
-      else rmsnorm_bwd_kernel<kF32, kW32, kL, kN, false><<<b.blocks, threads_of(kL), 0, st>>>(p);
+      if (aligned && once) rmsnorm_bwd_kernel<kF32, kW32, kL, kN, true, true><<<b.blocks, threads_of(kL), 0, st>>>(p);
+      else if (aligned) rmsnorm_bwd_kernel<kF32, kW32, kL, kN, true, false><<<b.blocks, threads_of(kL), 0, st>>>(p);
+      else if (once) rmsnorm_bwd_kernel<kF32, kW32, kL, kN, false, true><<<b.blocks, threads_of(kL), 0, st>>>(p);
+      else rmsnorm_bwd_kernel<kF32, kW32, kL, kN, false, false><<<b.blocks, threads_of(kL), 0, st>>>(p);
       return hipGetLastError();
     });
   }

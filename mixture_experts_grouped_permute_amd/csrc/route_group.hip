@@ -13,9 +13,9 @@
 //   not:           dl[idx_j] = S_j w_j g_j, and for softmax scores also -p_e sum_m w_m g_m at every expert.
 //
 // Forward: 16 lanes share a token; a group's experts lie with 16 / (power of two >= G) of them.  Scores are fp32
-// first: their error is known (2^-21 and a rounding of c), and where two numbers whose order counts are nearer than
-// that -- neighbours in the list, the last one in and the first one out, the last group in and the first one out -- the
-// wave does that token again in 64 bits (one of some thousand with fp32 logits).
+// first: their error is known, and where two numbers whose order counts are nearer than that -- neighbours in the list,
+// the last one in and the first one out, the last group in and the first one out -- the token is done again in 64 bits
+// (one of 460 with fp32 logits, a bias and 8 groups of 256 experts).
 #include "common.h"
 #include "kernels.h"
 #include "eight.h"
@@ -341,11 +341,15 @@ __global__ __launch_bounds__(64 * kWaves, kInline ? 1 : kN <= 16 ? 4 : 2) void r
       lo = fminf(lo, __shfl_xor(lo, d, 64));
       hi = fmaxf(hi, __shfl_xor(hi, d, 64));
     }
-    range = __any(odd) ? -kNone : hi - lo + 1.f;        // (infinite or NaN: every token is done in 64 bits)
+    // (infinite, NaN or so large that 64 bits round the scores away: every token is done in 64 bits)
+    range = __any(odd) || fmaxf(fabsf(lo), fabsf(hi)) > 0x1p20f ? -kNone : hi - lo + 1.f;
   }
-  const float t0_err = p.sigmoid ? 0x1p-20f : 0x1p-17f;  // twice the errors of two scores (a softmax's sum has more)
-  const float near = t0_err + 0x1p-22f * range;          // and of two of them with their biases
-  const bool hopeless = p.bias && !(range < 0x1p60f);
+  // Errors, u = 2^-24: of a sigmoid 4 u (exponential and reciprocal an ulp each, its argument's rounding), of a softmax 24 u;
+  // with the bias over the lowest, two roundings of up to `range` more.  So two scores differ by what they seem to within
+  // 2 (4 + 1 + 2 range) u, two sums of two within 2 (10 + 6 range) u: at least as much is allowed for.
+  const float t0_err = p.sigmoid ? 0x1p-20f : 0x1p-17f;
+  const float near = t0_err + 0x1p-21f * range;
+  const bool hopeless = p.bias && !(range < 0x1p60f);    // (64-bit roundings of what is below: 2^-33 at most, within the errors)
   float b[kN];
 #pragma unroll
   for (int c = 0; c < kN; ++c) b[c] = p.bias && q + lanes * c < own ? p.bias[g * n + q + lanes * c] - lo : 0.f;
@@ -460,7 +464,7 @@ __global__ __launch_bounds__(64 * kWaves, kInline ? 1 : kN <= 16 ? 4 : 2) void r
       const bool kept = own && rank < p.kg;
       if (scored) {
         const float least = -group_max<16>(kept ? -score : kNone), most = group_max<16>(kept ? kNone : score);
-        bad |= !(least - most > 2.f * t0_err + 0x1p-21f * (range + 2.f));
+        bad |= !(least - most > 2.f * t0_err + 0x1p-20f * (range + 2.f));
       }
       if (p.bias) {
 #pragma unroll
@@ -508,15 +512,18 @@ __global__ __launch_bounds__(64 * kWaves, kInline ? 1 : kN <= 16 ? 4 : 2) void r
       reach += dpp_pair<3>(reach);
       if (__any(close || reach != k)) {
         // equal logits with equal biases are equal in any arithmetic, and in the right order already: they pass
-        const float be = slot && p.bias ? p.bias[e < E ? e : 0] - lo : 0.f;
+        // (the biases themselves: over the lowest one two may round to the same)
+        const float be = slot && p.bias ? p.bias[e < E ? e : 0] : 0.f;
         const float lp = before(le), bp = before(be);
         bool odd = close && !(le == lp && be == bp);
         const int end_lane = (lane & 48) + k - 1;
         const float ll = __shfl(le, end_lane, 64), bl = __shfl(be, end_lane, 64);
         int others = slot && !(le == ll && be == bl) ? -1 : 0;
 #pragma unroll
-        for (int c = 0; c < kN; ++c)
-          others += key[c] >= floor && !(at_room(stage, place + e0 + lanes * c) == ll && b[c] == bl);
+        for (int c = 0; c < kN; ++c) {
+          const int ec = e0 + lanes * c;
+          if (key[c] >= floor) others += !(at_room(stage, place + ec) == ll && (!p.bias || p.bias[ec < E ? ec : 0] == bl));
+        }
         others += dpp_pair<0>(others);
         others += dpp_pair<1>(others);
         others += dpp_pair<2>(others);
@@ -637,9 +644,8 @@ __device__ __forceinline__ void store_rows(void* to, int64_t at, int n, int lane
       u32x4 w;
 #pragma unroll
       for (int j = 0; j < 4; ++j) w[j] = kF32 ? __builtin_bit_cast(uint32_t, v[j]) : pack_bf16x2(v[2 * j], v[2 * j + 1]);
-      // (bf16 past the caches: 131072 x 256 of softmax weights as they are, 70 us through them, 46 past; fp32: 34, 39)
-      if constexpr (kF32) *global<u32x4_any>(b) = w;
-      else __builtin_nontemporal_store(w, global<u32x4_any>(b));
+      // (past the caches: 131072 x 256 f32 39 us, 46 through them, bf16 of softmax weights as they are 27, 42; alike below 30 MB)
+      __builtin_nontemporal_store(w, global<u32x4_any>(b));
     } else {
 #pragma unroll
       for (int j = 0; j < kV; ++j)
@@ -688,7 +694,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_group_bwd_kernel(const Grou
     float* const mine = row + grp * E;
     if constexpr (kN > 0) {
       float v[kN > 0 ? kN : 1], m = kNone, s = 0.f;
-      // (bf16 through LDS: 131072 x 256 71 us with 2-byte loads of 16 lanes, 42 so; fp32 46, 52)
+      // (bf16 through LDS: 131072 x 256 71 us with 2-byte loads of 16 lanes, 42 so, both stored through the caches; fp32 46, 52)
       if constexpr (kF32) {
 #pragma unroll
         for (int c = 0; c < kN; ++c) {

@@ -115,6 +115,43 @@ def test_sum_in_place_and_gradient_in_place(dtype):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [B, F], ids=["bf16", "f32"])
+def test_gradient_over_the_residuals_own(dtype):
+    """dx written over dsum, as the C entry point allows."""
+    m = need_gpu()
+    from mixture_experts_grouped_permute_amd import _lib as L
+    lib = m.load()
+    for T, H in ((1, 4096), (3, 5), (600, 255), (40, 2048), (9, 30001), (700, 8192)):
+        dy, s, ds = (_x(T, H, dtype, i).cuda() for i in range(3))
+        w = _w(H, dtype).cuda()
+        want, wdw = m.moe_add_rmsnorm_bwd(dy, s, w, ds=ds)
+        dx, dw = ds.clone(), torch.empty(H, device="cuda")
+        ws = torch.empty(lib.moe_add_rmsnorm_bwd_workspace(T, H), dtype=torch.uint8, device="cuda")
+        io = L._io(dy)
+        st = lib.moe_add_rmsnorm_bwd(dy.data_ptr(), s.data_ptr(), dx.data_ptr(), io, w.data_ptr(), io, T, H, 1e-6,
+                                     dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), ws.numel(), L._stream(dy.device))
+        torch.cuda.synchronize()
+        assert st == 0 and torch.equal(dx, want) and torch.equal(dw, wdw)
+
+
+@gpu
+def test_more_rows_than_a_launch_takes():
+    m = need_gpu()
+    T, H = (1 << 27) + 3, 8
+    x = torch.ones((T, H), dtype=B, device="cuda")
+    x[0], x[-1], x[-4] = _x(1, H, B, 0).cuda(), _x(1, H, B, 1).cuda(), _x(1, H, B, 2).cuda()
+    w = _w(H, B).cuda()
+    y, _, _, _ = m.moe_add_rmsnorm(x, w)
+    dx, dw = m.moe_add_rmsnorm_bwd(x, x, w)
+    torch.cuda.synchronize()
+    at = torch.tensor([0, 1, T // 2, T - 4, T - 3, T - 2, T - 1], device="cuda")
+    want = norm.forward(x[at].cpu(), w.cpu(), 1e-6)
+    assert (np.abs(_np(y[at]) - want) <= (80 * U + _half(B)) * np.abs(want)).all()
+    rx, _, mag, _ = norm.backward(x[at].cpu(), x[at].cpu(), w.cpu(), 1e-6)
+    assert (np.abs(_np(dx[at]) - rx) <= 240 * U * mag + _half(B) * np.abs(rx) + 1e-38).all()
+
+
+@gpu
 def test_zero_rows_infinities_and_nan():
     m = need_gpu()
     for dtype in (B, F):

@@ -155,8 +155,8 @@ def test_nan_infinity_and_large_biases(dtype, E, k, G, kg, best):
     lg[5, E - 2] = nan
     lg[6] = nan
     for score in ("sigmoid", "softmax"):
-        for b in (None, torch.zeros(E), torch.linspace(-300, 300, E)):
-            if b is not None and E > 30:
+        for b in (None, torch.zeros(E), torch.linspace(-300, 300, E), torch.full((E,), -inf), torch.full((E,), 1e30)):
+            if b is not None and E > 30 and abs(float(b[0])) < 1e3:
                 b[5], b[9], b[11] = inf, -inf, nan
             kw = dict(score=score, groups=G, topk_groups=kg, group_best=best)
             idx, prob, _ = m.moe_route_grouped(lg.cuda(), k, bias=_gpu(b), **kw)
@@ -164,6 +164,44 @@ def test_nan_infinity_and_large_biases(dtype, E, k, G, kg, best):
             ri, rp, _ = group_route.forward(lg, k, b, **kw)
             np.testing.assert_array_equal(idx.cpu().numpy(), ri)
             _close(prob.cpu().double().numpy(), rp, 80 * U * rp + TINY)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [F, B], ids=["f32", "bf16"])
+def test_equal_scores_go_by_their_ids(dtype):
+    """Whole rows of equal logits, and biases that repeat, as routers begin: through the fp32 order and the 64-bit one."""
+    m = need_gpu()
+    g = np.random.default_rng(9)
+    for T, E, k, G, kg, best in ((50, 64, 8, 8, 3, 2), (5000, 64, 6, 1, 1, 1), (4500, 256, 8, 8, 4, 2), (4200, 48, 4, 3, 2, 1)):
+        lg = np.zeros((T, E))
+        lg[1::3] = np.round(g.standard_normal((len(lg[1::3]), E)) * 2) / 2
+        lg[2::3] = g.standard_normal((len(lg[2::3]), E)) * 1.5
+        b = torch.from_numpy(np.round(g.standard_normal(E) * 3).astype(np.float32) * np.float32(0.001))
+        t = torch.from_numpy(lg.astype(np.float32)).to(dtype)
+        for bias in (None, b, torch.zeros(E)):
+            for score in ("sigmoid", "softmax"):
+                kw = dict(score=score, groups=G, topk_groups=kg, group_best=best)
+                idx, prob, counts = m.moe_route_grouped(t.cuda(), k, bias=_gpu(bias), count=True, **kw)
+                torch.cuda.synchronize()
+                rows = np.r_[0:60, T - 60:T] if T > 120 else np.arange(T)
+                ri, rp, _ = group_route.forward(t[rows], k, bias, **kw)
+                np.testing.assert_array_equal(idx.cpu().numpy()[rows], ri)
+                _close(prob.cpu().double().numpy()[rows], rp, 80 * U * rp)
+                assert torch.equal(counts.long(), torch.bincount(idx.reshape(-1).long(), minlength=E))
+
+
+@gpu
+def test_biases_that_differ_by_less_than_their_distance_from_the_lowest_shows():
+    """1 + 2^-23 and 1 are the same over -3 in fp32: with equal logits the larger bias still goes first."""
+    m = need_gpu()
+    b = torch.ones(32)
+    b[20] += 2.0 ** -23
+    b[3] = -3.0
+    for T in (3, 5000):
+        lg = torch.zeros((T, 32))
+        idx, _, _ = m.moe_route_grouped(lg.cuda(), 3, bias=b.cuda())
+        torch.cuda.synchronize()
+        assert (idx.cpu() == torch.tensor([20, 0, 1], dtype=torch.int32)).all()
 
 
 @gpu
