@@ -8,6 +8,10 @@
 // workgroup's 256 threads have in flight at once.  Workgroups take the chunks in a fixed order, so that the sum does
 // not change from call to call.  A thread keeps the tensors' first chunks in registers, so that finding a chunk's
 // tensor is a vote of the wave and not a search through memory.
+//
+// Measured: 554M fp32 values into bf16 947 us -- 355 for the sum, 6.2 TB/s, and 590 for the scaling, 5.6 TB/s; 200
+// tensors with 32M values of both types into fp32 71 us -- 27 and 33 + 12 in two launches, since a table with outputs
+// holds 176.
 #include "common.h"
 #include "kernels.h"
 #include "eight.h"

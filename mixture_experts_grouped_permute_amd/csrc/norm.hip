@@ -8,7 +8,10 @@
 // rstd is formed again from s, which the backward reads anyway: both of its sums come from the same read.
 //
 // Memory bounds both.  A row stays in the registers of kL lanes between the sums and the results, kN pieces of 8
-// columns each, so that everything is read and written once.
+// columns each, so that everything is read and written once.  Measured: 16384 x 4096 bf16 with residual, y and codes
+// 98 us, 6.2 TB/s; 100003 x 1003 f32 169 us, 4.7 TB/s (rows at odd places: 14 % more is written, in partly filled lines);
+// one row of 4096 2.4 us.  Backward 16384 x 4096 bf16 90 us, 6.0 TB/s, of which 5 are the weight's sum; 20011 x 1407
+// f32 75 us, 4.5 TB/s.
 #include "common.h"
 #include "kernels.h"
 #include "block_scale.h"
