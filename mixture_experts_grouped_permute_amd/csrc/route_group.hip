@@ -689,8 +689,14 @@ __global__ __launch_bounds__(64 * kWaves) void route_group_bwd_kernel(const Grou
       g = p.dprob[at];
     }
     const bool has = e >= 0 && e < E;
-    const float sum = group_sum<16>(w * g);
-    float d = w * (p.renorm ? g - sum / p.scale : g);
+    // in 64 bits: g and the mean of all cancel, with one slot to nothing at all
+    double dot = (double)w * (double)g;
+    dot += pair<0>(dot);
+    dot += pair<1>(dot);
+    dot += pair<2>(dot);
+    dot += pair<3>(dot);
+    float d = (float)((double)w * (p.renorm ? (double)g - dot / (double)p.scale : (double)g));
+    const float sum = (float)dot;
     if (p.sigmoid && has) d *= 1.0f / (1.0f + expf(logit<kF32>(p.logits, t * E + e)));
     float* const mine = row + grp * E;
     if constexpr (kN > 0) {

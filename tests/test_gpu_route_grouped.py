@@ -240,6 +240,21 @@ def test_repeated_and_foreign_ids_in_the_gradient():
 
 
 @gpu
+def test_one_renormalised_slot_has_no_gradient():
+    """Its weight is the scale whatever the logits are: zeros, not what rounding leaves of a difference."""
+    m = need_gpu()
+    for score in ("sigmoid", "softmax"):
+        for scale in (1.0, 2.5, 0.1, 16.0):
+            for dtype in (F, B):
+                lg = _logits(333, 21, "normal", dtype).cuda()
+                idx, prob, _ = m.moe_route_grouped(lg, 1, score=score, scale=scale)
+                dp = torch.from_numpy(np.random.default_rng(3).standard_normal((333, 1)).astype(np.float32)).cuda()
+                out = m.moe_route_grouped_bwd(lg, idx, prob, dp, score=score, scale=scale)
+                torch.cuda.synchronize()
+                assert not out.any()
+
+
+@gpu
 def test_many_tokens_and_unaligned_logits():
     """More tokens than the kernels hold at once, and logits that begin anywhere."""
     m = need_gpu()
