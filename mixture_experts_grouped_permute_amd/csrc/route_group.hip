@@ -33,14 +33,43 @@ __device__ __forceinline__ uint64_t order_of(double v) {
   if (v != v) return ~0ull;
   return (u >> 63) ? ~u : u | 1ull << 63;
 }
-__device__ __forceinline__ uint64_t shfl_u64(uint64_t v, int src) {
-  return (uint64_t)__shfl((unsigned long long)v, src, 64);
+// A lane's value, in all of them (the lane is the same for all).
+__device__ __forceinline__ int from_lane(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+__device__ __forceinline__ uint64_t from_lane(uint64_t v, int lane) {
+  return (uint64_t)(uint32_t)from_lane((int)(uint32_t)(v >> 32), lane) << 32 | (uint32_t)from_lane((int)(uint32_t)v, lane);
+}
+__device__ __forceinline__ double from_lane(double v, int lane) {
+  return __builtin_bit_cast(double, from_lane(__builtin_bit_cast(uint64_t, v), lane));
+}
+template <int st>
+__device__ __forceinline__ uint64_t pair64(uint64_t v) {
+  return (uint64_t)(uint32_t)dpp_pair<st>((int)(uint32_t)(v >> 32)) << 32 | (uint32_t)dpp_pair<st>((int)(uint32_t)v);
+}
+__device__ __forceinline__ double sum16(double v) {      // over each 16 lanes
+  v += pair<0>(v);
+  v += pair<1>(v);
+  v += pair<2>(v);
+  return v + pair<3>(v);
 }
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
-  return v;
+  v = sum16(v);
+  return (from_lane(v, 0) + from_lane(v, 16)) + (from_lane(v, 32) + from_lane(v, 48));
 }
+__device__ __forceinline__ double wave_max(double v) {
+  v = fmax(v, pair<0>(v));
+  v = fmax(v, pair<1>(v));
+  v = fmax(v, pair<2>(v));
+  v = fmax(v, pair<3>(v));
+  return fmax(fmax(from_lane(v, 0), from_lane(v, 16)), fmax(from_lane(v, 32), from_lane(v, 48)));
+}
+// The larger key, of equal ones the lower id.
+__device__ __forceinline__ void take_larger(uint64_t& k, int& e, uint64_t ok, int oe) {
+  const bool other = ok > k || (ok == k && oe < e);
+  k = other ? ok : k;
+  e = other ? oe : e;
+}
+template <int st>
+__device__ __forceinline__ void larger_pair(uint64_t& k, int& e) { take_larger(k, e, pair64<st>(k), dpp_pair<st>(e)); }
 __device__ __forceinline__ void wave_lds() {            // LDS writes of the wave's lanes ahead of its later reads
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
@@ -53,7 +82,8 @@ __device__ __forceinline__ float logit(const void* lg, int64_t at) {
 }
 
 // One token by one wave, in 64 bits throughout: lane i holds experts i, i + 64, ..; cs: E doubles of the wave's.
-// Returns the lane's slot (lane < k).
+// Returns the lane's slot (lane < k).  Few tokens come here and each is waited for, so what counts is the time of one: lanes
+// exchange by moves in the VALU and whole waves by reading a lane, not through LDS (a token's 15 us with the launch 11).
 struct Slot {
   int e;
   float w;
@@ -63,12 +93,18 @@ __device__ __forceinline__ Slot route_token(const GroupRoute& p, int64_t t, int 
   constexpr int kC = kMaxExperts / 64;
   const double none = -__builtin_huge_val();
   double s[kC];
+  float bias[kC];
   uint64_t key[kC];
   bool out[kC];                                         // -inf: no weight
 #pragma unroll
   for (int c = 0; c < kC; ++c) {
     const int e = lane + 64 * c;
     s[c] = e < p.E ? (double)logit<kF32>(p.logits, t * p.E + e) : none;
+    bias[c] = p.bias && e < p.E ? p.bias[e] : 0.f;
+  }
+#pragma unroll
+  for (int c = 0; c < kC; ++c) {
+    const int e = lane + 64 * c;
     out[c] = s[c] == none;
     key[c] = order_of(s[c]);
     if (p.G > 1 && p.best == 1 && !p.bias && e < p.E) cs[e] = s[c];
@@ -80,8 +116,7 @@ __device__ __forceinline__ Slot route_token(const GroupRoute& p, int64_t t, int 
     double m = none;
 #pragma unroll
     for (int c = 0; c < kC; ++c) m = fmax(m, s[c]);
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) m = fmax(m, __shfl_xor(m, d, 64));
+    m = wave_max(m);
     if (m == none) m = 0.0;
     double total = 0.0;
 #pragma unroll
@@ -97,7 +132,7 @@ __device__ __forceinline__ Slot route_token(const GroupRoute& p, int64_t t, int 
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
       const int e = lane + 64 * c;
-      double v = s[c] + (p.bias && e < p.E ? (double)p.bias[e] : 0.0);
+      double v = s[c] + (double)bias[c];
       if (out[c]) v = none;
       if (p.bias) {
         key[c] = order_of(v);
@@ -135,19 +170,18 @@ __device__ __forceinline__ Slot route_token(const GroupRoute& p, int64_t t, int 
         b = oa; kb = ka2;
       }
     }
-    const uint64_t sum = order_of(p.best == 2 ? a + b : a);
-    const uint64_t mine = shfl_u64(sum, (lane < p.G ? lane : 0) * per);
+    const uint64_t sum = order_of(p.best == 2 ? a + b : a);   // of group gi
     wave_lds();
     int rank = 0;
     for (int h = 0; h < p.G; ++h) {
-      const uint64_t o = shfl_u64(mine, h);
-      rank += o > mine || (o == mine && h < lane);
+      const uint64_t o = from_lane(sum, h * per);
+      rank += o > sum || (o == sum && h < gi);
     }
-    const uint64_t kept = __ballot(lane < p.G && rank < p.kg);
+    const uint64_t kept = __ballot(gi < p.G && rank < p.kg);   // bit e / n per: whether expert e's group is
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
       const int e = lane + 64 * c;
-      if (e < p.E && !(kept >> (e / n) & 1)) {
+      if (e < p.E && !(kept >> (e / n * per) & 1)) {
         key[c] = order_of(none);
         out[c] = true;
       }
@@ -171,18 +205,16 @@ __device__ __forceinline__ Slot route_token(const GroupRoute& p, int64_t t, int 
         be = lane + 64 * c;
         bs = out[c] ? 0.0 : s[c];
       }
-    uint64_t tk = bk;
-    int te = be;
+    larger_pair<0>(bk, be);
+    larger_pair<1>(bk, be);
+    larger_pair<2>(bk, be);
+    larger_pair<3>(bk, be);
+    uint64_t tk = from_lane(bk, 0);
+    int te = from_lane(be, 0);
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-      const uint64_t ok = (uint64_t)__shfl_xor((unsigned long long)tk, d, 64);
-      const int oe = __shfl_xor(te, d, 64);
-      if (oe < kMaxExperts && (te == kMaxExperts || ok > tk || (ok == tk && oe < te))) {
-        tk = ok;
-        te = oe;
-      }
-    }
-    const double sel = __shfl(bs, te & 63, 64);         // (the owner's best is the wave's)
+    for (int r = 16; r < 64; r += 16) take_larger(tk, te, from_lane(bk, r), from_lane(be, r));
+    te = __builtin_amdgcn_readfirstlane(te);
+    const double sel = from_lane(bs, te & 63);          // (the owner's best is the wave's)
     if ((te & 63) == lane) gone |= 1u << (te >> 6);
     if (lane == j) {
       r.e = te;
@@ -190,7 +222,7 @@ __device__ __forceinline__ Slot route_token(const GroupRoute& p, int64_t t, int 
     }
   }
   if (p.renorm) {
-    const double total = wave_sum(w);
+    const double total = sum16(w);                      // (k <= 16)
     w = total == 0.0 ? 0.0 : w / total;
   }
   r.w = (float)(w * (double)p.scale);
