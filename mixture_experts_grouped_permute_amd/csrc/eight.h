@@ -64,6 +64,15 @@ struct Eight {
         else global<uint16_t>(p)[at + i] = (uint16_t)(w[0][i >> 1] >> (i & 1) * 16);
       }
   }
+  // without the first `skip` of them
+  __device__ __forceinline__ void store_from(void* p, int64_t at, int skip) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i >= skip) {
+        if constexpr (kF32) global<uint32_t>(p)[at + i] = w[i >> 2][i & 3];
+        else global<uint16_t>(p)[at + i] = (uint16_t)(w[0][i >> 1] >> (i & 1) * 16);
+      }
+  }
   __device__ __forceinline__ void zero() {
     w[0] = u32x4{0u, 0u, 0u, 0u};
     if constexpr (kF32) w[1] = u32x4{0u, 0u, 0u, 0u};

@@ -70,7 +70,7 @@ struct RowSum {
 
 // The columns of a lane's piece c: 8 from `col` on.  Where a row ends inside the piece it is moved back to end with
 // the row: its first `skip` columns are another lane's, whose results it repeats and whose sums it leaves out.
-// Rows of fewer than 8 columns never get here unaligned (the launcher pads nothing: they take kernel `narrow`).
+// (Rows of fewer than 8 columns have kernels of their own.)
 struct Piece {
   int col, skip;
   bool in;
@@ -276,7 +276,9 @@ __global__ __launch_bounds__(threads_of(kL)) void rmsnorm_bwd_kernel(const NormB
       if (in) {
         Eight<kF32, kAligned> e;
         e.set(o);
-        e.template store<kOnce>(p.dx, t * H + q[c].col);
+        // (late, and dx over ds: another wave may not have read its ds yet where a piece that was moved back repeats it)
+        if (kLate && !kAligned && q[c].skip) e.store_from(p.dx, t * H + q[c].col, q[c].skip);
+        else e.template store<kOnce>(p.dx, t * H + q[c].col);
       }
     }
     if constexpr (kLate) fetch(t + step);

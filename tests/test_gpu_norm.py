@@ -121,7 +121,9 @@ def test_gradient_over_the_residuals_own(dtype):
     m = need_gpu()
     from mixture_experts_grouped_permute_amd import _lib as L
     lib = m.load()
-    for T, H in ((1, 4096), (3, 5), (600, 255), (40, 2048), (9, 30001), (700, 8192)):
+    # (10243, 20483: the last, moved-back piece of a row is a wave's first)
+    for T, H in ((1, 4096), (3, 5), (600, 255), (40, 2048), (9, 30001), (700, 8192), (40, 10243), (40, 20483), (600, 10243),
+                 (600, 20483)):
         dy, s, ds = (_x(T, H, dtype, i).cuda() for i in range(3))
         w = _w(H, dtype).cuda()
         want, wdw = m.moe_add_rmsnorm_bwd(dy, s, w, ds=ds)
