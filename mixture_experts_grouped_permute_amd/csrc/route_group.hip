@@ -83,7 +83,8 @@ __device__ __forceinline__ float logit(const void* lg, int64_t at) {
 
 // One token by one wave, in 64 bits throughout: lane i holds experts i, i + 64, ..; cs: E doubles of the wave's.
 // Returns the lane's slot (lane < k).  Few tokens come here and each is waited for, so what counts is the time of one: lanes
-// exchange by moves in the VALU and whole waves by reading a lane, not through LDS (a token's 15 us with the launch 11).
+// exchange by moves in the VALU and whole waves by reading a lane, not through LDS (13 us a launch for 131072 tokens,
+// 15 through LDS).
 struct Slot {
   int e;
   float w;
@@ -332,15 +333,20 @@ __device__ __forceinline__ uint32_t whole(float x) {
 // The first is exact.  The others' roundings keep the order, so that one step apart is right without a bias, and as far
 // apart as twice the scores' errors with one; what is nearer and not of equal logits and biases is done again.
 // (Keys of the fp32 number in a double's mantissa, the id below it, need no second look at logits but 64-bit max and min
-// and moves of 2 words between lanes: 98 us at 131072 x 256 with a bias and 8 groups, where these take 75.)
+// and moves of 2 words between lanes: 98 us at 131072 x 256 with a bias and 8 groups, where these took 75.)
 // kInline: the wave does such tokens itself; else it marks them with id -1 for route_again_kernel, whose 64-bit code would
 // take half of this one's waves for its registers (140 us in one kernel, 98 and 19 in two).
-// Measured: 131072 x 256 f32, bias, 4 of 8 groups, k = 8, with counts: 91 us -- 75 here, VALU issue 72 % busy with 980
-// instructions for 4 tokens, 264 of them the networks, 180 the scores; 15 for the 285 tokens done again, 5 for the counts'
-// total -- of 28 that its bytes take.  Without groups and bias 55.
-template <int kN, int kK, bool kInline>
+// kHalf: half of the groups stay at most.  Those next in rank give their lanes to them: each takes over half the experts of
+// the one kg ahead, and the selection has half as many a lane.  131072 x 256 of 8 groups 83 us with it, 88 without (bf16 74
+// and 84), 50021 x 160 26 and 29, 131072 x 64 of 4 groups 43 and 45.
+// Measured: 131072 x 256 f32, bias, 4 of 8 groups, k = 8, with counts: 83 us -- 71 here, VALU issue 68 % busy with 870
+// instructions for 4 tokens, 180 of them the scores; 12.5 for the 285 tokens done again, 5 for the counts' total -- of 28
+// that its bytes take.  Without groups and bias 53.
+template <int kN, int kK, bool kInline, bool kHalf>
 __global__ __launch_bounds__(64 * kWaves, kInline ? 1 : kN <= 16 ? 4 : 2) void route_group_kernel(const GroupRoute p) {
   using K = Key<false>;
+  constexpr int kS = kHalf ? kN / 2 : kN;                // experts a lane in the selection
+  __shared__ uint8_t holder[kHalf ? kWaves * 64 : 1];    // the lane that holds the experts of the group of a rank
   __shared__ __attribute__((aligned(16))) char stage[room(kWaves * kSpan)];
   __shared__ int cnt[kMaxExperts];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, sub = lane & 15, grp = lane >> 4;
@@ -465,29 +471,30 @@ __global__ __launch_bounds__(64 * kWaves, kInline ? 1 : kN <= 16 ? 4 : 2) void r
         }
       }
     };
-    uint32_t key[kN];
-    int id = 255 - e0;
+    // what becomes the keys' upper bits; with a bias the scores do
+    uint32_t x[kN];
+    int id = 255 - e0;                                   // of the lane's first expert, counted down
     if (p.bias) {
       score_all();
     } else if (exact) {
 #pragma unroll
-      for (int c = 0; c < kN; ++c, id -= lanes) key[c] = with_id(rank_of<0x10000u>(v[c]), id);
+      for (int c = 0; c < kN; ++c) x[c] = rank_of<0x10000u>(v[c]);
     } else {
 #pragma unroll
-      for (int c = 0; c < kN; ++c, id -= lanes) key[c] = with_id(whole(__builtin_fmaf(v[c], by, plus)), id);
+      for (int c = 0; c < kN; ++c) x[c] = whole(__builtin_fmaf(v[c], by, plus));
     }
     if (p.G > 1) {
       if (sums && !p.bias) score_all();
-      float x = kNone, y = kNone;                        // the two largest
+      float first = kNone, second = kNone;               // the two largest
 #pragma unroll
       for (int c = 0; c < kN; ++c) {
-        y = __builtin_amdgcn_fmed3f(x, y, v[c]);
-        x = fmaxf(x, v[c]);
+        second = __builtin_amdgcn_fmed3f(first, second, v[c]);
+        first = fmaxf(first, v[c]);
       }
-      if (lanes > 1) merge_best<0>(x, y);
-      if (lanes > 2) merge_best<1>(x, y);
-      if (lanes > 4) merge_best<2>(x, y);
-      const float score = sums ? x + y : x;
+      if (lanes > 1) merge_best<0>(first, second);
+      if (lanes > 2) merge_best<1>(first, second);
+      if (lanes > 4) merge_best<2>(first, second);
+      const float score = sums ? first + second : first;
       int rank;
       if (lanes == 8) rank = rank_groups<8>(score, g);
       else if (lanes == 4) rank = rank_groups<4>(score, g);
@@ -498,24 +505,50 @@ __global__ __launch_bounds__(64 * kWaves, kInline ? 1 : kN <= 16 ? 4 : 2) void r
         const float least = -group_max<16>(kept ? -score : kNone), most = group_max<16>(kept ? kNone : score);
         bad |= !(least - most > 2.f * t0_err + 0x1p-20f * (range + 2.f));
       }
-      if (p.bias) {
+      if constexpr (kHalf) {
+        uint8_t* const at = holder + (tid & ~15) + q;
+        if (kept) at[rank * lanes] = (uint8_t)lane;
+        wave_lds();
+        const bool helps = own && !kept && rank < 2 * p.kg;
+        const int from_it = helps ? at[(rank - p.kg) * lanes] & 63 : lane;
+        wave_lds();
+        if (p.bias) {
+#pragma unroll
+          for (int c = 0; c < kN; ++c) x[c] = __builtin_bit_cast(uint32_t, v[c]);
+        }
+        const uint32_t none = p.bias ? 0xFF800000u : 0u;   // -inf, or the lowest number
+#pragma unroll
+        for (int c = 0; c < kS; ++c) {
+          const uint32_t other = (uint32_t)__shfl((int)x[kS + c], from_it, 64);
+          x[c] = kept ? x[c] : helps ? other : none;
+        }
+        const int half = __shfl(id, from_it, 64) - lanes * kS;
+        id = kept ? id : half;
+        if (p.bias) {
+#pragma unroll
+          for (int c = 0; c < kS; ++c) v[c] = __builtin_bit_cast(float, x[c]);
+        }
+      } else if (p.bias) {
 #pragma unroll
         for (int c = 0; c < kN; ++c) v[c] = kept ? v[c] : kNone;
       } else {
 #pragma unroll
-        for (int c = 0; c < kN; ++c) key[c] = kept ? key[c] : 0u;
+        for (int c = 0; c < kN; ++c) x[c] = kept ? x[c] : 0u;
       }
     }
     if (p.bias) {
 #pragma unroll
-      for (int c = 0; c < kN; ++c, id -= lanes) key[c] = with_id(whole(__builtin_fmaf(v[c], by, plus)), id);
+      for (int c = 0; c < kS; ++c) x[c] = whole(__builtin_fmaf(v[c], by, plus));
     }
-    constexpr int kA = kN > kK ? kN : kK;
+    uint32_t key[kS];
+#pragma unroll
+    for (int c = 0; c < kS; ++c, id -= lanes) key[c] = with_id(x[c], id);
+    constexpr int kA = kS > kK ? kS : kK;
     uint32_t a[kA];
 #pragma unroll
-    for (int c = 0; c < kN; ++c) a[c] = key[c];
-    sort_top<K, kN, kK>(a);
-    constexpr int kM = kN < kK ? kN : kK;
+    for (int c = 0; c < kS; ++c) a[c] = key[c];
+    sort_top<K, kS, kK>(a);
+    constexpr int kM = kS < kK ? kS : kK;
     merge_lanes<K, 16, kM, kK, 0>(a);
     // the lane's slot, and the last one
 #pragma unroll
@@ -537,7 +570,7 @@ __global__ __launch_bounds__(64 * kWaves, kInline ? 1 : kN <= 16 ? 4 : 2) void r
       const uint32_t floor = (last > apart ? last - apart : 0u) << 8;
       int reach = 0;
 #pragma unroll
-      for (int c = 0; c < kN; ++c) reach += key[c] >= floor;
+      for (int c = 0; c < kS; ++c) reach += key[c] >= floor;
       reach += dpp_pair<0>(reach);
       reach += dpp_pair<1>(reach);
       reach += dpp_pair<2>(reach);
@@ -552,8 +585,8 @@ __global__ __launch_bounds__(64 * kWaves, kInline ? 1 : kN <= 16 ? 4 : 2) void r
         const float ll = __shfl(le, end_lane, 64), bl = __shfl(be, end_lane, 64);
         int others = slot && !(le == ll && be == bl) ? -1 : 0;
 #pragma unroll
-        for (int c = 0; c < kN; ++c) {
-          const int ec = e0 + lanes * c;
+        for (int c = 0; c < kS; ++c) {
+          const int ec = kHalf ? 255 - (int)(key[c] & 255u) : e0 + lanes * c;
           if (key[c] >= floor) others += !(at_room(stage, place + ec) == ll && (!p.bias || p.bias[ec < E ? ec : 0] == bl));
         }
         others += dpp_pair<0>(others);
@@ -615,22 +648,28 @@ __global__ __launch_bounds__(64 * kWaves) void route_again_kernel(const GroupRou
   if (p.counts && tid < p.E) part[(int64_t)blockIdx.x * p.E + tid] = cnt[tid];
 }
 
-template <int kN, bool kInline>
+template <int kN, bool kInline, bool kHalf>
 void launch_k(const GroupRoute& p, int nb, hipStream_t st) {
-  if (p.k <= 2) route_group_kernel<kN, 2, kInline><<<nb, 64 * kWaves, 0, st>>>(p);
-  else if (p.k <= 4) route_group_kernel<kN, 4, kInline><<<nb, 64 * kWaves, 0, st>>>(p);
-  else if (p.k <= 8) route_group_kernel<kN, 8, kInline><<<nb, 64 * kWaves, 0, st>>>(p);
-  else route_group_kernel<kN, 16, kInline><<<nb, 64 * kWaves, 0, st>>>(p);
+  if (p.k <= 2) route_group_kernel<kN, 2, kInline, kHalf><<<nb, 64 * kWaves, 0, st>>>(p);
+  else if (p.k <= 4) route_group_kernel<kN, 4, kInline, kHalf><<<nb, 64 * kWaves, 0, st>>>(p);
+  else if (p.k <= 8) route_group_kernel<kN, 8, kInline, kHalf><<<nb, 64 * kWaves, 0, st>>>(p);
+  else route_group_kernel<kN, 16, kInline, kHalf><<<nb, 64 * kWaves, 0, st>>>(p);
 }
 template <bool kInline>
 void launch_n(const GroupRoute& p, int nb, hipStream_t st) {
   const int per = (p.E / p.G + p.lanes - 1) / p.lanes;   // experts a lane
-  if (per <= 1) launch_k<1, kInline>(p, nb, st);
-  else if (per <= 2) launch_k<2, kInline>(p, nb, st);
-  else if (per <= 4) launch_k<4, kInline>(p, nb, st);
-  else if (per <= 8) launch_k<8, kInline>(p, nb, st);
-  else if (per <= 16) launch_k<16, kInline>(p, nb, st);
-  else launch_k<32, kInline>(p, nb, st);
+  const bool half = !kInline && p.G > 1 && 2 * p.kg <= p.G;
+  constexpr bool kHalf = !kInline;
+  if (per <= 1) launch_k<1, kInline, false>(p, nb, st);
+  else if (per <= 2) launch_k<2, kInline, false>(p, nb, st);
+  else if (per <= 4 && half) launch_k<4, kInline, kHalf>(p, nb, st);
+  else if (per <= 4) launch_k<4, kInline, false>(p, nb, st);
+  else if (per <= 8 && half) launch_k<8, kInline, kHalf>(p, nb, st);
+  else if (per <= 8) launch_k<8, kInline, false>(p, nb, st);
+  else if (per <= 16 && half) launch_k<16, kInline, kHalf>(p, nb, st);
+  else if (per <= 16) launch_k<16, kInline, false>(p, nb, st);
+  else if (half) launch_k<32, kInline, kHalf>(p, nb, st);
+  else launch_k<32, kInline, false>(p, nb, st);
 }
 
 // counts[e] = sum over the nb blocks; a workgroup takes 16 experts, 64 slices of the blocks.

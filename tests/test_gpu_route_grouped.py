@@ -168,6 +168,32 @@ def test_nan_infinity_and_large_biases(dtype, E, k, G, kg, best):
 
 @gpu
 @pytest.mark.parametrize("dtype", [F, B], ids=["f32", "bf16"])
+@pytest.mark.parametrize("E,G,kg,k,best", [(256, 8, 4, 8, 2), (256, 8, 3, 8, 1), (256, 2, 1, 16, 2), (250, 2, 1, 3, 1),
+                                           (240, 16, 8, 6, 2), (255, 5, 2, 16, 2), (128, 16, 1, 5, 1), (99, 3, 1, 8, 2),
+                                           (64, 4, 2, 8, 2), (256, 4, 1, 2, 2), (252, 7, 3, 12, 1)])
+def test_few_groups_of_many_tokens(E, G, kg, k, best, dtype):
+    """Half of the groups or fewer, with rows that hold ties, NaN and infinities between ordinary ones."""
+    m = need_gpu()
+    T = 5003
+    lg = _logits(T, E, "normal", dtype)
+    lg[1::5] = torch.round(lg[1::5].float()).to(dtype)
+    lg[2::7, ::3] = -float("inf")
+    lg[3::11] = -float("inf")
+    lg[4::13, E - 1] = float("nan")
+    lg[5::17, E // 2] = float("inf")
+    for score in ("sigmoid", "softmax"):
+        for b in (None, _bias(E, "normal")):
+            kw = dict(score=score, groups=G, topk_groups=kg, group_best=best)
+            idx, prob, counts = m.moe_route_grouped(lg.cuda(), k, bias=_gpu(b), count=True, **kw)
+            torch.cuda.synchronize()
+            ri, rp, rc = group_route.forward(lg, k, b, **kw)
+            np.testing.assert_array_equal(idx.cpu().numpy(), ri)
+            np.testing.assert_array_equal(counts.cpu().numpy(), rc)
+            _close(prob.cpu().double().numpy(), rp, 80 * U * rp + TINY)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [F, B], ids=["f32", "bf16"])
 def test_equal_scores_go_by_their_ids(dtype):
     """Whole rows of equal logits, and biases that repeat, as routers begin: through the fp32 order and the 64-bit one."""
     m = need_gpu()
