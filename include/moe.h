@@ -370,7 +370,8 @@ moe_status moe_route_grouped_bwd(const void* logits, int logits_dtype, int64_t T
  * x, residual [T, H] in x_dtype (MOE_F32 or MOE_BF16); residual may be NULL.
  * weight      [H] in w_dtype: x_dtype or MOE_F32.
  * sum         [T, H] in x_dtype: receives s; given if and only if residual is.
- *             May be x or residual itself; no other two tensors overlap.
+ *             May be x or residual itself; outputs that overlap anything else
+ *             of the call are refused (MOE_ERR_INVALID_ARG).
  * y           [T, H] in x_dtype, or NULL.
  * q, scales   [T, H] E4M3 codes and [H/128, T] fp32 scales of the unrounded
  *             y, as fp8_block_quantize (axis 0) gives them: the operand of a
@@ -391,7 +392,8 @@ moe_status moe_add_rmsnorm(const void* x, const void* residual, int x_dtype, con
  *             dsum [T, H] the gradient that reaches s by other ways, or NULL;
  *             all in dtype.  weight [H] in w_dtype, as the forward's.
  * dx          [T, H] out in dtype: the gradient of s, and so of x and of
- *             residual.  May be dsum itself.  With r = 1 / sqrt(mean s^2 + eps):
+ *             residual.  May be dsum itself (other overlaps of an output are
+ *             refused, MOE_ERR_INVALID_ARG).  With r = 1 / sqrt(mean s^2 + eps):
  *               r (dy w - s r mean(dy w s r)) + dsum
  * dweight     [H] fp32 out: sum over the rows of dy s r.
  * workspace: moe_add_rmsnorm_bwd_workspace(T, H) bytes (device, 16-byte aligned,

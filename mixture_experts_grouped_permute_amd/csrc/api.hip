@@ -767,6 +767,23 @@ BalanceWs carve_balance(Carver& c, int64_t T, int E) {
 }
 inline bool under_4g(int64_t bytes) { return bytes < (int64_t)UINT32_MAX; }
 
+// Whether no output overlaps another tensor of the call (NULL: none): the first `out` places are outputs, the very first
+// of which may be one that is marked `same`.
+struct Place {
+  const void* p;
+  size_t bytes;
+  bool same;
+};
+bool held_apart(const Place* v, int n, int out) {
+  for (int i = 0; i < out; ++i)
+    for (int j = i + 1; j < n; ++j) {
+      if (!v[i].p || !v[j].p || (i == 0 && v[j].same && v[i].p == v[j].p)) continue;
+      const uintptr_t a = reinterpret_cast<uintptr_t>(v[i].p), b = reinterpret_cast<uintptr_t>(v[j].p);
+      if (a < b + v[j].bytes && b < a + v[i].bytes) return false;
+    }
+  return true;
+}
+
 // The norm's weight: the activations' type, or fp32.
 inline bool w_fits(int x_dtype, int w_dtype) { return w_dtype == x_dtype || w_dtype == MOE_F32; }
 
@@ -890,6 +907,10 @@ moe_status moe_add_rmsnorm(const void* x, const void* residual, int x_dtype, con
   MOE_CHECK(T <= (int64_t)INT32_MAX && H <= kNormMaxH && w_fits(x_dtype, w_dtype), MOE_ERR_UNSUPPORTED);
   if (q) MOE_CHECK(H % 128 == 0 && aligned16(x) && aligned16(residual) && aligned16(weight) && aligned16(sum) &&
                    aligned16(y) && aligned16(q), MOE_ERR_UNSUPPORTED);
+  const size_t all = (size_t)T * H, io = all * io_size(x_dtype);
+  const Place places[] = {{sum, io, false}, {y, io, false}, {q, all, false}, {scales, all / 32, false}, {x, io, true},
+                          {residual, io, true}, {weight, (size_t)H * io_size(w_dtype), false}};
+  MOE_CHECK(held_apart(places, 7, 4), MOE_ERR_INVALID_ARG);
   const NormFwd p{x, residual, weight, T, H, eps, sum, y, q, scales};
   HIP_TRY(launch_add_rmsnorm(p, x_dtype == MOE_F32, w_dtype == MOE_F32, reinterpret_cast<hipStream_t>(stream)));
   return MOE_OK;
@@ -908,6 +929,10 @@ moe_status moe_add_rmsnorm_bwd(const void* dy, const void* s, const void* dsum, 
   MOE_CHECK(T <= (int64_t)INT32_MAX && H <= kNormMaxH && w_fits(dtype, w_dtype), MOE_ERR_UNSUPPORTED);
   MOE_CHECK(workspace && workspace_bytes >= moe_add_rmsnorm_bwd_workspace(T, H), MOE_ERR_WORKSPACE);
   MOE_CHECK(aligned16(workspace), MOE_ERR_UNSUPPORTED);
+  const size_t io = (size_t)T * H * io_size(dtype);
+  const Place places[] = {{dx, io, false}, {dweight, (size_t)H * 4, false}, {workspace, moe_add_rmsnorm_bwd_workspace(T, H), false},
+                          {dy, io, false}, {s, io, false}, {dsum, io, true}, {weight, (size_t)H * io_size(w_dtype), false}};
+  MOE_CHECK(held_apart(places, 7, 3), MOE_ERR_INVALID_ARG);
   const NormBwd p{dy, s, dsum, weight, T, H, eps, dx, dweight, reinterpret_cast<float*>(workspace)};
   HIP_TRY(launch_rmsnorm_bwd(p, dtype == MOE_F32, w_dtype == MOE_F32, reinterpret_cast<hipStream_t>(stream)));
   return MOE_OK;

@@ -100,6 +100,25 @@ def test_add_rmsnorm_bwd_validation(lib):
     assert lib.moe_add_rmsnorm_bwd(*a) == uns
 
 
+def test_the_norms_outputs_are_held_apart(lib):
+    inv, _, _ = _codes()
+    MB = 1 << 20
+    T, H = 64, 256                                                # 32 KB in bf16, 64 in fp32
+    x, r, w, s, y, q, d, ws = (MB * (i + 1) for i in range(8))
+    ok = dict(x=x, r=r, w=w, s=s, y=y, q=q, d=d)
+    for change in (dict(s=x + 16), dict(s=r - 16), dict(s=x + T * H * 2 - 16), dict(y=x), dict(y=r + 32), dict(s=y), dict(q=x),
+                   dict(q=y + T * H), dict(d=q + T * H - 4), dict(w=s + 64), dict(d=w + H * 2 - 4), dict(s=x, y=x)):
+        a = dict(ok, **change)
+        assert lib.moe_add_rmsnorm(a["x"], a["r"], 1, a["w"], 1, T, H, 1e-6, a["s"], a["y"], a["q"], a["d"], None) == inv, change
+    need = lib.moe_add_rmsnorm_bwd_workspace(T, H)
+    ok = dict(dy=x, s=r, ds=s, w=w, dx=y, dw=q, ws=ws)
+    for change in (dict(dx=x), dict(dx=r), dict(dx=s + 16), dict(dx=s - 4), dict(dw=w), dict(dw=y + 64), dict(ws=x + 16),
+                   dict(dw=ws + need - 16), dict(ws=r - need + 16), dict(dx=s, dy=s)):
+        a = dict(ok, **change)
+        assert lib.moe_add_rmsnorm_bwd(a["dy"], a["s"], a["ds"], 0, a["w"], 0, T, H, 1e-6, a["dx"], a["dw"], a["ws"], need,
+                                       None) == inv, change
+
+
 def _arrays(ptrs, numel, kinds):
     n = len(ptrs)
     return (ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*numel), (ctypes.c_int32 * n)(*kinds)

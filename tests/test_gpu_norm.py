@@ -313,6 +313,10 @@ def test_refusals_on_the_gpu():
         m.moe_add_rmsnorm(torch.zeros((1, 40000), device="cuda"), torch.ones(40000, device="cuda"))
     with pytest.raises(m.MoeError):                       # codes want 16-byte rows
         m.moe_add_rmsnorm(torch.zeros(4 * 256 + 1, device="cuda")[1:].view(4, 256), w, codes=True)
+    rows = torch.zeros((6, 256), device="cuda")
+    with pytest.raises(m.MoeError):                       # the sum over a part of what is read
+        m.moe_add_rmsnorm(rows[:4], w, residual=x, sum_out=rows[1:5])
+    m.moe_add_rmsnorm(rows[:3], w, residual=x[:3], sum_out=rows[3:])    # (beside it)
     with pytest.raises(TypeError):
         m.moe_add_rmsnorm_bwd(x, x.bfloat16(), w)
     with pytest.raises(ValueError):
