@@ -410,7 +410,7 @@ moe_status moe_add_rmsnorm_bwd(const void* dy, const void* s, const void* dsum, 
  *
  * grads       HOST array of n device pointers, numel HOST [n] values of each
  *             (0: skipped, its pointer may be NULL), dtypes HOST int32 [n]
- *             (MOE_F32 or MOE_BF16).  Aligned to their type.
+ *             (MOE_F32 or MOE_BF16).  Aligned to their type, below 2^47.
  * sumsq       [1] fp64 out, device.
  * 1 <= n <= 65536, numel <= 2^35.  workspace: moe_grad_sumsq_workspace(numel, n)
  * bytes (device, 16-byte aligned, nothing in it is read before it is written).

@@ -788,6 +788,7 @@ bool held_apart(const Place* v, int n, int out) {
 inline bool w_fits(int x_dtype, int w_dtype) { return w_dtype == x_dtype || w_dtype == MOE_F32; }
 
 constexpr int64_t kMostGrad = (int64_t)1 << 35;   // (a launch's chunks stay within int32)
+inline bool in_47_bits(const void* p) { return reinterpret_cast<uint64_t>(p) >> 47 == 0; }   // (the tables' addresses)
 
 // Whether no output of a clipping overlaps another tensor that the call reads or writes (its own gradient, as the same
 // values in the same type, apart): workgroups take them in no order.
@@ -949,7 +950,7 @@ moe_status moe_grad_sumsq(const void* const* grads, const int64_t* numel, const 
   MOE_CHECK(n <= MOE_MAX_GRADS, MOE_ERR_UNSUPPORTED);
   for (int i = 0; i < n; ++i) {
     MOE_CHECK(numel[i] >= 0 && (grads[i] || numel[i] == 0) && io_ok(dtypes[i]), MOE_ERR_INVALID_ARG);
-    MOE_CHECK(numel[i] <= kMostGrad, MOE_ERR_UNSUPPORTED);
+    MOE_CHECK(numel[i] <= kMostGrad && in_47_bits(grads[i]), MOE_ERR_UNSUPPORTED);
   }
   MOE_CHECK(workspace && workspace_bytes >= moe_grad_sumsq_workspace(numel, n), MOE_ERR_WORKSPACE);
   MOE_CHECK(aligned16(workspace), MOE_ERR_UNSUPPORTED);
@@ -967,7 +968,7 @@ moe_status moe_grad_clip(const void* const* grads, const int64_t* numel, const i
   for (int i = 0; i < n; ++i) {
     MOE_CHECK(numel[i] >= 0 && ((grads[i] && out[i]) || numel[i] == 0), MOE_ERR_INVALID_ARG);
     MOE_CHECK(io_ok(dtypes[i]) && io_ok(out_dtypes[i]), MOE_ERR_INVALID_ARG);
-    MOE_CHECK(numel[i] <= kMostGrad, MOE_ERR_UNSUPPORTED);
+    MOE_CHECK(numel[i] <= kMostGrad && in_47_bits(grads[i]) && in_47_bits(out[i]), MOE_ERR_UNSUPPORTED);
   }
   const moe_status s = check_apart(grads, numel, dtypes, n, out, out_dtypes);
   if (s != MOE_OK) return s;

@@ -10,8 +10,8 @@
 // tensor is a vote of the wave and not a search through memory.
 //
 // Measured: 554M fp32 values into bf16 947 us -- 355 for the sum, 6.2 TB/s, and 590 for the scaling, 5.6 TB/s; 200
-// tensors with 32M values of both types into fp32 71 us -- 27 and 33 + 12 in two launches, since a table with outputs
-// holds 176.
+// tensors with 32M values of both types into fp32 64 us, 27 and 38 (71 with 64-bit addresses, of which a table with
+// outputs holds 176: 27 and 33 + 12 in two launches); 300 of up to 5000 values 22 (25).
 #include "common.h"
 #include "kernels.h"
 #include "eight.h"
@@ -23,18 +23,33 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kChunk = 8192, kPieces = kChunk / (8 * kThreads);
-constexpr int kSumTable = 256, kClipTable = 176;
-constexpr uint64_t kF32Bit = 1ull << 63;                // in a table's address: fp32 values (else bf16)
+constexpr int kSumTable = 312, kClipTable = 216;
+constexpr uint64_t kF32Bit = 1ull << 47;                // in a table's address: fp32 values (else bf16)
 
+// Addresses in 48 bits (a process has 47), so that a launch takes a quarter more tensors; all in whole words, which are
+// read as scalars.
 template <int kTensors, bool kOut>
 struct Table {
-  uint64_t g[kTensors];
-  uint64_t out[kOut ? kTensors : 1];
+  uint32_t g[kTensors], g_last[kTensors];                // lower word; upper 16 bits, and << 16 the values of the last chunk
+  uint32_t out[kOut ? kTensors : 1], out_up[kOut ? kTensors / 2 : 1];   // lower word; upper 16 bits, two in a word
   int32_t first[kTensors + 1];         // chunk of the launch that the tensor begins with
-  uint16_t last[kTensors];             // values of its last chunk
   int tensors;
+  __device__ __forceinline__ uint64_t grad(int e) const { return g[e] | (uint64_t)(g_last[e] & 0xFFFFu) << 32; }
+  __device__ __forceinline__ uint64_t to(int e) const {
+    return out[e] | (uint64_t)(out_up[e / 2] >> 16 * (e & 1) & 0xFFFFu) << 32;
+  }
+  __device__ __forceinline__ int last(int e) const { return (int)(g_last[e] >> 16); }
+  void set(int e, uint64_t a, int values) {
+    g[e] = (uint32_t)a;
+    g_last[e] = (uint32_t)(a >> 32) | (uint32_t)values << 16;
+  }
+  void set_out(int e, uint64_t a) {
+    const uint32_t up = (uint32_t)(a >> 32);
+    out[e] = (uint32_t)a;
+    out_up[e / 2] = e & 1 ? out_up[e / 2] | up << 16 : up;
+  }
 };
-static_assert(sizeof(Table<kSumTable, false>) <= 3800 && sizeof(Table<kClipTable, true>) <= 4000, "kernel arguments");
+static_assert(sizeof(Table<kSumTable, false>) <= 4000 && sizeof(Table<kClipTable, true>) <= 4000, "kernel arguments");
 
 // A chunk: its tensor, its first value and how many it has.
 struct Chunk {
@@ -59,7 +74,7 @@ struct Finder {
 #pragma unroll
     for (int i = 0; i < kR; ++i) e += __popcll(__ballot(first[i] <= c));
     const int k = c - t.first[e];
-    return {e, (int64_t)k * kChunk, c + 1 == t.first[e + 1] ? t.last[e] : kChunk};
+    return {e, (int64_t)k * kChunk, c + 1 == t.first[e + 1] ? t.last(e) : kChunk};
   }
 };
 
@@ -113,7 +128,7 @@ __global__ __launch_bounds__(kThreads) void grad_sumsq_kernel(const Table<kSumTa
   const int chunks = tab.first[tab.tensors];
   for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
     const Chunk k = finder.find(tab, c);
-    const uint64_t g = tab.g[k.e];
+    const uint64_t g = tab.grad(k.e);
     const void* base = reinterpret_cast<const void*>(g & ~kF32Bit);
     if (g & kF32Bit) for_pieces<true, kOnce>(base, k.at, k.n, add);
     else for_pieces<false, kOnce>(base, k.at, k.n, add);
@@ -145,7 +160,7 @@ __global__ __launch_bounds__(kThreads) void grad_clip_kernel(const Table<kTensor
   const int chunks = tab.first[tab.tensors];
   for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
     const Chunk k = finder.find(tab, c);
-    const uint64_t g = tab.g[k.e], o = kOut ? tab.out[kOut ? k.e : 0] : g;
+    const uint64_t g = tab.grad(k.e), o = kOut ? tab.to(kOut ? k.e : 0) : g;
     if (by == 1.0f && g == o) continue;                 // in place, and nothing to change
     const void* base = reinterpret_cast<const void*>(g & ~kF32Bit);
     void* to = reinterpret_cast<void*>(o & ~kF32Bit);
@@ -183,10 +198,9 @@ int next_table(const GradList& l, int* at, Table<kTensors, kOut>* tab) {
     const int i = *at;
     const int64_t n = l.numel[i];
     if (n == 0) continue;
-    tab->g[e] = entry(l.g[i], l.dtype[i]);
-    if constexpr (kOut) tab->out[e] = entry(l.out[i], l.out_dtype[i]);
+    tab->set(e, entry(l.g[i], l.dtype[i]), (int)((n - 1) % kChunk) + 1);
+    if constexpr (kOut) tab->set_out(e, entry(l.out[i], l.out_dtype[i]));
     tab->first[e] = (int32_t)chunks;
-    tab->last[e] = (uint16_t)((n - 1) % kChunk + 1);
     chunks += (n - 1) / kChunk + 1;
     ++e;
   }
@@ -198,8 +212,8 @@ int next_table(const GradList& l, int* at, Table<kTensors, kOut>* tab) {
 constexpr int kSumBlocks = 1024, kClipBlocks = 2048;
 
 // Whether the gradients are more than the last cache (256 MB) holds, so that none is left in it for the clipping: both
-// passes then go past the caches (1.4 GB + 0.7 GB in fp32 into bf16: 948 us instead of 1000; 96 MB of 200 tensors 73
-// us through the caches, 76 past them).
+// passes then go past the caches (1.4 GB + 0.7 GB in fp32 into bf16: 948 us instead of 1000; 96 MB of 200 tensors 3 us
+// less through the caches).
 bool past_caches(const GradList& l) {
   double bytes = 0.0;
   for (int i = 0; i < l.n; ++i) bytes += (double)l.numel[i] * (l.dtype[i] == 0 ? 4 : 2);
@@ -262,7 +276,7 @@ hipError_t launch_grad_clip(const GradList& l, const double* sumsq, double* part
   int64_t parts = 1;
   if (!sumsq) {
     // each workgroup adds the parts of one launch up by itself, 8 KB of them, in place of a launch that does it (4.7 us
-    // of 200 tensors' 73); more are added up once
+    // for 200 tensors); more are added up once
     parts = launch_parts(l, part, st);
     sumsq = part;
     if (parts > kSumBlocks || parts == 0) {
@@ -274,7 +288,7 @@ hipError_t launch_grad_clip(const GradList& l, const double* sumsq, double* part
   }
   bool in_place = true;
   for (int i = 0; i < l.n; ++i) in_place &= l.numel[i] == 0 || (l.g[i] == l.out[i] && l.dtype[i] == l.out_dtype[i]);
-  // (256 tensors a launch in place, 176 with outputs of their own)
+  // (312 tensors a launch in place, 216 with outputs of their own)
   if (in_place) launch_scaled<kSumTable, false>(l, sumsq, (int)parts, max_norm, norm, st);
   else launch_scaled<kClipTable, true>(l, sumsq, (int)parts, max_norm, norm, st);
   return hipGetLastError();

@@ -158,6 +158,8 @@ def test_grad_clip_validation(lib):
     assert _clip(lib, [P], [4], [0], [None], [0], norm=P) == inv
     assert _clip(lib, [P], [4], [0], [2 * P], [2], norm=P) == inv
     assert _clip(lib, [P], [(1 << 35) + 1], [0], [P], [0], norm=P) == uns
+    assert _clip(lib, [1 << 47], [4], [0], [P], [0], norm=P) == uns               # no address of a process
+    assert _clip(lib, [P], [4], [0], [(1 << 48) + P], [0], norm=P) == uns
 
 
 def test_grad_clip_refuses_overlaps(lib):

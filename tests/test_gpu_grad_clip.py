@@ -30,7 +30,7 @@ def _check(out, want, dtype):
 
 
 LISTS = [[1], [0, 3], [7, 0, 0, 65536], [32768], [32769, 1, 2, 3], [100003, 5, 77777], [3] * 300, [1000] * 129, [128, 1 << 20],
-         list(range(1, 200))]
+         list(range(1, 200)), [9] * 217, [2] * 313, [8193] * 433]
 
 
 @gpu
