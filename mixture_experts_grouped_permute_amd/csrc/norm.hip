@@ -247,7 +247,8 @@ __global__ __launch_bounds__(threads_of(kL)) void rmsnorm_bwd_kernel(const NormB
         for (int i = 0; i < (kF32 ? 2 : 1); ++i) asm volatile("" : "+v"(rs[c].w[i]), "+v"(rd[c].w[i]));
     }
     Sum::sum(v, red, turn);
-    const float rstd = 1.0f / sqrtf(v[0] / (float)H + p.eps);
+    // (a place without a row adds nothing to dw, also where eps is 0: its zeros times infinity would)
+    const float rstd = t < p.T ? 1.0f / sqrtf(v[0] / (float)H + p.eps) : 0.f;
     const float mean = v[1] * rstd / (float)H;          // of g xh
 #pragma unroll
     for (int c = 0; c < kN; ++c) {

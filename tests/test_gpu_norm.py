@@ -321,3 +321,21 @@ def test_refusals_on_the_gpu():
         m.moe_add_rmsnorm_bwd(x, x.bfloat16(), w)
     with pytest.raises(ValueError):
         m.moe_add_rmsnorm_bwd(x, x, w, ds=x[:2])
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [B, F], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,H", [(1, 64), (3, 8), (5, 255), (7, 128), (515, 130), (515, 96), (1001, 700), (513, 2048),
+                                 (600, 1003), (2, 20483)])
+def test_gradient_without_eps(T, H, dtype):
+    """Places for rows that there are none of (a workgroup holds up to 16) leave the weight's gradient alone."""
+    m = need_gpu()
+    s, dy, w = _x(T, H, dtype, 0), _x(T, H, dtype, 1), _w(H, dtype)
+    y, _, _, _ = m.moe_add_rmsnorm(s.cuda(), w.cuda(), eps=0.0)
+    dx, dw = m.moe_add_rmsnorm_bwd(dy.cuda(), s.cuda(), w.cuda(), eps=0.0)
+    torch.cuda.synchronize()
+    want = norm.forward(s, w, 0.0)
+    assert (np.abs(_np(y) - want) <= (80 * U + _half(dtype)) * np.abs(want) + 1e-38).all()
+    rx, rw, mag, wmag = norm.backward(dy, s, w, 0.0)
+    assert (np.abs(_np(dx) - rx) <= 240 * U * mag + _half(dtype) * np.abs(rx) + 1e-38).all()
+    assert (np.abs(_np(dw) - rw) <= (T + 100) * U * wmag + 1e-38).all()
