@@ -323,7 +323,9 @@ moe_status moe_route_balance_bwd(const void* logits, int logits_dtype, const uin
  *   topk_idx [T, k] int32: the experts of the k largest c in descending order
  *   (equal: lower id).
  *   topk_prob [T, k] fp32: s at topk_idx, 0 where c is -inf; with renormalize
- *   divided by their sum over the k (0 where that is 0); times scale.
+ *   divided by their sum over the k (0 where that is 0); times scale.  Scores are
+ *   64-bit numbers in this: the sigmoid of a logit below -709.78 is 0, so a row of
+ *   nothing else (a padding token's lowest value) has weights 0, and no gradient.
  * Without a bias experts are ordered by their logits (as their scores are, also
  * where these round to the same value), and groups of one best by their best
  * one's; else c and the sums are compared as 64-bit values.  A NaN goes ahead of

@@ -4,7 +4,7 @@
 //   the G groups of n = E / G consecutive experts are ordered by the sum of their `best` (1 or 2) largest c, the
 //   kg best stay (equal sums: lower group), experts of the others have c = -inf;
 //   idx = the k largest c (equal: lower id);  w_j = s[idx_j], 0 where c is -inf, divided by their sum if
-//   renormalised (0 if that is 0), times scale.
+//   renormalised (0 if that is 0), times scale.  (0 as 64-bit numbers are: a sigmoid below l = -709.78.)
 // Without a bias experts are ordered by their logits, as their scores are, and groups of one best by their best's; else
 // c and the sums are compared as 64-bit values, so that the order does not hang on how an exponential rounds.
 //
@@ -26,6 +26,8 @@ namespace {
 
 constexpr int kWaves = 4, kTokens = 4 * kWaves;         // tokens of a workgroup at a time
 constexpr float kNone = -__builtin_huge_valf();
+// The least logit whose sigmoid 1 / (1 + exp(-l)) is not 0 in 64 bits: -709.7827, the largest double's logarithm, cut to fp32.
+constexpr float kLeast = -0x1.62e42ep9f;
 
 // A number in the order of the doubles: -inf lowest, both zeros equal, every NaN on top.
 __device__ __forceinline__ uint64_t order_of(double v) {
@@ -596,16 +598,25 @@ __global__ __launch_bounds__(64 * kWaves, kInline ? 1 : kN <= 16 ? 4 : 2) void r
         bad |= odd || others != 0;
       }
     }
-    // weights: of sigmoids as multiples of e^top, which the quotient drops, so that tiny ones keep their ratios
+    // weights: of sigmoids as multiples of e^top, which the quotient drops, so that tiny ones keep their ratios, down to
+    // those that are 0 in 64 bits; softmax scores among which a bias has selected none that is near the row's largest
+    // may be 0 as well, and are left to 64 bits
     float w = 0.f;
     if (p.sigmoid) {
       const float top = p.renorm ? fminf(group_max<16>(le), 0.f) : 0.f;
-      w = le >= 0.f ? 1.0f / (1.0f + expf(-le)) : expf(le - top) / (1.0f + expf(le));
+      w = le >= 0.f ? 1.0f / (1.0f + expf(-le)) : le < kLeast ? 0.f : expf(le - top) / (1.0f + expf(le));
+    } else if (p.renorm) {
+      const float top = group_max<16>(le);
+      if (p.bias) bad |= !(top - m > -700.f);
+      w = expf(le - top);
     } else {
-      w = p.renorm ? expf(le - group_max<16>(le)) : expf(le - m) / total;
+      w = expf(le - m) / total;
     }
     w = slot ? w : 0.f;
-    if (p.renorm) w /= group_sum<16>(w);
+    if (p.renorm) {
+      const float sum = group_sum<16>(w);
+      w = sum == 0.f ? 0.f : w / sum;
+    }
     const uint64_t again = __ballot(bad && in);
     const bool done = (again >> (lane & 48) & 0xFFFFu) == 0;
     if (in && done && slot) {

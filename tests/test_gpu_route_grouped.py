@@ -370,3 +370,44 @@ def test_refusals_on_the_gpu():
         m.moe_route_grouped_bwd(lg, idx, prob, prob, scale=-1.0)
     with pytest.raises(m.MoeError):
         m.moe_route_grouped(torch.zeros((0, 8), device="cuda"), 2)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [F, B], ids=["f32", "bf16"])
+@pytest.mark.parametrize("T", [40, 5003])
+@pytest.mark.parametrize("E,k,G,kg,best", [(16, 4, 1, 1, 1), (64, 8, 8, 4, 2), (256, 8, 1, 1, 1), (256, 6, 8, 5, 1)])
+def test_rows_of_very_low_logits(E, k, G, kg, best, T, dtype):
+    """Whole rows whose sigmoids are 0 in 64 bits (below -709.78, a padding token's lowest value among them) have no weight
+    and no gradient, whichever way a token takes; of the lowest that are not the ratios stay.  Softmax scores likewise,
+    where a bias selects what lies far below the row's largest."""
+    m = need_gpu()
+    g = np.random.default_rng(E)
+    lg = g.standard_normal((T, E)) * 1.5
+    low = np.arange(T) % 10
+    lg[low == 1] = float(torch.finfo(dtype).min)
+    lg[low == 2] = -1000.0
+    lg[low == 3] = -1000.0 - 64 * np.round(g.random(((low == 3).sum(), E)) * 60)
+    lg[low == 4] = -712.0 + 8 * np.round(g.random(((low == 4).sum(), E)))          # 0 or not, experts apart
+    lg[low == 5] -= 500.0
+    lg[low == 6] = -5000.0                                                         # softmax: all alike
+    lg[low == 7, : E // 2] -= 1000.0                                               # half of them far below
+    lg[low == 8, : E // 2] -= 600.0
+    t = torch.from_numpy(lg.astype(np.float32)).to(dtype)
+    rows = np.r_[0:80, T - 40:T] if T > 120 else np.arange(T)
+    first = torch.where(torch.arange(E) < E // 2, 3.0, 0.0)                        # selects the lower half
+    for score in ("sigmoid", "softmax"):
+        for b in (None, _bias(E, "normal"), torch.zeros(E), _bias(E, "normal") + first):
+            for renorm in (True, False):
+                kw = dict(score=score, groups=G, topk_groups=kg, group_best=best, renormalize=renorm, scale=2.5)
+                idx, prob, counts = m.moe_route_grouped(t.cuda(), k, bias=_gpu(b), count=True, **kw)
+                dp = torch.from_numpy(np.random.default_rng(1).standard_normal((T, k)).astype(np.float32))
+                out = m.moe_route_grouped_bwd(t.cuda(), idx, prob, dp.cuda(), score=score, renormalize=renorm, scale=2.5)
+                torch.cuda.synchronize()
+                ri, rp, _ = group_route.forward(t[rows], k, b, **kw)
+                log(f"{score} bias {b is not None} renorm {renorm}")
+                np.testing.assert_array_equal(idx.cpu().numpy()[rows], ri)
+                _close(prob.cpu().double().numpy()[rows], rp, 80 * U * rp + TINY * 2.5)
+                assert torch.equal(counts.long(), torch.bincount(idx.reshape(-1).long(), minlength=E))
+                if score == "sigmoid":
+                    none = torch.from_numpy((low >= 1) & (low <= 3)).cuda()
+                    assert not prob[none].any() and not out[none].any()
