@@ -435,10 +435,11 @@ moe_status moe_grad_sumsq(const void* const* grads, const int64_t* numel, const 
  * sumsq       [1] fp64, device (moe_grad_sumsq's, or the sum of several), or
  *             NULL: that of grads, computed here in moe_grad_sumsq_workspace
  *             bytes of workspace (else unused).
- * max_norm    at least 0 (infinity: never scaled).
+ * max_norm    at least 0 (infinity: never scaled, also with an infinite sumsq).
  * norm        [1] fp32 out, device.
- * The product is fp32, rounded once.  An infinite sumsq gives c = 0 (and NaN
- * at infinite gradients), a NaN one NaN everywhere: test norm.
+ * The product is fp32, rounded once.  An infinite sumsq gives c = 0 under a
+ * finite max_norm (and NaN at infinite gradients), a NaN one NaN everywhere,
+ * whatever max_norm is: test norm.
  * ------------------------------------------------------------------------ */
 moe_status moe_grad_clip(const void* const* grads, const int64_t* numel, const int32_t* dtypes, int n,
                          void* const* out, const int32_t* out_dtypes, const double* sumsq, float max_norm,

@@ -788,8 +788,9 @@ def moe_grad_sumsq(grads) -> torch.Tensor:
 def moe_grad_clip(grads, max_norm: float, sumsq: Optional[torch.Tensor] = None, out=None) -> torch.Tensor:
     """Scales the gradients (a GradTable, or a list of tensors) by min(1, max_norm / (norm + 1e-6)), norm =
     sqrt(sumsq), in place or into `out` (a list of tensors with as many values, bf16 or f32; a GradTable has its own).
-    sumsq: float64 [1] (None: that of these gradients).  Returns norm, float32 [1], on the GPU; one that is not
-    finite leaves gradients that are not."""
+    sumsq: float64 [1] (None: that of these gradients).  Returns norm, float32 [1], on the GPU.  Test it: a NaN one makes
+    every value NaN; an infinite one makes finite values 0 and infinite ones NaN under a finite max_norm, and an
+    infinite max_norm leaves them as they are."""
     lib = load()
     if isinstance(grads, GradTable):
         if out is not None:

@@ -155,7 +155,8 @@ __global__ __launch_bounds__(kThreads) void grad_clip_kernel(const Table<kTensor
   const double total = sqrt(parts == 1 ? *sumsq : sum_parts(sumsq, parts));
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)total;
   const double ratio = (double)max_norm / (total + 1e-6);
-  const float by = ratio >= 1.0 || max_norm == __builtin_huge_valf() ? 1.0f : (float)ratio;   // (a NaN stays)
+  // (a NaN total stays one, also without a limit)
+  const float by = ratio >= 1.0 || (max_norm == __builtin_huge_valf() && total == total) ? 1.0f : (float)ratio;
   const Finder<kTensors, kOut> finder(tab);
   const int chunks = tab.first[tab.tensors];
   for (int c = blockIdx.x; c < chunks; c += gridDim.x) {

@@ -201,3 +201,27 @@ def test_refusals_on_the_gpu():
         m.moe_grad_clip([a], -1.0)
     with pytest.raises(m.MoeError):
         m.moe_grad_clip([a], float("nan"))
+
+
+@gpu
+def test_a_norm_that_is_nan_shows_without_a_limit():
+    """max_norm infinite: nothing is scaled, but a NaN norm makes every value NaN, as with any other limit."""
+    m = need_gpu()
+    nan, inf = float("nan"), float("inf")
+    for dtype in (F, B):
+        g = [torch.ones(9000, device="cuda", dtype=dtype), torch.ones(3, device="cuda")]
+        g[1][1] = nan
+        to = [torch.zeros(9000, device="cuda"), torch.zeros(3, device="cuda", dtype=B)]
+        n = m.moe_grad_clip(g, inf, out=to)
+        assert torch.isnan(n).all() and all(torch.isnan(t).all() for t in to)
+        n = m.moe_grad_clip(g, inf)
+        assert torch.isnan(n).all() and all(torch.isnan(t).all() for t in g)
+    for limit in (inf, 1.0):
+        g = [torch.ones(500, device="cuda")]
+        n = m.moe_grad_clip(g, limit, sumsq=torch.full((1,), nan, device="cuda", dtype=torch.float64))
+        assert torch.isnan(n).all() and torch.isnan(g[0]).all()
+    g = [torch.ones(500, device="cuda")]
+    n = m.moe_grad_clip(g, inf, sumsq=torch.full((1,), inf, device="cuda", dtype=torch.float64))
+    assert torch.isinf(n).all() and (g[0] == 1).all()
+    n = m.moe_grad_clip(g, 1.0, sumsq=torch.full((1,), inf, device="cuda", dtype=torch.float64))
+    assert torch.isinf(n).all() and not g[0].any()
