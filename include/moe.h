@@ -430,8 +430,9 @@ moe_status moe_grad_sumsq(const void* const* grads, const int64_t* numel, const 
  * grads, numel, dtypes, n: as moe_grad_sumsq.
  * out         HOST array of n device pointers that receive the results, in
  *             out_dtypes; out[i] may be grads[i] (in place, of one type; then
- *             nothing is written where c is 1).  Other overlaps between out and
- *             any tensor of the call are refused (MOE_ERR_INVALID_ARG).
+ *             nothing is written where c is 1).  Other overlaps between what is
+ *             written (out, norm, the workspace) and any tensor of the call are
+ *             refused (MOE_ERR_INVALID_ARG).
  * sumsq       [1] fp64, device (moe_grad_sumsq's, or the sum of several), or
  *             NULL: that of grads, computed here in moe_grad_sumsq_workspace
  *             bytes of workspace (else unused).

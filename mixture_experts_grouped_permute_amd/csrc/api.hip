@@ -791,26 +791,36 @@ constexpr int64_t kMostGrad = (int64_t)1 << 35;   // (a launch's chunks stay wit
 inline bool in_47_bits(const void* p) { return reinterpret_cast<uint64_t>(p) >> 47 == 0; }   // (the tables' addresses)
 
 // Whether no output of a clipping overlaps another tensor that the call reads or writes (its own gradient, as the same
-// values in the same type, apart): workgroups take them in no order.
+// values in the same type, apart), the `more` ones among them: workgroups take them in no order.
 struct Span {
   uintptr_t lo, hi;
   bool written;
 };
+constexpr int kMoreSpans = 3;
+Span span(const void* p, size_t bytes, bool written) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return {a, a + bytes, written};
+}
+inline bool clash(const Span& a, const Span& b) { return (a.written || b.written) && a.lo < b.hi && b.lo < a.hi; }
 moe_status check_apart(const void* const* grads, const int64_t* numel, const int32_t* dtypes, int n, void* const* out,
-                       const int32_t* out_dtypes) {
+                       const int32_t* out_dtypes, const Span (&more)[kMoreSpans]) {
   Span* v = new (std::nothrow) Span[2 * (size_t)n];
   if (!v) return MOE_ERR_WORKSPACE;
   size_t m = 0;
   for (int i = 0; i < n; ++i) {
     if (numel[i] == 0) continue;
-    const uintptr_t o = reinterpret_cast<uintptr_t>(out[i]), g = reinterpret_cast<uintptr_t>(grads[i]);
-    v[m++] = {o, o + (uintptr_t)numel[i] * io_size(out_dtypes[i]), true};
-    if (g != o || dtypes[i] != out_dtypes[i]) v[m++] = {g, g + (uintptr_t)numel[i] * io_size(dtypes[i]), false};
+    v[m++] = span(out[i], (size_t)numel[i] * io_size(out_dtypes[i]), true);
+    if (grads[i] != out[i] || dtypes[i] != out_dtypes[i]) v[m++] = span(grads[i], (size_t)numel[i] * io_size(dtypes[i]), false);
+  }
+  bool apart = true;
+  // (each with all: in the list they would leave it unsorted)
+  for (int k = 0; k < kMoreSpans; ++k) {
+    for (size_t i = 0; i < m; ++i) apart &= !clash(more[k], v[i]);
+    for (int j = 0; j < k; ++j) apart &= !clash(more[k], more[j]);
   }
   const auto before = [](const Span& a, const Span& b) { return a.lo < b.lo; };
   if (!std::is_sorted(v, v + m, before)) std::sort(v, v + m, before);
   uintptr_t any = 0, written = 0;                        // the furthest ends so far
-  bool apart = true;
   for (size_t i = 0; i < m && apart; ++i) {
     apart = v[i].lo >= (v[i].written ? any : written);
     any = std::max(any, v[i].hi);
@@ -970,12 +980,15 @@ moe_status moe_grad_clip(const void* const* grads, const int64_t* numel, const i
     MOE_CHECK(io_ok(dtypes[i]) && io_ok(out_dtypes[i]), MOE_ERR_INVALID_ARG);
     MOE_CHECK(numel[i] <= kMostGrad && in_47_bits(grads[i]) && in_47_bits(out[i]), MOE_ERR_UNSUPPORTED);
   }
-  const moe_status s = check_apart(grads, numel, dtypes, n, out, out_dtypes);
-  if (s != MOE_OK) return s;
+  const size_t need = sumsq ? 0 : moe_grad_sumsq_workspace(numel, n);
   if (!sumsq) {
-    MOE_CHECK(workspace && workspace_bytes >= moe_grad_sumsq_workspace(numel, n), MOE_ERR_WORKSPACE);
+    MOE_CHECK(workspace && workspace_bytes >= need, MOE_ERR_WORKSPACE);
     MOE_CHECK(aligned16(workspace), MOE_ERR_UNSUPPORTED);
   }
+  const Span more[kMoreSpans] = {span(norm, sizeof(float), true), span(sumsq, sumsq ? sizeof(double) : 0, false),
+                                 span(sumsq ? nullptr : workspace, need, true)};
+  const moe_status s = check_apart(grads, numel, dtypes, n, out, out_dtypes, more);
+  if (s != MOE_OK) return s;
   const GradList l{grads, numel, dtypes, out, out_dtypes, n};
   HIP_TRY(launch_grad_clip(l, sumsq, reinterpret_cast<double*>(workspace), max_norm, norm, reinterpret_cast<hipStream_t>(stream)));
   return MOE_OK;

@@ -190,3 +190,25 @@ def test_binding_refusals():
         m.GradTable([])
     with pytest.raises(ValueError):
         m.GradTable([x], [x, x])
+
+
+def test_grad_clip_refuses_outputs_over_its_norm_sum_and_workspace(lib):
+    """What the workgroups read their factor from, or leave the norm in, shares no memory with what others write."""
+    inv, _, wsp = _codes()
+    MB = 1 << 20
+    need = lib.moe_grad_sumsq_workspace((ctypes.c_int64 * 2)(1000, 70000), 2)
+    def call(sumsq, norm, ws, outs=(16 * MB, 20 * MB)):
+        return _clip(lib, [MB, 4 * MB], [1000, 70000], [0, 1], outs, [0, 0], sumsq=sumsq, norm=norm, ws=ws, wbytes=need)
+    for sumsq, norm, ws, outs in (
+            (16 * MB + 8, 8 * MB, None, (16 * MB, 20 * MB)),                       # the sum in an output
+            (20 * MB + 70000 * 4 - 8, 8 * MB, None, (16 * MB, 20 * MB)),
+            (9 * MB, 16 * MB + 3996, None, (16 * MB, 20 * MB)),                    # the norm in an output, in a gradient
+            (9 * MB, 4 * MB + 2 * 69998, None, (16 * MB, 20 * MB)),
+            (9 * MB, 9 * MB + 4, None, (16 * MB, 20 * MB)),                        # the norm over the sum
+            (MB + 400, 8 * MB, None, (MB, 20 * MB)),                               # in place
+            (9 * MB, MB, None, (MB, 20 * MB)),
+            (None, 8 * MB, 16 * MB + 3984, (16 * MB, 20 * MB)),                    # the workspace: in an output, in a gradient,
+            (None, 8 * MB, MB - need + 16, (16 * MB, 20 * MB)),                    # over the norm
+            (None, 8 * MB + need - 16, 8 * MB, (16 * MB, 20 * MB))):
+        assert call(sumsq, norm, ws, outs) == inv, (sumsq, norm, ws, outs)
+    assert call(None, 16 * MB, None) == wsp

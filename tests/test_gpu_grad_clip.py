@@ -225,3 +225,31 @@ def test_a_norm_that_is_nan_shows_without_a_limit():
     assert torch.isinf(n).all() and (g[0] == 1).all()
     n = m.moe_grad_clip(g, 1.0, sumsq=torch.full((1,), inf, device="cuda", dtype=torch.float64))
     assert torch.isinf(n).all() and not g[0].any()
+
+
+@gpu
+def test_tensors_that_end_where_the_norm_and_the_sum_begin():
+    """Beside one another in one piece of memory; a workspace that is not used may be anywhere.  Over one another: refused."""
+    m = need_gpu()
+    lib = m.load()
+    from mixture_experts_grouped_permute_amd import _lib as L
+    flat = torch.zeros(64, dtype=torch.float64, device="cuda")
+    f32 = flat.view(F)
+    g, sumsq, norm_at = f32[:20], flat[10:11], f32[22:23]
+    g.fill_(2.0)
+    table = m.GradTable([g])
+    need = lib.moe_grad_sumsq_workspace(table._at[1], 1)
+    ptrs, numel, kinds, outs, okinds = table._at
+    def call(sum_at, norm_to, ws, wbytes):
+        st = lib.moe_grad_clip(ptrs, numel, kinds, 1, outs, okinds, sum_at, 1.0, norm_to, ws, wbytes, L._stream(flat.device))
+        torch.cuda.synchronize()
+        return st
+    sumsq.fill_(4.0)
+    assert call(sumsq.data_ptr(), norm_at.data_ptr(), f32[4:].data_ptr(), need) == 0
+    assert float(norm_at) == 2.0 and (g - 1.0).abs().max() <= 1e-6 and float(sumsq) == 4.0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    assert call(None, norm_at.data_ptr(), ws.data_ptr(), need) == 0
+    assert abs(float(norm_at) - 20 ** 0.5) <= 1e-5
+    for bad in ((sumsq.data_ptr(), sumsq.data_ptr() + 4, None, 0), (sumsq.data_ptr(), f32[19:].data_ptr(), None, 0),
+                (g.data_ptr(), norm_at.data_ptr(), None, 0), (None, ws.data_ptr() + 8, ws.data_ptr(), need)):
+        assert call(*bad) == L.MOE_ERR_INVALID_ARG
