@@ -411,3 +411,44 @@ def test_rows_of_very_low_logits(E, k, G, kg, best, T, dtype):
                 if score == "sigmoid":
                     none = torch.from_numpy((low >= 1) & (low <= 3)).cuda()
                     assert not prob[none].any() and not out[none].any()
+
+
+@gpu
+@pytest.mark.parametrize("k", [2, 3, 8, 13])
+@pytest.mark.parametrize("E,G,kg,best", [
+    (16, 1, 1, 1), (32, 1, 1, 1), (60, 1, 1, 1), (65, 1, 1, 1), (128, 1, 1, 1), (129, 1, 1, 1), (256, 1, 1, 1),   # no groups
+    (16, 16, 14, 1), (32, 16, 9, 2), (60, 15, 8, 2), (80, 16, 9, 1), (128, 4, 3, 2), (240, 8, 5, 2),             # over half of them
+    (256, 2, 2, 2), (255, 3, 2, 2), (255, 5, 3, 1), (252, 9, 5, 2),
+    (64, 4, 2, 2), (128, 16, 8, 1), (256, 16, 8, 2), (255, 3, 1, 2)])                                             # half or fewer
+def test_many_tokens_of_each_width(E, G, kg, best, k):
+    """Each count of experts a lane (1 to 32), with and without the halving of groups, by each length of list, in one launch
+    and at more tokens than one does to the end; rows that hold ties, NaN and infinities between ordinary ones.  And the
+    gradient at those widths."""
+    m = need_gpu()
+    for T, dtype in ((97, F), (97, B), (4099, F), (4099, B)):
+        rows = np.arange(T) if T < 1000 else np.r_[0:150, 2000:2050, T - 60:T]
+        mask = torch.from_numpy(np.random.default_rng(E).random(T) < 0.7)
+        dp = torch.from_numpy(np.random.default_rng(k).standard_normal((T, k)).astype(np.float32))
+        lg = _logits(T, E, "normal", dtype)
+        lg[1::5] = torch.round(lg[1::5].float()).to(dtype)
+        lg[2::7, ::3] = -float("inf")
+        lg[3::11] = -float("inf")
+        lg[4::13, E - 1] = float("nan")
+        lg[5::17, E // 2] = float("inf")
+        for score, b, renorm in (("sigmoid", None, True), ("sigmoid", _bias(E, "normal"), True),
+                                 ("softmax", None, False), ("softmax", _bias(E, "normal") * 0.1, True)):
+            kw = dict(score=score, groups=G, topk_groups=kg, group_best=best, renormalize=renorm)
+            idx, prob, counts = m.moe_route_grouped(lg.cuda(), k, bias=_gpu(b), count=True, token_mask=mask.cuda(), **kw)
+            i2, p2, _ = m.moe_route_grouped(lg.cuda(), k, bias=_gpu(b), **kw)
+            out = m.moe_route_grouped_bwd(lg.cuda(), idx, prob, dp.cuda(), score=score, renormalize=renorm)
+            torch.cuda.synchronize()
+            assert torch.equal(idx, i2) and torch.equal(prob.nan_to_num(7.0), p2.nan_to_num(7.0))
+            log(f"{T} x {E} {score} bias {b is not None}")
+            ri, rp, _ = group_route.forward(lg[rows], k, b, **kw)
+            np.testing.assert_array_equal(idx.cpu().numpy()[rows], ri)
+            _close(prob.cpu().double().numpy()[rows], rp, 80 * U * rp + TINY)
+            live = idx.cpu()[mask].reshape(-1).long()
+            assert torch.equal(counts.cpu().long(), torch.bincount(live, minlength=E))
+            want, mag = group_route.backward(lg[rows], ri, prob.cpu().numpy()[rows], dp.numpy()[rows], score, renorm)
+            _close(out.cpu().double().numpy()[rows], want,
+                   96 * U * mag + np.abs(want) * float(torch.finfo(dtype).eps) / 2 + TINY * 16)
