@@ -253,3 +253,40 @@ def test_tensors_that_end_where_the_norm_and_the_sum_begin():
     for bad in ((sumsq.data_ptr(), sumsq.data_ptr() + 4, None, 0), (sumsq.data_ptr(), f32[19:].data_ptr(), None, 0),
                 (g.data_ptr(), norm_at.data_ptr(), None, 0), (None, ws.data_ptr() + 8, ws.data_ptr(), need)):
         assert call(*bad) == L.MOE_ERR_INVALID_ARG
+
+
+@gpu
+@pytest.mark.parametrize("kinds,out", [("f32", "in place"), ("f32", "bf16"), ("f32", "f32"), ("bf16", "in place"),
+                                       ("bf16", "f32"), ("both", "in place"), ("both", "bf16")])
+def test_more_than_the_caches_hold(kinds, out):
+    """Over 256 MB of gradients go past the caches: views at odd addresses, with tails and single values among them.  The
+    64-bit sum over 7e7 values (1e-10 of itself) and the products on the GPU, by elementary operations."""
+    m = need_gpu()
+    wide = {"f32": 33_000_000, "bf16": 66_000_000, "both": 44_000_000}[kinds]
+    sizes = [wide + 5, 1, 8191, wide + 8192, 8193, 7]
+    dt = [F if kinds == "f32" or (kinds == "both" and i % 2 == 0) else B for i in range(6)]
+    od = dt if out == "in place" else [F if out == "f32" else B] * 6
+    gen = torch.Generator(device="cuda").manual_seed(len(kinds) + len(out))
+    g, to = [], []
+    for i, n in enumerate(sizes):
+        flat = (torch.randn(n + 8, generator=gen, device="cuda") * 0.01).to(dt[i])
+        g.append(flat[1 + i:1 + i + n])
+        to.append(torch.full((n + 8,), 9.0, dtype=od[i], device="cuda")[3:3 + n] if out != "in place" else None)
+    assert sum(t.numel() * t.element_size() for t in g) > 256e6
+    before = [t.clone() for t in g]
+    full = float(torch.stack([(t.double() * t.double()).sum() for t in g]).sum()) ** 0.5
+    assert abs(float(m.moe_grad_sumsq(g)) - full ** 2) <= 1e-10 * full ** 2
+    for limit in (2 * full, 0.3 * full):
+        n = m.moe_grad_clip(g, limit, out=None if out == "in place" else to)
+        torch.cuda.synchronize()
+        assert abs(float(n) - full) <= 2 * U * full
+        c = min(1.0, limit / (full + 1e-6))
+        for o, d, b, t in zip(g if out == "in place" else to, od, before, g):
+            want = b.double() * c
+            tol = (3 * U + (float(torch.finfo(d).eps) / 2 if d == B else 0)) * want.abs() + 2.0 ** -133
+            assert bool(((o.double() - want).abs() <= tol).all())
+            assert out == "in place" or torch.equal(t, b)
+        if out != "in place":
+            for o, d in zip(to, od):                                  # (what lies around the views stays)
+                whole = torch.empty(0, dtype=d, device="cuda").set_(o.untyped_storage())
+                assert bool((whole[:3] == 9).all()) and bool((whole[3 + o.numel():] == 9).all())

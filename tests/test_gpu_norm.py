@@ -339,3 +339,83 @@ def test_gradient_without_eps(T, H, dtype):
     rx, rw, mag, wmag = norm.backward(dy, s, w, 0.0)
     assert (np.abs(_np(dx) - rx) <= 240 * U * mag + _half(dtype) * np.abs(rx) + 1e-38).all()
     assert (np.abs(_np(dw) - rw) <= (T + 100) * U * wmag + 1e-38).all()
+
+
+def _rows_on_gpu(T, H, dtype, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn((T, H), generator=g, device="cuda")
+    return x.mul_(torch.exp(0.7 * torch.randn(H, generator=g, device="cuda"))).to(dtype)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,wdtype", [(B, B), (B, F), (F, F)], ids=["bf16", "bf16-w32", "f32"])
+@pytest.mark.parametrize("H", [104, 107, 248, 250, 509, 512, 1003, 1024, 2047, 2048, 4093, 4096, 8184, 8190, 16383, 16384, 30001,
+                               32768])
+def test_more_than_the_caches_hold(H, dtype, wdtype):
+    """Results stored past the caches (402 MB forward, 604 backward), at each count of lanes a row, whole pieces and pieces
+    that are moved back; dx apart from ds and over it.  The formulas in 64 bits on the GPU, by elementary operations.
+    dweight: at least 256 workgroups share the rows, so a sum has at most T / 256 + 1 terms in turn, and 16 in LDS."""
+    m = need_gpu()
+    from mixture_experts_grouped_permute_amd import _lib as L
+    lib = m.load()
+    size = 2 if dtype == B else 4
+    T = (576 << 20) // (4 * size * H) + 5
+    log(f"norm {T} x {H} {dtype}")
+    x, r, dy = (_rows_on_gpu(T, H, dtype, i) for i in range(3))
+    w = _w(H, wdtype).cuda()
+    kw = dict(residual=r, codes=H % 128 == 0)
+    got = m.moe_add_rmsnorm(x, w, **kw)
+    again = m.moe_add_rmsnorm(x, w, **kw)
+    y, s, q, scales = got
+    for a, b in zip(got, again):
+        assert (a is None and b is None) or torch.equal(a, b)
+    if q is not None and dtype == F:
+        cq, cs = m.fp8_block_quantize(y)
+        assert torch.equal(cq, q) and torch.equal(cs, scales)
+    dx, dw = m.moe_add_rmsnorm_bwd(dy, s, w, ds=r)
+    over, dw2 = r.clone(), torch.empty(H, device="cuda")
+    ws = torch.empty(lib.moe_add_rmsnorm_bwd_workspace(T, H), dtype=torch.uint8, device="cuda")
+    st = lib.moe_add_rmsnorm_bwd(dy.data_ptr(), s.data_ptr(), over.data_ptr(), L._io(dy), w.data_ptr(), L._io(w), T, H, 1e-6,
+                                 over.data_ptr(), dw2.data_ptr(), ws.data_ptr(), ws.numel(), L._stream(dy.device))
+    torch.cuda.synchronize()
+    assert st == 0 and torch.equal(over, dx) and torch.equal(dw2, dw)
+    w64, half = w.double(), _half(dtype)
+    want_dw, mag_dw = torch.zeros(H, device="cuda", dtype=torch.float64), torch.zeros(H, device="cuda", dtype=torch.float64)
+    step = max(1, (1 << 23) // H)
+    for t in range(0, T, step):
+        at = slice(t, min(t + step, T))
+        s64, d64 = s[at].double(), dy[at].double()
+        assert torch.equal(s[at], (x[at].float() + r[at].float()).to(dtype))
+        rstd = 1 / torch.sqrt((s64 * s64).mean(1, keepdim=True) + 1e-6)
+        xh = s64 * rstd
+        want = xh * w64
+        assert bool(((y[at].double() - want).abs() <= (80 * U + half) * want.abs() + 1e-38).all())
+        gw = d64 * w64
+        want = rstd * (gw - xh * (gw * xh).mean(1, keepdim=True)) + r[at].double()
+        mag = rstd * (gw.abs() + xh.abs() * (gw * xh).abs().mean(1, keepdim=True)) + r[at].double().abs()
+        assert bool(((dx[at].double() - want).abs() <= 240 * U * mag + half * want.abs() + 1e-38).all())
+        want_dw += (d64 * xh).sum(0)
+        mag_dw += (d64 * xh).abs().sum(0)
+    assert bool(((dw.double() - want_dw).abs() <= (T / 256 + 120) * U * mag_dw).all())
+
+
+@gpu
+def test_weight_gradient_of_more_rows_than_a_launch_takes():
+    """Terms of one sign, 16385 of them in turn by each of 512 x 16 places, 16 in LDS; each within 80 u.  (The oracle's sum
+    over the 2^27 rows is in 64 bits.)"""
+    m = need_gpu()
+    T, H = (1 << 27) + 3, 8
+    x, w = torch.empty((T, H), dtype=B, device="cuda"), _w(H, B).cuda()
+    want = torch.zeros(H, device="cuda", dtype=torch.float64)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    step = 1 << 23
+    for t in range(0, T, step):
+        part = x[t:t + step]
+        part.copy_(torch.randn(part.shape, generator=g, device="cuda"))
+        p64 = part.double()
+        want += (p64 * p64 / torch.sqrt((p64 * p64).mean(1, keepdim=True) + 1e-6)).sum(0)
+    _, dw = m.moe_add_rmsnorm_bwd(x, x, w)
+    torch.cuda.synchronize()
+    err = (dw.double() - want).abs() / want
+    log(f"dweight off by {float(err.max()) / U:.0f} u")
+    assert float(err.max()) <= (16385 + 16 + 100) * U
