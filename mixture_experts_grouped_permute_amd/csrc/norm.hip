@@ -437,6 +437,8 @@ Shape shape_few(int64_t H) {
   return {1024, 4};
 }
 constexpr int64_t kFewRows = 512;
+// Whether shape_of gives it as well: 512 rows of the others (of up to 16384 columns, 134 MB) stay in the caches.
+constexpr bool for_many(int L, int N) { return !(N == 1 && L >= 256) && !(N == 2 && L == 1024); }
 constexpr int64_t kOnceBytes = (int64_t)384 << 20, kOnceBytesBwd = (int64_t)576 << 20;
 
 template <class F>
@@ -474,10 +476,13 @@ hipError_t launch_fwd(const NormFwd& p, hipStream_t st) {
     for (int64_t t0 = 0; t0 < p.T; t0 += kMost * rows) {
       const int64_t need = (p.T - t0 + rows - 1) / rows;
       const unsigned grid = (unsigned)(need < kMost ? need : kMost);
-      if (aligned && once) add_rmsnorm_kernel<kF32, kW32, kL, kN, true, true><<<grid, kT, 0, st>>>(p, t0);
-      else if (aligned) add_rmsnorm_kernel<kF32, kW32, kL, kN, true, false><<<grid, kT, 0, st>>>(p, t0);
-      else if (once) add_rmsnorm_kernel<kF32, kW32, kL, kN, false, true><<<grid, kT, 0, st>>>(p, t0);
-      else add_rmsnorm_kernel<kF32, kW32, kL, kN, false, false><<<grid, kT, 0, st>>>(p, t0);
+      const auto go = [&](auto past) {
+        constexpr bool kOnce = decltype(past)::value;
+        if (aligned) add_rmsnorm_kernel<kF32, kW32, kL, kN, true, kOnce><<<grid, kT, 0, st>>>(p, t0);
+        else add_rmsnorm_kernel<kF32, kW32, kL, kN, false, kOnce><<<grid, kT, 0, st>>>(p, t0);
+      };
+      if (once) go(std::bool_constant<for_many(kL, kN)>{});
+      else go(std::false_type{});
     }
     return hipGetLastError();
   });
@@ -515,10 +520,13 @@ hipError_t launch_bwd(NormBwd p, hipStream_t st) {
     const bool aligned = p.H % 8 == 0 && at16(p.dy) && at16(p.s) && at16(p.dsum) && at16(p.weight) && at16(p.dx);
     e = with_shape(b.s, [&](auto l, auto n) {
       constexpr int kL = decltype(l)::value, kN = decltype(n)::value;
-      if (aligned && once) rmsnorm_bwd_kernel<kF32, kW32, kL, kN, true, true><<<b.blocks, threads_of(kL), 0, st>>>(p);
-      else if (aligned) rmsnorm_bwd_kernel<kF32, kW32, kL, kN, true, false><<<b.blocks, threads_of(kL), 0, st>>>(p);
-      else if (once) rmsnorm_bwd_kernel<kF32, kW32, kL, kN, false, true><<<b.blocks, threads_of(kL), 0, st>>>(p);
-      else rmsnorm_bwd_kernel<kF32, kW32, kL, kN, false, false><<<b.blocks, threads_of(kL), 0, st>>>(p);
+      const auto go = [&](auto past) {
+        constexpr bool kOnce = decltype(past)::value;
+        if (aligned) rmsnorm_bwd_kernel<kF32, kW32, kL, kN, true, kOnce><<<b.blocks, threads_of(kL), 0, st>>>(p);
+        else rmsnorm_bwd_kernel<kF32, kW32, kL, kN, false, kOnce><<<b.blocks, threads_of(kL), 0, st>>>(p);
+      };
+      if (once) go(std::bool_constant<for_many(kL, kN)>{});
+      else go(std::false_type{});
       return hipGetLastError();
     });
   }
