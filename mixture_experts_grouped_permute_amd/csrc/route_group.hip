@@ -15,7 +15,7 @@
 // Forward: 16 lanes share a token; a group's experts lie with 16 / (power of two >= G) of them.  Scores are fp32
 // first: their error is known, and where two numbers whose order counts are nearer than that -- neighbours in the list,
 // the last one in and the first one out, the last group in and the first one out -- the token is done again in 64 bits
-// (one of 460 with fp32 logits, a bias and 8 groups of 256 experts).
+// (one of 460 with sigmoids of fp32 logits, a bias and 8 groups of 256 experts; of softmax scores with a bias far more).
 #include "common.h"
 #include "kernels.h"
 #include "eight.h"
@@ -339,11 +339,11 @@ __device__ __forceinline__ uint32_t whole(float x) {
 // kInline: the wave does such tokens itself; else it marks them with id -1 for route_again_kernel, whose 64-bit code would
 // take half of this one's waves for its registers (140 us in one kernel, 98 and 19 in two).
 // kHalf: half of the groups stay at most.  Those next in rank give their lanes to them: each takes over half the experts of
-// the one kg ahead, and the selection has half as many a lane.  131072 x 256 of 8 groups 83 us with it, 88 without (bf16 74
+// the one kg ahead, and the selection has half as many a lane.  131072 x 256 of 8 groups 83 us with it, 88 without (bf16 75
 // and 84), 50021 x 160 26 and 29, 131072 x 64 of 4 groups 43 and 45.
-// Measured: 131072 x 256 f32, bias, 4 of 8 groups, k = 8, with counts: 83 us -- 71 here, VALU issue 68 % busy with 870
-// instructions for 4 tokens, 180 of them the scores; 12.5 for the 285 tokens done again, 5 for the counts' total -- of 28
-// that its bytes take.  Without groups and bias 53.
+// Measured: 131072 x 256 f32, bias, 4 of 8 groups, k = 8, with counts: 82 us of 28 that its bytes take; VALU issue is 68 %
+// busy with 870 instructions for 4 tokens, 180 of them the scores.  Profiled, where the three kernels overlap less, 69
+// here, 12.8 for the 285 tokens done again, 4.9 for the counts' total.  Without groups, bias and counts 52.
 template <int kN, int kK, bool kInline, bool kHalf>
 __global__ __launch_bounds__(64 * kWaves, kInline ? 1 : kN <= 16 ? 4 : 2) void route_group_kernel(const GroupRoute p) {
   using K = Key<false>;
@@ -387,6 +387,8 @@ __global__ __launch_bounds__(64 * kWaves, kInline ? 1 : kN <= 16 ? 4 : 2) void r
   // Errors, u = 2^-24: of a sigmoid 4 u (exponential and reciprocal an ulp each, its argument's rounding), of a softmax 24 u;
   // with the bias over the lowest, two roundings of up to `range` more.  So two scores differ by what they seem to within
   // 2 (4 + 1 + 2 range) u, two sums of two within 2 (10 + 6 range) u: at least as much is allowed for.
+  // (For softmax scores that is the error of one near 1, and 256 experts whose logits are close have scores of 1 / 256 that
+  // differ by less: 131072 x 256 with a bias takes 104 us at logits of deviation 1.5, 359 at 0.1.)
   const float t0_err = p.sigmoid ? 0x1p-20f : 0x1p-17f;
   const float near = t0_err + 0x1p-21f * range;
   const bool hopeless = p.bias && !(range < 0x1p60f);    // (64-bit roundings of what is below: 2^-33 at most, within the errors)
