@@ -612,7 +612,8 @@ def moe_route_grouped(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor]
     consecutive experts each token keeps the topk_groups (None: all) with the largest sums of their group_best (1 or
     2; None: 2, or 1 in groups of one) best s + bias, and of their experts the k with the largest s + bias; equal
     ones: lower id.  bias: optional float32 [E], which counts in the selection alone.  The weights are s of the
-    selected, with renormalize divided by their sum, times scale.
+    selected, with renormalize divided by their sum (0 where that is 0, as 64-bit scores are: sigmoids below -709.78),
+    times scale.
     count: also return the slots of each expert; token_mask: optional bool or uint8 [T], tokens whose slots are
     not counted where it is 0.
     Returns (topk_idx int32 [T, k], topk_prob float32 [T, k], counts int32 [E] or None)."""

@@ -339,7 +339,7 @@ __device__ __forceinline__ uint32_t whole(float x) {
 // kInline: the wave does such tokens itself; else it marks them with id -1 for route_again_kernel, whose 64-bit code would
 // take half of this one's waves for its registers (140 us in one kernel, 98 and 19 in two).
 // kHalf: half of the groups stay at most.  Those next in rank give their lanes to them: each takes over half the experts of
-// the one kg ahead, and the selection has half as many a lane.  131072 x 256 of 8 groups 83 us with it, 88 without (bf16 75
+// the one kg ahead, and the selection has half as many a lane.  131072 x 256 of 8 groups 83 us with it, 88 without (bf16 74
 // and 84), 50021 x 160 26 and 29, 131072 x 64 of 4 groups 43 and 45.
 // Measured: 131072 x 256 f32, bias, 4 of 8 groups, k = 8, with counts: 82 us of 28 that its bytes take; VALU issue is 68 %
 // busy with 870 instructions for 4 tokens, 180 of them the scores.  Profiled, where the three kernels overlap less, 69
